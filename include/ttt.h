@@ -314,6 +314,162 @@ ttt_status ttt_stream_step_static(const ttt_config* cfg,
                                   const void* Q, int64_t m, void* O, ttt_stream_t stream);
 
 /*
+ * Gated delta rule: the causal sibling of the linear fast weights (mlp =
+ * TTT_MLP_LINEAR).  The state S of a head has the linear mode's layout
+ * (float [d][d], row = output); token after token it fades and is corrected
+ * towards the token's value at the token's key, then read:
+ *   S' = exp(log_decay_t) S,  u = beta_t (v_t - S' k_t),  S <- S' + u k_t^T,
+ *   o_t = scale * S q_t.
+ * (One gradient step of 1/2 |S' k - v|^2 with step beta; the keys and queries
+ * are taken as they are: normalise them before the call where that is wanted.)
+ *
+ * ttt_delta_config: `heads` state heads; `qk_heads` heads of Q and K, a
+ *   divisor of `heads` (state head h reads Q/K head h / (heads / qk_heads));
+ *   d = 64, 128 or 256; scale finite.
+ * ttt_delta_tokens: n tokens, packed.  Q, K: rows of qk_heads*d, V: rows of
+ *   heads*d values of the precision's token type, consecutive rows ldq, ldk,
+ *   ldv elements apart (at least the row; a multiple of 16 bytes), so they may
+ *   be columns of one projection's output.  log_decay (<= 0; -inf forgets
+ *   everything) and beta: float [n][heads], dense.  With `offsets` (device
+ *   int64 [seqs + 1], non-decreasing, within 0..n) sequence i is the tokens
+ *   offsets[i] .. offsets[i+1]-1; NULL: one sequence of all n tokens (seqs
+ *   must be 1).  Sequences may be empty.  Rows of O (and of the token
+ *   gradients) that belong to no sequence are left as they are.  Offsets that
+ *   decrease or leave 0..n are clamped and reported in the device error word
+ *   (TTT_DEVICE_ERR_OFFSETS); the outputs are then undefined.
+ *
+ * ttt_delta_chunk: all tokens of every sequence.  S_in: float
+ *   [seqs][heads][d][d] or NULL (zeros); S_out: the states after the last
+ *   tokens, or NULL; it may be S_in (in place).  An empty sequence hands its
+ *   state on.  O: [n][heads*d] dense, token type.
+ *   BF16_TC: chunks of 64 tokens on the tensor cores, the state and every sum
+ *   in fp32 (operands that are not bf16 by nature go in as a bf16 pair hi +
+ *   lo, so the state keeps 16 bits and more).  FP32_CHECK: token by token in
+ *   fp32 on CUDA cores.
+ * ttt_delta_step: one token for each of tok->n requests (tok->seqs = n,
+ *   tok->offsets = NULL) on a pool of `pool` states float
+ *   [pool][heads][d][d]: request i works on S[slots[i]] (slots: device int32
+ *   [n]; NULL: slot i, and pool >= n).  S_out receives the states of the
+ *   slots that were named and no others; it may be S (in place).  A slot that
+ *   appears several times takes its tokens in the order of i.  A slot outside
+ *   0..pool-1 (-1: padding) touches no state and its row of O is zero.
+ * ttt_delta_backward: gradients of sum(dO . O) + sum(dS_out . S_out) for the
+ *   tokens and S_in of ttt_delta_chunk.  dO: [n][heads*d] dense, token type;
+ *   dS_out: float [seqs][heads][d][d] or NULL (zeros).  Writes dQ, dK
+ *   ([n][qk_heads*d], summed over the heads that share them), dV
+ *   ([n][heads*d]), token type, dense; dlog_decay, dbeta: float [n][heads];
+ *   dS_in: float [seqs][heads][d][d] or NULL; it may be dS_out (in place).
+ *   Nothing is kept from the forward call: it is recomputed in the workspace.
+ *
+ * Outputs alias no input except where said.  Workspace bytes:
+ * ttt_delta_workspace_bytes(cfg, n, seqs, backward); 0 for an invalid config.
+ * Results are the same from run to run.
+ */
+typedef struct {
+  int32_t heads;
+  int32_t qk_heads;
+  int32_t d;
+  int32_t precision; /* TTT_PREC_* : type of Q, K, V, O and their gradients */
+  float scale;       /* factor of the read, e.g. 1/sqrt(d) */
+} ttt_delta_config;
+
+typedef struct {
+  const void* Q;
+  const void* K;
+  const void* V;
+  const float* log_decay;
+  const float* beta;
+  int64_t ldq, ldk, ldv; /* elements between rows */
+  int64_t n;
+  const int64_t* offsets; /* device, or NULL */
+  int64_t seqs;
+} ttt_delta_tokens;
+
+enum { TTT_DEVICE_ERR_OFFSETS = 8 };
+
+size_t ttt_delta_workspace_bytes(const ttt_delta_config* cfg, int64_t n, int64_t seqs,
+                                 int32_t backward);
+ttt_status ttt_delta_chunk(const ttt_delta_config* cfg, const ttt_delta_tokens* tok,
+                           const float* S_in, float* S_out, void* O, void* workspace,
+                           size_t workspace_bytes, ttt_stream_t stream);
+ttt_status ttt_delta_step(const ttt_delta_config* cfg, const ttt_delta_tokens* tok,
+                          const int32_t* slots, int64_t pool, const float* S, float* S_out,
+                          void* O, ttt_stream_t stream);
+ttt_status ttt_delta_backward(const ttt_delta_config* cfg, const ttt_delta_tokens* tok,
+                              const float* S_in, const void* dO, const float* dS_out, void* dQ,
+                              void* dK, void* dV, float* dlog_decay, float* dbeta, float* dS_in,
+                              void* workspace, size_t workspace_bytes, ttt_stream_t stream);
+
+/*
+ * Rotary positions over three axes, for the q and k of image and video tokens
+ * (time or frame, height, width).  Of the d values of a head the first
+ * rot[0] + rot[1] + rot[2] are rotated (the rest pass unchanged), as pairs:
+ * the first rot[0]/2 pairs by the token's position on axis 0, the next
+ * rot[1]/2 by axis 1, the next rot[2]/2 by axis 2.  Pair j (counted over all
+ * axes, R = the sum of rot) is
+ *   TTT_ROPE_HALF:  values j and j + R/2      TTT_ROPE_PAIRS: 2j and 2j + 1
+ * and turns by position * base^(-e), with
+ *   TTT_ROPE_FREQ_AXIS: e = i / (rot[a]/2), i counted within axis a
+ *   TTT_ROPE_FREQ_HEAD: e = j / (R/2), over the whole head
+ *   (x, y) -> (x cos - y sin, y cos + x sin); inverse != 0 turns back, which
+ * is also the gradient: it maps dQ_out, dK_out to dQ, dK.
+ * Angles are formed and reduced in fp64, the rotation is fp32, rounded once.
+ *  - d = 64, 128 or 256; rot[] even, >= 0, sum 2..d; base[] finite, > 0.  With
+ *    FREQ_HEAD every pair still uses its own axis' base.
+ *  - positions: float [n][3] (whole numbers are exact to 2^24); fractions and
+ *    negative positions are fine.  A position of infinity or NaN gives NaN.
+ *  - Q: rows of q_heads*d values ldq apart, Q_out likewise ldq_out; K, K_out
+ *    too, or k_heads = 0 with K = K_out = NULL.  Rows a multiple of 16 bytes
+ *    apart.  Q_out may be Q and K_out K (in place, same row distance).
+ */
+enum { TTT_ROPE_HALF = 0, TTT_ROPE_PAIRS = 1 };
+enum { TTT_ROPE_FREQ_AXIS = 0, TTT_ROPE_FREQ_HEAD = 1 };
+typedef struct {
+  int32_t d;
+  int32_t rot[3];
+  float base[3];
+  int32_t layout;    /* TTT_ROPE_HALF or TTT_ROPE_PAIRS */
+  int32_t freq;      /* TTT_ROPE_FREQ_* */
+  int32_t precision; /* TTT_PREC_*: bf16 or float values */
+} ttt_rope_config;
+ttt_status ttt_rope(const ttt_rope_config* cfg, const void* Q, int64_t ldq, int32_t q_heads,
+                    const void* K, int64_t ldk, int32_t k_heads, const float* positions,
+                    int64_t n, void* Q_out, int64_t ldq_out, void* K_out, int64_t ldk_out,
+                    int32_t inverse, ttt_stream_t stream);
+
+/*
+ * Layer norm (in front of the projections that make q, k, v and eta):
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1/sqrt(var + eps),
+ * over rows of `dim` values, var the mean square distance from the mean (taken
+ * in a second pass over the row, which stays on chip).  X: rows ldx elements
+ * apart; weight, bias: float [dim], each may be NULL (1 and 0); Y: [rows][dim]
+ * dense; stats: float [rows][2] (mean, rstd) or NULL.  X and Y of the
+ * precision's token type; Y may be X (then ldx = dim).
+ * ttt_layer_norm_backward: from X, dY (rows lddy apart), weight and the stats
+ *   of the forward call: dX ([rows][dim] dense, or NULL; it may be dY or X
+ *   when that is dense), dweight and dbias (float [dim], each may be NULL).
+ *   The sums over the rows are taken in fp32, in an order that depends on the
+ *   sizes only.  dX is NULL or not, at least one output is wanted.  Rows = 0
+ *   gives dweight = dbias = 0.  Workspace: ttt_norm_workspace_bytes(cfg, rows)
+ *   (needed for dweight or dbias).
+ *  - dim 1 .. 65536; eps >= 0, finite.  ldx, lddy >= dim, any value.
+ */
+typedef struct {
+  int64_t dim;
+  float eps;
+  int32_t precision; /* TTT_PREC_*: bf16 or float X, Y */
+} ttt_norm_config;
+size_t ttt_norm_workspace_bytes(const ttt_norm_config* cfg, int64_t rows);
+ttt_status ttt_layer_norm(const ttt_norm_config* cfg, const void* X, int64_t ldx, int64_t rows,
+                          const float* weight, const float* bias, void* Y, float* stats,
+                          ttt_stream_t stream);
+ttt_status ttt_layer_norm_backward(const ttt_norm_config* cfg, const void* X, int64_t ldx,
+                                   const void* dY, int64_t lddy, int64_t rows,
+                                   const float* weight, const float* stats, void* dX,
+                                   float* dweight, float* dbias, void* workspace,
+                                   size_t workspace_bytes, ttt_stream_t stream);
+
+/*
  * Tracing.  With tracing on, every kernel launch of the library is bracketed
  * by two CUDA events on the caller's stream (host-side state: an event pool
  * and per-kernel totals, guarded by a mutex).  ttt_trace_read synchronises

@@ -7,6 +7,10 @@ exposes the same entry points through a thin ctypes binding:
     ttt_update_workspace_bytes, ttt_shadow_bytes, ttt_check_device_error,
     ttt_trace_enable, ttt_trace_read
 
+and, around the layer (``_ops``): the gated delta rule (ttt_delta_chunk,
+ttt_delta_step, ttt_delta_backward), rotary positions over three axes
+(ttt_rope) and layer norm (ttt_layer_norm, ttt_layer_norm_backward).
+
 The binding (and torch) is imported on first use, so ``workloads`` can be
 imported on machines without CUDA.
 """
@@ -26,9 +30,20 @@ _EXPORTS = {
     "TTT_ERR_DEVICE", "MLP_SWIGLU", "MLP_LINEAR",
 }
 
+_OPS_EXPORTS = {
+    "ttt_delta_config", "ttt_delta_tokens", "make_delta_config", "ttt_delta_workspace_bytes",
+    "alloc_delta_workspace", "ttt_delta_chunk", "ttt_delta_step", "ttt_delta_backward",
+    "DEVICE_ERR_OFFSETS", "ttt_rope_config", "make_rope_config", "ttt_rope", "ROPE_HALF",
+    "ROPE_PAIRS", "ROPE_FREQ_AXIS", "ROPE_FREQ_HEAD", "ttt_norm_config", "make_norm_config",
+    "ttt_norm_workspace_bytes", "ttt_layer_norm", "ttt_layer_norm_backward",
+}
+
 
 def __getattr__(name):
     if name in _EXPORTS:
         from . import _binding
         return getattr(_binding, name)
+    if name in _OPS_EXPORTS:
+        from . import _ops
+        return getattr(_ops, name)
     raise AttributeError(name)

@@ -20,6 +20,7 @@ enum DeviceErr : int {
   kErrWaitOperand = 5,   // MMA issuer gave up waiting for an epilogue operand
   kErrWaitFinal = 6,     // final drain gave up
   kErrSelfTest = 7,      // ttt_selftest_wait_timeout: the wait ran out as intended
+  kErrOffsets = 8,       // sequence offsets decrease or leave 0..n
   // debug builds only (TTT_DCHECK): a range check failed
   kErrCheckTma = 16,     // a TMA coordinate outside its tensor
   kErrCheckTmem = 17,    // a TMEM column outside the allocation

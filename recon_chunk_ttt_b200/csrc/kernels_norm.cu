@@ -1,0 +1,489 @@
+// Layer norm and its gradient.
+//   y = (x - mean) rstd w + b;   with xh = (x - mean) rstd, g = dy w:
+//   dx = rstd (g - mean(g) - xh mean(g xh)),  dw = sum_rows dy xh,  db = sum_rows dy.
+//
+// Bound by memory: forward reads x and writes y, backward reads x and dy and
+// writes dx, each once.  A row lies in the registers of a group of threads
+// (a warp, 4 or 16 of them), so the mean, then the squares about the mean, then
+// the result are taken from one read.  In the backward kernel a thread keeps
+// its columns' sums of dy and dy xh in registers over all rows of its block;
+// the blocks' sums meet in the workspace and a second kernel adds them in
+// their order (no atomics).
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "ops_internal.h"
+
+namespace ttt {
+namespace {
+
+template <typename T, int V>
+struct Ld;
+template <>
+struct Ld<float, 4> {
+  static __device__ __forceinline__ void get(const float* p, float* x) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  }
+  static __device__ __forceinline__ void put(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+};
+template <>
+struct Ld<float, 1> {
+  static __device__ __forceinline__ void get(const float* p, float* x) { x[0] = *p; }
+  static __device__ __forceinline__ void put(float* p, const float* x) { *p = x[0]; }
+};
+template <>
+struct Ld<__nv_bfloat16, 8> {
+  static __device__ __forceinline__ void get(const __nv_bfloat16* p, float* x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                   pack_bf16x2(x[6], x[7]));
+  }
+};
+template <>
+struct Ld<__nv_bfloat16, 1> {
+  static __device__ __forceinline__ void get(const __nv_bfloat16* p, float* x) {
+    x[0] = __bfloat162float(*p);
+  }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, const float* x) {
+    *p = __float2bfloat16_rn(x[0]);
+  }
+};
+// w, b: floats, as many as the token vector holds
+template <int V>
+__device__ __forceinline__ void get_f(const float* p, float* x) {
+  if (V == 1) {
+    x[0] = *p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) Ld<float, 4>::get(p + i, x + i);
+  }
+}
+
+// Sum over the G threads of a group (one or more warps of the block), the same
+// value in all of them, in a fixed order.  `slot` alternates between sums so
+// that one barrier a sum is enough.
+template <int G>
+__device__ __forceinline__ float group_sum(float x, float* red) {
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+  if (G > 32) {
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int w = 0; w < G / 32; ++w) x += red[w];
+  }
+  return x;
+}
+
+// Threads of a block: 8 rows a block for a warp each, else one row.
+constexpr int block_of(int G) { return G == 32 ? 256 : G; }
+
+template <typename T, int V, int G, int NV>
+__global__ void __launch_bounds__(block_of(G))
+    norm_kernel(const T* X, int64_t ldx, int64_t rows, int dim, float eps,
+                const float* __restrict__ w, const float* __restrict__ b, T* Y, float* stats) {
+  __shared__ float red[2][G / 32];
+  const int64_t row = (int64_t)blockIdx.x * (block_of(G) / G) + threadIdx.x / G;
+  if (G == 32 && row >= rows) return;  // whole warps; a larger group is the block
+  const int l = threadIdx.x % G, nv = dim / V;
+  const T* x = X + row * ldx;
+  float v[NV][V], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (l + i * G < nv) {
+      Ld<T, V>::get(x + (l + i * G) * V, v[i]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[i][c] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) sum += v[i][c];
+  }
+  const float inv = 1.f / dim;
+  const float mean = group_sum<G>(sum, red[0]) * inv;
+  float sq = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (l + i * G < nv)
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        v[i][c] -= mean;
+        sq = fmaf(v[i][c], v[i][c], sq);
+      }
+  const float rstd = 1.f / sqrtf(group_sum<G>(sq, red[1]) * inv + eps);
+  T* y = Y + row * dim;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (l + i * G < nv) {
+      float g[V], o[V];
+      if (w != nullptr) get_f<V>(w + (l + i * G) * V, g);
+#pragma unroll
+      for (int c = 0; c < V; ++c) o[c] = w != nullptr ? v[i][c] * rstd * g[c] : v[i][c] * rstd;
+      if (b != nullptr) {
+        get_f<V>(b + (l + i * G) * V, g);
+#pragma unroll
+        for (int c = 0; c < V; ++c) o[c] += g[c];
+      }
+      Ld<T, V>::put(y + (l + i * G) * V, o);
+    }
+  if (stats != nullptr && l == 0) stats[2 * row] = mean, stats[2 * row + 1] = rstd;
+}
+
+// Rows wider than the registers of a block: a block of 512 threads reads its row
+// three times (from the caches after the first).
+template <typename T>
+__global__ void __launch_bounds__(512)
+    norm_wide_kernel(const T* X, int64_t ldx, int dim, float eps, const float* __restrict__ w,
+                     const float* __restrict__ b, T* Y, float* stats) {
+  __shared__ float red[2][16];
+  const int64_t row = blockIdx.x;
+  const T* x = X + row * ldx;
+  float sum = 0.f, sq = 0.f, e;
+  for (int c = threadIdx.x; c < dim; c += 512) {
+    Ld<T, 1>::get(x + c, &e);
+    sum += e;
+  }
+  const float mean = group_sum<512>(sum, red[0]) / dim;
+  for (int c = threadIdx.x; c < dim; c += 512) {
+    Ld<T, 1>::get(x + c, &e);
+    sq = fmaf(e - mean, e - mean, sq);
+  }
+  const float rstd = 1.f / sqrtf(group_sum<512>(sq, red[1]) / dim + eps);
+  for (int c = threadIdx.x; c < dim; c += 512) {
+    Ld<T, 1>::get(x + c, &e);
+    e = (e - mean) * rstd;
+    if (w != nullptr) e *= w[c];
+    if (b != nullptr) e += b[c];
+    Ld<T, 1>::put(Y + row * dim + c, &e);
+  }
+  if (stats != nullptr && threadIdx.x == 0) stats[2 * row] = mean, stats[2 * row + 1] = rstd;
+}
+
+// One block's sums over its rows, columns in place: part[2][blocks][dim], dw then db.
+template <typename T, int V, int G, int NV, bool COLS>
+__global__ void __launch_bounds__(block_of(G))
+    norm_backward_kernel(const T* X, int64_t ldx, const T* dY, int64_t lddy, int64_t rows, int dim,
+                         const float* __restrict__ w, const float* __restrict__ stats, T* dX,
+                         float* part) {
+  constexpr int RB = block_of(G) / G;  // rows a block works on at a time
+  __shared__ float red[2][2][G / 32];
+  extern __shared__ float cols[];  // [RB > 1 ? dim : 0]
+  const int l = threadIdx.x % G, nv = dim / V;
+  const float inv = 1.f / dim;
+  float aw[COLS ? NV : 1][V] = {}, ab[COLS ? NV : 1][V] = {};
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RB + threadIdx.x / G; row < rows;
+       row += (int64_t)gridDim.x * RB) {
+    const float mean = stats[2 * row], rstd = stats[2 * row + 1];
+    float xh[NV][V], g[NV][V], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (l + i * G < nv) {
+        Ld<T, V>::get(X + row * ldx + (l + i * G) * V, xh[i]);
+        Ld<T, V>::get(dY + row * lddy + (l + i * G) * V, g[i]);
+      }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (l + i * G < nv) {
+        float ww[V];
+        if (w != nullptr) get_f<V>(w + (l + i * G) * V, ww);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          xh[i][c] = (xh[i][c] - mean) * rstd;
+          if (COLS) {
+            aw[i][c] = fmaf(g[i][c], xh[i][c], aw[i][c]);
+            ab[i][c] += g[i][c];
+          }
+          if (w != nullptr) g[i][c] *= ww[c];
+          s1 += g[i][c];
+          s2 = fmaf(g[i][c], xh[i][c], s2);
+        }
+      }
+    if (dX == nullptr) continue;  // the same for the whole grid
+    s1 = group_sum<G>(s1, red[turn][0]) * inv;
+    s2 = group_sum<G>(s2, red[turn][1]) * inv;
+    turn ^= 1;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (l + i * G < nv) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) g[i][c] = rstd * (g[i][c] - s1 - xh[i][c] * s2);
+        Ld<T, V>::put(dX + row * dim + (l + i * G) * V, g[i]);
+      }
+  }
+  if (COLS) {
+    float* pw = part + (size_t)blockIdx.x * dim;
+    float* pb = pw + (size_t)gridDim.x * dim;
+    for (int which = 0; which < 2; ++which) {
+      float(&acc)[COLS ? NV : 1][V] = which == 0 ? aw : ab;
+      float* out = which == 0 ? pw : pb;
+      if (RB == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (l + i * G < nv)
+#pragma unroll
+            for (int c = 0; c < V; ++c) out[(l + i * G) * V + c] = acc[i][c];
+      } else {  // the block's warps in turn
+        for (int r = 0; r < RB; ++r) {
+          if ((int)threadIdx.x / G == r)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+              if (l + i * G < nv)
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                  float& z = cols[(l + i * G) * V + c];
+                  z = r == 0 ? acc[i][c] : z + acc[i][c];
+                }
+          __syncthreads();
+        }
+        for (int c = threadIdx.x; c < dim; c += block_of(G)) out[c] = cols[c];
+        __syncthreads();
+      }
+    }
+  }
+}
+
+// dX of wide rows: three reads, as the forward kernel.
+template <typename T>
+__global__ void __launch_bounds__(512)
+    norm_backward_wide_kernel(const T* X, int64_t ldx, const T* dY, int64_t lddy, int dim,
+                              const float* __restrict__ w, const float* __restrict__ stats, T* dX) {
+  __shared__ float red[2][16];
+  const int64_t row = blockIdx.x;
+  const float mean = stats[2 * row], rstd = stats[2 * row + 1];
+  float s1 = 0.f, s2 = 0.f, x, g;
+  for (int c = threadIdx.x; c < dim; c += 512) {
+    Ld<T, 1>::get(X + row * ldx + c, &x);
+    Ld<T, 1>::get(dY + row * lddy + c, &g);
+    if (w != nullptr) g *= w[c];
+    s1 += g;
+    s2 = fmaf(g, (x - mean) * rstd, s2);
+  }
+  s1 = group_sum<512>(s1, red[0]) / dim;
+  s2 = group_sum<512>(s2, red[1]) / dim;
+  for (int c = threadIdx.x; c < dim; c += 512) {
+    Ld<T, 1>::get(X + row * ldx + c, &x);
+    Ld<T, 1>::get(dY + row * lddy + c, &g);
+    if (w != nullptr) g *= w[c];
+    g = rstd * (g - s1 - (x - mean) * rstd * s2);
+    Ld<T, 1>::put(dX + row * dim + c, &g);
+  }
+}
+
+// Column sums of wide rows: a thread owns a column, a block a range of rows.
+// Runs before dX is written, which may lie over X or dY.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    norm_cols_wide_kernel(const T* X, int64_t ldx, const T* dY, int64_t lddy, int64_t rows,
+                          int64_t per, int dim, const float* __restrict__ stats, float* part) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= dim) return;
+  const int64_t r0 = (int64_t)blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
+  float sw = 0.f, sb = 0.f, x, g;
+  for (int64_t row = r0; row < r1; ++row) {
+    Ld<T, 1>::get(X + row * ldx + c, &x);
+    Ld<T, 1>::get(dY + row * lddy + c, &g);
+    sw = fmaf(g, (x - stats[2 * row]) * stats[2 * row + 1], sw);
+    sb += g;
+  }
+  part[(size_t)blockIdx.y * dim + c] = sw;
+  part[((size_t)gridDim.y + blockIdx.y) * dim + c] = sb;
+}
+
+// dw, db = the blocks' sums, added in order: 32 columns a block, 8 rows of
+// threads take every 8th block's sum, then their 8 sums in order.
+__global__ void __launch_bounds__(256)
+    norm_columns_kernel(const float* __restrict__ part, int blocks, int dim, float* dw, float* db) {
+  __shared__ float red[8][32];
+  float* out = blockIdx.y == 0 ? dw : db;
+  if (out == nullptr) return;
+  const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
+  const float* p = part + (size_t)blockIdx.y * blocks * dim + c;
+  float s = 0.f;
+  if (c < dim)
+    for (int k = r; k < blocks; k += 8) s += p[(size_t)k * dim];
+  red[r][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (r == 0 && c < dim) {
+    for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x];
+    out[c] = s;
+  }
+}
+
+// How a row is laid over threads: G threads, NV vectors of V values each.  The
+// smallest group that holds the row in at most 4 vectors a thread (registers:
+// 32 values; the backward kernel keeps 4 such arrays), except the largest
+// group, which takes up to 8.  G = 0: too wide.
+struct Shape {
+  int V, G, NV;
+};
+Shape shape_of(const NormArgs& a, bool aligned) {
+  Shape s;
+  const int full = a.bf16 ? 8 : 4;
+  s.V = aligned && a.dim % full == 0 ? full : 1;
+  const int64_t nv = (a.dim + s.V - 1) / s.V;
+  s.G = nv <= 32 * 4 ? 32 : nv <= 128 * 4 ? 128 : nv <= 512 * 8 ? 512 : 0;
+  if (s.G == 512 && s.V == 8 && nv > 512 * 4) s.G = 0;
+  if (s.G == 0) return s;
+  const int64_t per = (nv + s.G - 1) / s.G;
+  s.NV = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8;
+  return s;
+}
+
+bool vector_rows(const NormArgs& a, const void* X, int64_t ldx, const void* Y, int64_t ldy) {
+  const int full = a.bf16 ? 8 : 4;
+  (void)X, (void)Y;  // 16-byte aligned, checked at the entry
+  return ldx % full == 0 && ldy % full == 0;
+}
+
+constexpr int kBlocksPerSM = 8;
+
+// Blocks of the backward kernel (and the rows of its partial sums).
+int backward_blocks(const NormArgs& a, const Shape& s) {
+  const int rb = s.G == 32 ? 8 : 1;
+  const int64_t need = (a.rows + rb - 1) / rb;
+  const int64_t most = 148 * (s.G == 512 ? 2 : s.G == 128 ? kBlocksPerSM : 3);
+  return (int)(need < most ? (need < 1 ? 1 : need) : most);
+}
+int wide_blocks(const NormArgs& a) { return (int)(a.rows < 64 ? (a.rows < 1 ? 1 : a.rows) : 64); }
+
+template <typename T, int V, int G, int NV>
+cudaError_t launch_forward(const NormArgs& a, const void* X, int64_t ldx, const float* w,
+                           const float* b, void* Y, float* stats, cudaStream_t st) {
+  constexpr int rb = block_of(G) / G;
+  norm_kernel<T, V, G, NV><<<(unsigned)((a.rows + rb - 1) / rb), block_of(G), 0, st>>>(
+      static_cast<const T*>(X), ldx, a.rows, (int)a.dim, a.eps, w, b, static_cast<T*>(Y), stats);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, int G, int NV>
+cudaError_t launch_backward(const NormArgs& a, const void* X, int64_t ldx, const void* dY,
+                            int64_t lddy, const float* w, const float* stats, void* dX,
+                            float* part, int blocks, cudaStream_t st) {
+  const int smem = G == 32 && part != nullptr ? (int)a.dim * 4 : 0;
+  if (part != nullptr)
+    norm_backward_kernel<T, V, G, NV, true><<<blocks, block_of(G), smem, st>>>(
+        static_cast<const T*>(X), ldx, static_cast<const T*>(dY), lddy, a.rows, (int)a.dim, w,
+        stats, static_cast<T*>(dX), part);
+  else
+    norm_backward_kernel<T, V, G, NV, false><<<blocks, block_of(G), 0, st>>>(
+        static_cast<const T*>(X), ldx, static_cast<const T*>(dY), lddy, a.rows, (int)a.dim, w,
+        stats, static_cast<T*>(dX), part);
+  return cudaGetLastError();
+}
+
+// f(T, V, G, NV) for a shape.
+#define TTT_NORM_NV(T, V, G, CALL)       \
+  (s.NV == 1   ? CALL<T, V, G, 1> NORM_ARGS   \
+   : s.NV == 2 ? CALL<T, V, G, 2> NORM_ARGS   \
+               : CALL<T, V, G, 4> NORM_ARGS)
+#define TTT_NORM_G(T, V, CALL)                                  \
+  (s.G == 32    ? TTT_NORM_NV(T, V, 32, CALL)                   \
+   : s.G == 128 ? TTT_NORM_NV(T, V, 128, CALL)                  \
+   : s.NV == 8  ? CALL<T, V == 8 ? 1 : V, 512, 8> NORM_ARGS     \
+                : TTT_NORM_NV(T, V, 512, CALL))
+#define TTT_NORM(CALL)                                                                  \
+  (a.bf16 ? (s.V == 8 ? TTT_NORM_G(__nv_bfloat16, 8, CALL) : TTT_NORM_G(__nv_bfloat16, 1, CALL)) \
+          : (s.V == 4 ? TTT_NORM_G(float, 4, CALL) : TTT_NORM_G(float, 1, CALL)))
+
+}  // namespace
+
+size_t norm_workspace_bytes(const NormArgs& a) {
+  // the largest of the plans that strides may ask for
+  size_t most = (size_t)wide_blocks(a);
+  for (int aligned = 0; aligned < 2; ++aligned) {
+    const Shape s = shape_of(a, aligned != 0);
+    if (s.G != 0 && (size_t)backward_blocks(a, s) > most) most = (size_t)backward_blocks(a, s);
+  }
+  return most * 2 * (size_t)a.dim * 4;
+}
+
+cudaError_t norm_forward(const NormArgs& a, const void* X, int64_t ldx, const float* w,
+                         const float* b, void* Y, float* stats, cudaStream_t st) {
+  if (a.rows == 0) return cudaSuccess;
+  const Shape s = shape_of(a, vector_rows(a, X, ldx, Y, a.dim));
+  TraceScope ts("layer_norm", st);
+  if (s.G == 0) {
+    if (a.bf16)
+      norm_wide_kernel<<<(unsigned)a.rows, 512, 0, st>>>(
+          static_cast<const __nv_bfloat16*>(X), ldx, (int)a.dim, a.eps, w, b,
+          static_cast<__nv_bfloat16*>(Y), stats);
+    else
+      norm_wide_kernel<<<(unsigned)a.rows, 512, 0, st>>>(static_cast<const float*>(X), ldx,
+                                                         (int)a.dim, a.eps, w, b,
+                                                         static_cast<float*>(Y), stats);
+    return cudaGetLastError();
+  }
+#define NORM_ARGS (a, X, ldx, w, b, Y, stats, st)
+  return TTT_NORM(launch_forward);
+#undef NORM_ARGS
+}
+
+cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const void* dY,
+                          int64_t lddy, const float* w, const float* stats, void* dX, float* dw,
+                          float* db, void* ws, cudaStream_t st) {
+  const bool cols = dw != nullptr || db != nullptr;
+  if (a.rows == 0) {
+    cudaError_t e = cudaSuccess;
+    if (dw != nullptr) e = cudaMemsetAsync(dw, 0, (size_t)a.dim * 4, st);
+    if (e == cudaSuccess && db != nullptr) e = cudaMemsetAsync(db, 0, (size_t)a.dim * 4, st);
+    return e;
+  }
+  const Shape s = shape_of(a, vector_rows(a, X, ldx, dY, lddy));
+  float* part = cols ? static_cast<float*>(ws) : nullptr;
+  cudaError_t e = cudaSuccess;
+  int blocks;
+  if (s.G == 0) {
+    blocks = wide_blocks(a);
+    const int64_t per = (a.rows + blocks - 1) / blocks;
+    TraceScope ts("layer_norm_backward", st);
+    const dim3 grid((unsigned)((a.dim + 255) / 256), (unsigned)blocks);
+    if (a.bf16) {
+      using B = __nv_bfloat16;
+      const B *x = static_cast<const B*>(X), *dy = static_cast<const B*>(dY);
+      if (cols)
+        norm_cols_wide_kernel<<<grid, 256, 0, st>>>(x, ldx, dy, lddy, a.rows, per, (int)a.dim,
+                                                    stats, part);
+      if (dX != nullptr)
+        norm_backward_wide_kernel<<<(unsigned)a.rows, 512, 0, st>>>(
+            x, ldx, dy, lddy, (int)a.dim, w, stats, static_cast<B*>(dX));
+    } else {
+      const float *x = static_cast<const float*>(X), *dy = static_cast<const float*>(dY);
+      if (cols)
+        norm_cols_wide_kernel<<<grid, 256, 0, st>>>(x, ldx, dy, lddy, a.rows, per, (int)a.dim,
+                                                    stats, part);
+      if (dX != nullptr)
+        norm_backward_wide_kernel<<<(unsigned)a.rows, 512, 0, st>>>(
+            x, ldx, dy, lddy, (int)a.dim, w, stats, static_cast<float*>(dX));
+    }
+    e = cudaGetLastError();
+  } else {
+    blocks = backward_blocks(a, s);
+    TraceScope ts("layer_norm_backward", st);
+#define NORM_ARGS (a, X, ldx, dY, lddy, w, stats, dX, part, blocks, st)
+    e = TTT_NORM(launch_backward);
+#undef NORM_ARGS
+  }
+  if (e != cudaSuccess || !cols) return e;
+  TraceScope ts("layer_norm_columns", st);
+  norm_columns_kernel<<<dim3((unsigned)((a.dim + 31) / 32), 2), 256, 0, st>>>(part, blocks,
+                                                                              (int)a.dim, dw, db);
+  return cudaGetLastError();
+}
+
+}  // namespace ttt
