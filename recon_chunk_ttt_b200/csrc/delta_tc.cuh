@@ -1,0 +1,182 @@
+// Shared pieces of the tensor-core kernels of the gated delta rule
+// (kernels_delta_tc.cu, kernels_delta_grad.cu): sequences and chunks, operand
+// splitting, warp-level matrix fragments.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "ops_internal.h"
+#include "tc_util.cuh"
+
+namespace ttt {
+namespace {
+
+constexpr int kC = 64;  // tokens of a chunk
+
+// The tokens of sequence i, and its first chunk slot: start / kC + i leaves
+// room for the chunks of every sequence before it (ceil(len / kC) <= end / kC -
+// start / kC + 1) and needs no scan.  Offsets that decrease or leave 0..n are
+// cut, so that every slot and row stays inside its array.
+struct SeqRange {
+  int64_t t0, t1, slot;
+  bool bad;
+};
+__device__ __forceinline__ SeqRange seq_range(const int64_t* offsets, int64_t n, int64_t i) {
+  if (offsets == nullptr) return {0, n, 0, false};
+  const int64_t a = offsets[i], b = offsets[i + 1];
+  SeqRange s;
+  s.bad = a < 0 || b < a || b > n;
+  s.t0 = a < 0 ? 0 : (a > n ? n : a);
+  s.t1 = b < s.t0 ? s.t0 : (b > n ? n : b);
+  s.slot = s.t0 / kC + i;
+  return s;
+}
+
+// The tokens of a chunk slot (len = 0: the slot holds none): the last sequence
+// whose first slot is not behind it, found by halving.
+struct ChunkRange {
+  int64_t t0;
+  int len;
+};
+__device__ __forceinline__ ChunkRange chunk_range(const int64_t* offsets, int64_t n, int64_t seqs,
+                                                  int64_t slot) {
+  int64_t lo = 0, hi = seqs;  // the answer lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (seq_range(offsets, n, mid).slot <= slot)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const SeqRange s = seq_range(offsets, n, lo);
+  ChunkRange c;
+  c.t0 = s.t0 + (slot - s.slot) * kC;
+  c.len = slot < s.slot || c.t0 >= s.t1 ? 0 : s.t1 - c.t0 < kC ? (int)(s.t1 - c.t0) : kC;
+  return c;
+}
+
+// ---------------------------------------------------------------- fragments
+// Byte offset of (row, col) in a tile of 64-value (128-byte) columns blocks of
+// `rows` rows each, 16-byte units swizzled by the row: what a TMA load with the
+// 128-byte swizzle lays down, and free of bank conflicts for ldmatrix.
+__device__ __forceinline__ uint32_t sw(int rows, int row, int col) {
+  return (uint32_t)((col >> 6) * rows * 128 + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) +
+                    (col & 7) * 2);
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm4_t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 operands, fp32 sums.  c: rows lane/4
+// and +8, columns 2 (lane%4) + {0, 1}; a pair of c tiles is laid out like an a
+// operand, which lets a product's result be the next one's operand in place.
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x = hi + mid + lo in bf16: hi and mid are x's upper bits cut off (exact
+// remainders), lo the rest rounded: 24 bits, as good as fp32.  Two values, packed.
+__device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t& mid,
+                                       uint32_t& lo) {
+  const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
+  hi = __byte_perm(xb, yb, 0x7632);
+  const float x1 = x - __uint_as_float(xb & 0xffff0000u);
+  const float y1 = y - __uint_as_float(yb & 0xffff0000u);
+  const uint32_t xc = __float_as_uint(x1), yc = __float_as_uint(y1);
+  mid = __byte_perm(xc, yc, 0x7632);
+  lo = pack_bf16x2(x1 - __uint_as_float(xc & 0xffff0000u), y1 - __uint_as_float(yc & 0xffff0000u));
+}
+// The a operand made of two neighbouring c tiles, split.
+__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4],
+                                        uint32_t (&hi)[4], uint32_t (&mid)[4], uint32_t (&lo)[4]) {
+  split3(c0[0], c0[1], hi[0], mid[0], lo[0]);
+  split3(c0[2], c0[3], hi[1], mid[1], lo[1]);
+  split3(c1[0], c1[1], hi[2], mid[2], lo[2]);
+  split3(c1[2], c1[3], hi[3], mid[3], lo[3]);
+}
+
+// An A operand kept in shared memory, 16 bytes a lane.
+__device__ __forceinline__ void load_a(const uint4* p, uint32_t (&r)[4]) {
+  const uint4 v = *p;
+  r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+}
+// Mask of a packed pair of tokens t, t + 1 of which those before `valid` count.
+__device__ __forceinline__ uint32_t keep_pair(int t, int valid) {
+  return t + 1 < valid ? 0xffffffffu : t < valid ? 0xffffu : 0u;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ---------------------------------------------------------------- workspace
+// What the chunk kernel leaves for each (slot, head): T as three bf16 parts,
+// P (one part for the forward pass, three for the gradient), and the gates
+// gamma[64], rest[64], beta[64], each token's.  T and P are lower triangular:
+// their 16-column strips hold the rows from the diagonal block down, 32 bytes
+// a row, the two 16-byte units exchanged in every second group of four rows
+// (free of bank conflicts for ldmatrix, and what a TMA load with the 32-byte
+// swizzle lays down).  They are stored as they lie in shared memory, so one
+// bulk copy brings the whole block.
+constexpr int kTri = 32 * (64 + 48 + 32 + 16);
+constexpr int kGates = 1024;
+__host__ __device__ constexpr int chunk_bytes(int p_parts) { return (3 + p_parts) * kTri + kGates; }
+// (row, 8-value unit) of a tile of 16 columns, 32 bytes a row
+__device__ __forceinline__ uint32_t sw32(int row, int unit) {
+  return (uint32_t)(row * 32 + ((unit ^ ((row >> 2) & 1)) << 4));
+}
+// (row, col) of a triangle, col / 16 <= row / 16
+__device__ __forceinline__ uint32_t tri(int row, int col) {
+  const int k = col >> 4;
+  return (uint32_t)(32 * (64 * k - 8 * k * (k - 1))) + sw32(row - 16 * k, (col >> 3) & 1) +
+         (col & 7) * 2;
+}
+
+inline int64_t chunk_slots(const DeltaArgs& a) { return a.n / kC + a.seqs; }
+
+// Token rows as boxes of 64 tokens: all columns of a head, as [d / 64][64][64];
+// or 16 columns, as [64][16].
+inline bool head_map(CUtensorMap* m, const void* base, int64_t n, int64_t ld, int cols, int d) {
+  const uint64_t dims[3] = {64, (uint64_t)n, (uint64_t)cols / 64};
+  const uint64_t str[2] = {(uint64_t)ld * 2, 128};
+  const uint32_t box[3] = {64, kC, (uint32_t)d / 64};
+  return make_map(m, base, 3, dims, str, box);
+}
+inline bool strip_map(CUtensorMap* m, const void* base, int64_t n, int64_t ld, int cols) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)n};
+  const uint64_t str[1] = {(uint64_t)ld * 2};
+  const uint32_t box[2] = {16, kC};
+  return make_map(m, base, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_32B);
+}
+
+}  // namespace
+
+// Inverses, P and gates of every chunk into `blocks` (kernels_delta_tc.cu).
+cudaError_t delta_prepare(const DeltaArgs& a, bool gradient, uint8_t* blocks, cudaStream_t st);
+
+}  // namespace ttt

@@ -1,0 +1,738 @@
+// Gated delta rule in chunks of 64 tokens on the tensor cores.
+//
+// Inside a chunk, with G the running sum of the log decays, gamma = e^G,
+// Gamma_ij = e^(G_i - G_j) and S the state before the chunk (rows = outputs):
+//   (I + L) U = beta (V - gamma K S^T),  L = strictly lower part of beta Gamma (K K^T)
+//   O = scale gamma (Q S^T) + P U,       P = lower part of scale Gamma (Q K^T)
+//   S <- gamma_64 S + U^T (rest K),      rest_j = e^(G_64 - G_j)
+// T = (I + L)^-1 and P need no state: delta_chunk_kernel forms them for all
+// chunks at once.  What is left is a chain over the chunks of a sequence, and
+// delta_state_kernel makes its step short.  It works on the transposes: a warp
+// owns 16 rows of S in registers, as accumulators, whose layout is that of an
+// A operand: S K^T, then (beta ..)^T T^T, then U^T K all read the result before
+// them from registers, with no trip through shared memory and no barrier
+// between warps.  (A tcgen05 tile would take 64 or 128 rows and carry every
+// intermediate from tensor memory through registers to shared memory and back,
+// three times a step, on the one path that cannot be overlapped.)
+// K, Q, V tiles come by TMA and T, P, gates by one bulk copy, two chunks deep.
+//
+// The state is fp32 in and out, so operands that are not bf16 by nature (S, T,
+// the right-hand side, U) enter as three bf16 parts, of whose products those
+// above 2^-24 are taken: S K^T and U^T K three each (K is exact), T six.  O is
+// rounded to bf16 in the end: two parts of S and U, one of P (2^-9, a bf16
+// operand's rounding, next to O's own).
+
+#include "delta_tc.cuh"
+#include <type_traits>
+
+namespace ttt {
+namespace {
+
+// ----------------------------------------------------------------------------
+// delta_chunk_kernel: T, P and the gates of one chunk and head.
+// ----------------------------------------------------------------------------
+constexpr int kChunkThreads = 128;
+constexpr int kLS = 36;  // row length of the 32 x 32 fp32 blocks: 16-byte rows, spread over banks
+
+struct ChunkArgs {
+  const __nv_bfloat16 *Q, *K;
+  const float *g, *b;
+  int64_t ldq, ldk, n;
+  const int64_t* offsets;
+  int64_t seqs;
+  int H, Hk;
+  float scale;
+  uint8_t* blocks;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+
+template <int D, bool GRAD>
+__global__ void __launch_bounds__(kChunkThreads)
+    delta_chunk_kernel(const __grid_constant__ ChunkArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t *sK = smem, *sQ = smem + kC * D * 2;
+  // fp32 blocks over the tiles once the products are taken: L21, and the
+  // transposes of L11, L22; T11, T22, L21 T11, T21
+  float* fb = reinterpret_cast<float*>(smem);
+  __shared__ double G[kC];
+  __shared__ float beta[kC];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int64_t slot = blockIdx.x;
+  const int h = blockIdx.y, hk = h / (a.H / a.Hk);
+  const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
+  if (c.len == 0) return;
+
+  for (int e = tid; e < kC * D / 8; e += kChunkThreads) {
+    const int row = e / (D / 8), col = e % (D / 8) * 8;
+    const bool ok = row < c.len;
+    const int64_t t = c.t0 + (ok ? row : 0);
+    cp16(smem_u32(sK) + sw(kC, row, col), a.K + t * a.ldk + hk * D + col, ok);
+    cp16(smem_u32(sQ) + sw(kC, row, col), a.Q + t * a.ldq + hk * D + col, ok);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if (warp == 0) {  // running sums of the log decays, in fp64: differences of far sums stay exact
+    double x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = 2 * lane + i;
+      const float g = j < c.len ? a.g[(c.t0 + j) * a.H + h] : 0.f;
+      x[i] = g < -1e4f ? -1e4 : (double)g;  // e^-1e4 is 0 like e^-inf, but its sums are numbers
+    }
+    double s = x[0] + x[1];
+    for (int m = 1; m < 32; m *= 2) {
+      const double o = __shfl_up_sync(0xffffffffu, s, m);
+      if (lane >= m) s += o;
+    }
+    G[2 * lane] = s - x[1];
+    G[2 * lane + 1] = s;
+  } else if (warp == 1) {
+    for (int j = lane; j < kC; j += 32) {
+      float b = j < c.len ? a.b[(c.t0 + j) * a.H + h] : 0.f;
+      // The gradient divides U by beta.  A beta of nothing becomes 2^-100: the
+      // token's U is then that small (its part in any sum rounds away), but
+      // U / beta has all its digits.
+      if (GRAD && j < c.len && fabsf(b) < 0x1p-100f) b = 0x1p-100f;
+      beta[j] = b;
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+
+  // K K^T and Q K^T: a warp takes 16 rows, up to the diagonal
+  float kk[8][4] = {}, qk[8][4] = {};
+  const int m0 = warp * 16;
+  for (int k = 0; k < D / 16; ++k) {
+    uint32_t ak[4], aq[4], b[4];
+    const int ar = m0 + (lane % 16), ac = k * 16 + (lane / 16) * 8;
+    ldsm4(smem_u32(sK) + sw(kC, ar, ac), ak);
+    ldsm4(smem_u32(sQ) + sw(kC, ar, ac), aq);
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      if (p <= warp) {
+        ldsm4(smem_u32(sK) + sw(kC, p * 16 + (lane / 16) * 8 + lane % 8,
+                                k * 16 + (lane / 8 % 2) * 8), b);
+        mma(kk[2 * p], ak, b[0], b[1]);
+        mma(kk[2 * p + 1], ak, b[2], b[3]);
+        mma(qk[2 * p], aq, b[0], b[1]);
+        mma(qk[2 * p + 1], aq, b[2], b[3]);
+      }
+  }
+  __syncthreads();  // the tiles are free
+
+  uint8_t* out = a.blocks + (slot * a.H + h) * (int64_t)chunk_bytes(GRAD ? 3 : 1);
+  uint8_t* outP = out + 3 * kTri;
+  float *L21 = fb, *Lt1 = fb + 32 * kLS, *Lt2 = fb + 2 * 32 * kLS, *T1 = fb + 3 * 32 * kLS,
+        *T2 = fb + 4 * 32 * kLS, *Z = fb + 5 * 32 * kLS;
+#pragma unroll
+  for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int i = m0 + lane / 4 + 8 * half, j = nt * 8 + 2 * (lane % 4);
+      float p[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float e = j + x <= i ? expf((float)(G[i] - G[j + x])) : 0.f;
+        p[x] = j + x <= i ? a.scale * e * qk[nt][2 * half + x] : 0.f;
+        const float l = j + x < i ? beta[i] * e * kk[nt][2 * half + x] : 0.f;
+        if (i < 32) {
+          if (j + x < 32) Lt1[(j + x) * kLS + i] = l;
+        } else if (j + x < 32) {
+          L21[(i - 32) * kLS + j + x] = l;
+        } else {
+          Lt2[(j + x - 32) * kLS + i - 32] = l;
+        }
+      }
+      if (j / 16 > i / 16) continue;  // above the diagonal blocks
+      uint32_t* dst = reinterpret_cast<uint32_t*>(outP + tri(i, j));
+      if (GRAD) {
+        uint32_t hi, mid, lo;
+        split3(p[0], p[1], hi, mid, lo);
+        dst[0] = hi;
+        dst[kTri / 4] = mid;
+        dst[2 * kTri / 4] = lo;
+      } else {
+        dst[0] = pack_bf16x2(p[0], p[1]);
+      }
+    }
+  __syncthreads();
+
+  // (I + L)^-1 by halves: the two diagonal blocks by substitution (a thread
+  // holds a column), then T21 = -T22 L21 T11.
+  if (warp < 2) {
+    const float* Lt = warp == 0 ? Lt1 : Lt2;
+    float* T = warp == 0 ? T1 : T2;
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = i == lane ? 1.f : 0.f;
+#pragma unroll
+    for (int k = 0; k < 31; ++k)
+#pragma unroll
+      for (int i4 = (k + 1) / 4; i4 < 8; ++i4) {
+        const float4 l = *reinterpret_cast<const float4*>(Lt + k * kLS + i4 * 4);
+        const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (i4 * 4 + q > k) x[i4 * 4 + q] = fmaf(-lv[q], x[k], x[i4 * 4 + q]);
+      }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) T[i * kLS + lane] = x[i];
+  } else if (warp == 2) {  // gates
+    float* gates = reinterpret_cast<float*>(out + (3 + (GRAD ? 3 : 1)) * kTri);
+    for (int j = lane; j < kC; j += 32) {
+      gates[j] = expf((float)G[j]);
+      gates[kC + j] = expf((float)(G[kC - 1] - G[j]));
+      gates[2 * kC + j] = beta[j];
+    }
+  }
+  __syncthreads();
+  const int r = tid / 4, cb = tid % 4 * 8;
+  float z[8] = {};
+#pragma unroll 4
+  for (int k = 0; k < 32; ++k) {
+    const float l = L21[r * kLS + k];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) z[q] = fmaf(l, T1[k * kLS + cb + q], z[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) Z[r * kLS + cb + q] = z[q];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) z[q] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < 32; ++k) {
+    const float l = -T2[r * kLS + k];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) z[q] = fmaf(l, Z[k * kLS + cb + q], z[q]);
+  }
+  // rows r and r + 32 of T, 8 columns of each half, as 16-byte units
+  const float* src[3] = {T1 + r * kLS + cb, z, T2 + r * kLS + cb};
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const int i = r + (q > 0 ? 32 : 0), j = cb + (q == 2 ? 32 : 0);
+    if (j / 16 > i / 16) continue;
+    uint32_t w[3][4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      split3(src[q][2 * x], src[q][2 * x + 1], w[0][x], w[1][x], w[2][x]);
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      *reinterpret_cast<uint4*>(out + x * kTri + tri(i, j)) =
+          make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// delta_state_kernel: the chain over a sequence's chunks.
+//
+// KS warps share 16 rows of S, D / KS columns each; a block has RG such groups.
+// The partial products S K^T, S Q^T are added through shared memory, each warp
+// takes its share of the tokens through r, u and o, and gets the others' u for
+// its columns of S: three meetings a step.
+// The tensor cores cut an accumulator's last bits off with every product they
+// add to it (measured: 1 + 0.75 ulp stays 1), so small parts are summed apart
+// from large ones, and the state takes one fp32 addition a chunk.
+// ----------------------------------------------------------------------------
+template <int D, int KS, int RG>
+struct SK {
+  static constexpr int WARPS = KS * RG;
+  static constexpr int KQ = kC * D * 2;               // one of K, Q
+  static constexpr int BLOCK = chunk_bytes(1);
+  static constexpr int V = kC * 32;                   // 16 columns
+  static constexpr int STAGE = 2 * KQ + RG * V + BLOCK;
+  // exchange of a group: partial r, partial o (each warp's for the others'
+  // tiles), r in parts, u in parts
+  static constexpr int X_PART = 8 * (KS - 1) * 32 * 16, X_R = 8 * 3 * 32 * 8, X_U = 8 * 5 * 32 * 8;
+  static constexpr int X = 2 * X_PART + X_R + X_U;
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int OFF_X = 2 * STAGE;
+  static constexpr int OFF_BAR = OFF_X + RG * X;
+  static constexpr int SMEM = OFF_BAR + 192 + 1024;
+  static_assert((KS == 2 || KS == 4) && RG <= 2, "tiles and barriers of a group");
+  static_assert(STAGE % 1024 == 0, "tiles are aligned to the swizzle");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct StateArgs {
+  int64_t n;
+  const int64_t* offsets;
+  int H, Hk;
+  float scale;
+  const uint8_t* blocks;
+  const float* S_in;
+  float* S_out;
+  __nv_bfloat16* O;
+  int* err;
+};
+
+template <int D, int KS, int RG>
+__global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
+    delta_state_kernel(const __grid_constant__ CUtensorMap mQ,
+                       const __grid_constant__ CUtensorMap mK,
+                       const __grid_constant__ CUtensorMap mV, const StateArgs a) {
+  using L = SK<D, KS, RG>;
+  constexpr int DK = D / KS, NT = 8 / KS;  // a warp's columns of S; its token tiles of r, u, o
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* empty = full + 2;
+  uint64_t* met = empty + 2;  // 3 for each group: partial sums, r, u are written
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(met + 3 * RG);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int h = blockIdx.y, hk = h / (a.H / a.Hk);
+  const int64_t seq = blockIdx.z;
+  const SeqRange sr = seq_range(a.offsets, a.n, seq);
+  const int64_t len = sr.t1 - sr.t0;
+  const int64_t nc = (len + kC - 1) / kC;
+  if (threadIdx.x == 0) {
+    if (sr.bad) atomicExch(a.err, (int)kErrOffsets);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], L::WARPS);
+    }
+    for (int i = 0; i < 3 * RG; ++i) mbar_init(&met[i], KS);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == L::WARPS) {  // ------------------------------------------------ loads
+    if (lane == 0) {
+      int64_t issued = 0;
+      for (int64_t c = 0; c < nc; ++c) {
+        const int s = (int)(c & 1);
+        if (!mbar_wait(&empty[s], (uint32_t)((c >> 1) & 1) ^ 1, abort_flag, a.err, kErrWaitEmpty))
+          break;
+        uint8_t* st = smem + s * L::STAGE;
+        const int t = (int)(sr.t0 + c * kC);
+        mbar_arrive_expect_tx(&full[s], L::STAGE);
+        tma_load_3d(st, &mK, &full[s], 0, t, hk * (D / 64));
+        tma_load_3d(st + L::KQ, &mQ, &full[s], 0, t, hk * (D / 64));
+        for (int g = 0; g < RG; ++g)
+          tma_load_2d(st + 2 * L::KQ + g * L::V, &mV, &full[s],
+                      h * D + ((int)blockIdx.x * RG + g) * 16, t);
+        bulk_load(st + 2 * L::KQ + RG * L::V,
+                  a.blocks + ((sr.slot + c) * a.H + h) * (int64_t)L::BLOCK, L::BLOCK, &full[s]);
+        ++issued;
+      }
+      drain_ring(full, 2, issued, a.err);
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- 16 rows
+  const int grp = warp / KS, kw = warp % KS;
+  const int r0 = ((int)blockIdx.x * RG + grp) * 16, c0 = kw * DK;
+  const int row = lane / 4, col = 2 * (lane % 4);
+  uint8_t* x_part = smem + L::OFF_X + grp * L::X;
+  uint8_t* x_r = x_part + 2 * L::X_PART;
+  uint8_t* x_u = x_r + L::X_R;
+  // A warp's token tiles (8 tokens): of each 2 KS the one of its number from the
+  // front and from the back, so that all warps have the same share of the
+  // triangles; the warp a tile belongs to; this lane's ldmatrix row in a pair.
+  const auto tile = [&](int j) { return j / 2 * 2 * KS + (j % 2 == 0 ? kw : 2 * KS - 1 - kw); };
+  const auto owner = [](int t) { return t % (2 * KS) < KS ? t % (2 * KS) : 2 * KS - 1 - t % (2 * KS); };
+  const auto pair_row = [&](int p) { return tile(2 * p + lane / 16) * 8 + lane % 8; };
+  met += 3 * grp;
+  // all lanes' writes before it are seen by the warps that wait
+  const auto arrive = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&met[i]);
+  };
+  const auto wait = [&](int i, int64_t c) {
+    return __all_sync(0xffffffffu,
+                      mbar_wait(&met[i], (uint32_t)(c & 1), abort_flag, a.err, kErrWaitOperand));
+  };
+  float s[DK / 8][4];
+  const float* Si =
+      a.S_in == nullptr ? nullptr : a.S_in + ((seq * a.H + h) * D + r0) * (int64_t)D + c0;
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j) {
+    float2 x = make_float2(0.f, 0.f), y = x;
+    if (Si != nullptr) {
+      x = *reinterpret_cast<const float2*>(Si + row * D + j * 8 + col);
+      y = *reinterpret_cast<const float2*>(Si + (row + 8) * D + j * 8 + col);
+    }
+    s[j][0] = x.x, s[j][1] = x.y, s[j][2] = y.x, s[j][3] = y.y;
+  }
+  // ldmatrix rows and columns of this lane: operands stored [n][k] and [k][n]
+  const int nk_r = (lane / 16) * 8 + lane % 8, nk_c = lane / 8 % 2;
+  const int kn_r = lane % 16, kn_c = (lane / 16) * 8;
+
+  for (int64_t c = 0; c < nc; ++c) {
+    const int st = (int)(c & 1);
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (uint32_t)((c >> 1) & 1), abort_flag, a.err,
+                                           kErrWaitFull)))
+      break;
+    uint8_t* base = smem + st * L::STAGE;
+    uint8_t* vp = base + 2 * L::KQ + grp * L::V;
+    const uint32_t sK = smem_u32(base), sQ = sK + L::KQ, sV = smem_u32(vp),
+                   sT = sK + 2 * L::KQ + RG * L::V, sP = sT + 3 * kTri;
+    const float* gates =
+        reinterpret_cast<const float*>(base + 2 * L::KQ + RG * L::V + 4 * kTri);
+    const int valid = len - c * kC < kC ? (int)(len - c * kC) : kC;
+
+    // r = S K^T (three parts of S), o = S Q^T (two), both [16 rows x 64 tokens], over this
+    // warp's columns of S.  The parts of r are sent off before the turn to o.
+    uint32_t sh[DK / 16][4], sm[DK / 16][4];
+    float rt[NT][4], ot[NT][4];  // this warp's tiles of the group's sums
+    {
+      float r[8][4] = {}, rs[8][4] = {};  // of the first part of S, of the small ones
+      uint32_t b[2][4];
+      ldsm4(sK + sw(kC, nk_r, c0 + nk_c * 8), b[0]);
+#pragma unroll
+      for (int k = 0; k < DK / 16; ++k) {
+        uint32_t lo[4];
+        split_a(s[2 * k], s[2 * k + 1], sh[k], sm[k], lo);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int f = k * 4 + p + 1;
+          uint32_t(&x)[4] = b[p % 2];
+          if (f < DK / 4)
+            ldsm4(sK + sw(kC, f % 4 * 16 + nk_r, c0 + f / 4 * 16 + nk_c * 8), b[f % 2]);
+          mma(rs[2 * p], sm[k], x[0], x[1]);
+          mma(rs[2 * p + 1], sm[k], x[2], x[3]);
+          mma(r[2 * p], sh[k], x[0], x[1]);
+          mma(r[2 * p + 1], sh[k], x[2], x[3]);
+          mma(rs[2 * p], lo, x[0], x[1]);
+          mma(rs[2 * p + 1], lo, x[2], x[3]);
+        }
+      }
+      float4* xp = reinterpret_cast<float4*>(x_part);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) r[t][y] += rs[t][y];
+        if (owner(t) != kw)
+          xp[(t * (KS - 1) + (kw < owner(t) ? kw : kw - 1)) * 32 + lane] =
+              make_float4(r[t][0], r[t][1], r[t][2], r[t][3]);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int w = 0; w < KS; ++w)  // registers have no index: pick by this warp's number
+          if (w == kw)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              rt[j][y] = r[j / 2 * 2 * KS + (j % 2 == 0 ? w : 2 * KS - 1 - w)][y];
+      arrive(0);
+    }
+    {
+      float o[8][4] = {};
+      uint32_t b[2][4];
+      ldsm4(sQ + sw(kC, nk_r, c0 + nk_c * 8), b[0]);
+#pragma unroll
+      for (int e = 0; e < DK / 4; ++e) {  // 4 pairs of tiles for each 16 columns
+        const int k = e / 4, p = e % 4, f = e + 1;
+        if (f < DK / 4) ldsm4(sQ + sw(kC, f % 4 * 16 + nk_r, c0 + f / 4 * 16 + nk_c * 8), b[f % 2]);
+        mma(o[2 * p], sh[k], b[e % 2][0], b[e % 2][1]);
+        mma(o[2 * p + 1], sh[k], b[e % 2][2], b[e % 2][3]);
+        mma(o[2 * p], sm[k], b[e % 2][0], b[e % 2][1]);
+        mma(o[2 * p + 1], sm[k], b[e % 2][2], b[e % 2][3]);
+      }
+      float4* xp = reinterpret_cast<float4*>(x_part + L::X_PART);
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (owner(t) != kw)
+          xp[(t * (KS - 1) + (kw < owner(t) ? kw : kw - 1)) * 32 + lane] =
+              make_float4(o[t][0], o[t][1], o[t][2], o[t][3]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int w = 0; w < KS; ++w)
+          if (w == kw)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              ot[j][y] = o[j / 2 * 2 * KS + (j % 2 == 0 ? w : 2 * KS - 1 - w)][y];
+    }
+    const auto add_parts = [&](float(&x)[NT][4], const uint8_t* from) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int w = 0; w < KS - 1; ++w) {
+          const float4 v =
+              reinterpret_cast<const float4*>(from)[(tile(j) * (KS - 1) + w) * 32 + lane];
+          x[j][0] += v.x, x[j][1] += v.y, x[j][2] += v.z, x[j][3] += v.w;
+        }
+    };
+    if (!wait(0, c)) break;
+    add_parts(rt, x_part);
+    // r = beta (v - gamma r)
+#pragma unroll
+    for (int p = 0; p < NT / 2; ++p) {
+      uint32_t v[4];  // (tokens, rows 0-7), (tokens, rows 8-15) of a tile, then of the next
+      ldsm4_t(sV + sw32(pair_row(p), nk_c), v);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = tile(2 * p + x) * 8 + col;
+        const float2 ga = *reinterpret_cast<const float2*>(gates + t);
+        const float2 be = *reinterpret_cast<const float2*>(gates + 2 * kC + t);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t w = v[2 * x + y / 2];
+          const float vv = __uint_as_float(y % 2 ? w & 0xffff0000u : w << 16);
+          const float gg = y % 2 ? ga.y : ga.x, bb = y % 2 ? be.y : be.x;
+          rt[2 * p + x][y] = t + y % 2 < valid ? bb * (vv - gg * rt[2 * p + x][y]) : 0.f;
+        }
+      }
+    }
+    // u = r T^T: tokens i take tokens j <= i
+    float ut[NT][4] = {};
+    {
+      // the parts of r as A operands [tokens / 16][part][lane]: a tile is half of one
+      uint2* xr = reinterpret_cast<uint2*>(x_r);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint32_t hi[2], mid[2], lo[2];
+        split3(rt[j][0], rt[j][1], hi[0], mid[0], lo[0]);
+        split3(rt[j][2], rt[j][3], hi[1], mid[1], lo[1]);
+        const int t = tile(j);
+        uint2* d = xr + (t / 2 * 3 * 32 + lane) * 2 + t % 2;
+        d[0] = make_uint2(hi[0], hi[1]);
+        d[64] = make_uint2(mid[0], mid[1]);
+        d[128] = make_uint2(lo[0], lo[1]);
+      }
+      arrive(1);
+      if (!wait(1, c)) break;
+      float us[2][NT][4] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k > tile(NT - 1) / 2) break;
+        uint32_t hi[4], mid[4], lo[4];
+        const uint4* d = reinterpret_cast<const uint4*>(xr) + k * 3 * 32 + lane;
+        load_a(d, hi);
+        load_a(d + 32, mid);
+        load_a(d + 64, lo);
+#pragma unroll
+        for (int p = 0; p < NT / 2; ++p) {
+          if (k > tile(2 * p + 1) / 2) continue;
+          uint32_t b[3][4];
+          // strip k of T holds rows from 16 k on; a pair's first tile may lie above
+          const int tr = pair_row(p) < 16 * k ? 16 * k : pair_row(p);
+#pragma unroll
+          for (int x = 0; x < 3; ++x) ldsm4(sT + x * kTri + tri(tr, k * 16 + nk_c * 8), b[x]);
+          if (k <= tile(2 * p) / 2) {
+            mma(ut[2 * p], hi, b[0][0], b[0][1]);
+            mma(us[0][2 * p], mid, b[0][0], b[0][1]);
+            mma(us[1][2 * p], hi, b[1][0], b[1][1]);
+            mma(us[0][2 * p], lo, b[0][0], b[0][1]);
+            mma(us[1][2 * p], mid, b[1][0], b[1][1]);
+            mma(us[0][2 * p], hi, b[2][0], b[2][1]);
+          }
+          mma(ut[2 * p + 1], hi, b[0][2], b[0][3]);
+          mma(us[0][2 * p + 1], mid, b[0][2], b[0][3]);
+          mma(us[1][2 * p + 1], hi, b[1][2], b[1][3]);
+          mma(us[0][2 * p + 1], lo, b[0][2], b[0][3]);
+          mma(us[1][2 * p + 1], mid, b[1][2], b[1][3]);
+          mma(us[0][2 * p + 1], hi, b[2][2], b[2][3]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) ut[j][y] += us[0][j][y] + us[1][j][y];
+    }
+    // parts of u (for o) and of rest u (for S)
+    uint4* xu = reinterpret_cast<uint4*>(x_u);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int t = tile(j);
+      uint32_t hi[2], mid[2], lo[2];
+      uint2* d = reinterpret_cast<uint2*>(xu) + (t / 2 * 5 * 32 + lane) * 2 + t % 2;
+      split3(ut[j][0], ut[j][1], hi[0], mid[0], lo[0]);
+      split3(ut[j][2], ut[j][3], hi[1], mid[1], lo[1]);
+      d[0] = make_uint2(hi[0], hi[1]);
+      d[64] = make_uint2(mid[0], mid[1]);
+      const float2 re = *reinterpret_cast<const float2*>(gates + kC + t * 8 + col);
+      split3(ut[j][0] * re.x, ut[j][1] * re.y, hi[0], mid[0], lo[0]);
+      split3(ut[j][2] * re.x, ut[j][3] * re.y, hi[1], mid[1], lo[1]);
+      d[128] = make_uint2(hi[0], hi[1]);
+      d[192] = make_uint2(mid[0], mid[1]);
+      d[256] = make_uint2(lo[0], lo[1]);
+    }
+    arrive(2);
+    // o = scale gamma o + u P^T
+    add_parts(ot, x_part + L::X_PART);  // written before r's parts were
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const float2 ga = *reinterpret_cast<const float2*>(gates + tile(j) * 8 + col);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) ot[j][y] *= a.scale * (y % 2 ? ga.y : ga.x);
+    }
+    if (!wait(2, c)) break;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k > tile(NT - 1) / 2) break;
+      uint32_t hi[4], mid[4];
+      load_a(xu + k * 5 * 32 + lane, hi);
+      load_a(xu + k * 5 * 32 + 32 + lane, mid);
+#pragma unroll
+      for (int p = 0; p < NT / 2; ++p) {
+        if (k > tile(2 * p + 1) / 2) continue;
+        uint32_t b[4];
+        const int tr = pair_row(p) < 16 * k ? 16 * k : pair_row(p);
+        ldsm4(sP + tri(tr, k * 16 + nk_c * 8), b);
+        const bool first = k <= tile(2 * p) / 2;
+        mma(ot[2 * p + 1], hi, b[2], b[3]);
+        if (first) mma(ot[2 * p], hi, b[0], b[1]);
+        mma(ot[2 * p + 1], mid, b[2], b[3]);
+        if (first) mma(ot[2 * p], mid, b[0], b[1]);
+      }
+    }
+    // O over this group's V (each warp over the tokens it has read), then out
+#pragma unroll
+    for (int p = 0; p < NT / 2; ++p) {
+      const uint32_t w[4] = {pack_bf16x2(ot[2 * p][0], ot[2 * p][1]),
+                             pack_bf16x2(ot[2 * p][2], ot[2 * p][3]),
+                             pack_bf16x2(ot[2 * p + 1][0], ot[2 * p + 1][1]),
+                             pack_bf16x2(ot[2 * p + 1][2], ot[2 * p + 1][3])};
+      stsm4_t(sV + sw32(pair_row(p), nk_c), w);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < NT / 2; ++p) {
+      const int t = tile(2 * p + lane / 16) * 8 + lane / 2 % 8;
+      const uint4 w = *reinterpret_cast<const uint4*>(vp + sw32(t, lane % 2));
+      if (t < valid)
+        *reinterpret_cast<uint4*>(a.O + (sr.t0 + c * kC + t) * (int64_t)a.H * D + h * D + r0 +
+                                  (lane % 2) * 8) = w;
+    }
+    // S = gamma_64 S + (rest u) K
+    {
+      uint32_t hi[4][4], mid[4][4], lo[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        load_a(xu + k * 5 * 32 + 64 + lane, hi[k]);
+        load_a(xu + k * 5 * 32 + 96 + lane, mid[k]);
+        load_a(xu + k * 5 * 32 + 128 + lane, lo[k]);
+      }
+      const float gl = gates[kC - 1];
+      // Rows of K behind the sequence may hold anything: they count as zero here, where
+      // tokens are summed (elsewhere they only reach their own columns).
+      const auto update = [&](auto tail) {
+        uint32_t b[2][4];
+        ldsm4_t(sK + sw(kC, kn_r, c0 + kn_c), b[0]);
+        float d0[4] = {}, d1[4] = {}, e0[4] = {}, e1[4] = {};
+#pragma unroll
+        for (int e = 0; e < DK / 4; ++e) {  // 4 steps of 16 tokens for each 16 columns
+          const int j = e / 4, k = e % 4, f = e + 1;
+          uint32_t(&x)[4] = b[e % 2];
+          if (f < DK / 4)
+            ldsm4_t(sK + sw(kC, f % 4 * 16 + kn_r, c0 + f / 4 * 16 + kn_c), b[f % 2]);
+          if (decltype(tail)::value) {
+            const uint32_t k0 = keep_pair(k * 16 + col, valid),
+                           k1 = keep_pair(k * 16 + 8 + col, valid);
+            x[0] &= k0, x[1] &= k1, x[2] &= k0, x[3] &= k1;
+          }
+          mma(e0, mid[k], x[0], x[1]);
+          mma(e1, mid[k], x[2], x[3]);
+          mma(d0, hi[k], x[0], x[1]);
+          mma(d1, hi[k], x[2], x[3]);
+          mma(e0, lo[k], x[0], x[1]);
+          mma(e1, lo[k], x[2], x[3]);
+          if (k == 3)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              s[2 * j][y] = fmaf(gl, s[2 * j][y], d0[y] + e0[y]);
+              s[2 * j + 1][y] = fmaf(gl, s[2 * j + 1][y], d1[y] + e1[y]);
+              d0[y] = d1[y] = e0[y] = e1[y] = 0.f;
+            }
+        }
+      };
+      if (valid == kC)
+        update(std::false_type());
+      else
+        update(std::true_type());
+    }
+    fence_proxy_async_smem();  // O's stores into the stage come before the next loads
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+  }
+
+  if (a.S_out != nullptr) {
+    float* So = a.S_out + ((seq * a.H + h) * D + r0) * (int64_t)D + c0;
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j) {
+      *reinterpret_cast<float2*>(So + row * D + j * 8 + col) = make_float2(s[j][0], s[j][1]);
+      *reinterpret_cast<float2*>(So + (row + 8) * D + j * 8 + col) = make_float2(s[j][2], s[j][3]);
+    }
+  }
+}
+
+template <int D, bool GRAD>
+cudaError_t launch_chunks(const DeltaArgs& a, uint8_t* blocks, cudaStream_t st) {
+  const int need = 2 * kC * D * 2, fp = 6 * 32 * kLS * 4;
+  const int smem = (need > fp ? need : fp) + 1024;
+  const cudaError_t e = ensure_smem_attr(delta_chunk_kernel<D, GRAD>, smem);
+  if (e != cudaSuccess) return e;
+  const ChunkArgs k = {static_cast<const __nv_bfloat16*>(a.Q), static_cast<const __nv_bfloat16*>(a.K),
+                       a.g, a.b, a.ldq, a.ldk, a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, blocks};
+  TraceScope ts("delta_chunk", st);
+  delta_chunk_kernel<D, GRAD>
+      <<<dim3((unsigned)chunk_slots(a), (unsigned)a.H), kChunkThreads, smem, st>>>(k);
+  return cudaGetLastError();
+}
+
+template <int D, int KS, int RG>
+cudaError_t launch_state(const DeltaArgs& a, const float* S_in, float* S_out, void* O,
+                         const uint8_t* blocks, cudaStream_t st) {
+  using L = SK<D, KS, RG>;
+  int* err = device_error_ptr();
+  if (err == nullptr) return cudaErrorInvalidDevice;
+  CUtensorMap mQ = {}, mK = {}, mV = {};
+  if (a.n > 0 && (!head_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D, D) ||
+                  !head_map(&mK, a.K, a.n, a.ldk, a.Hk * D, D) ||
+                  !strip_map(&mV, a.V, a.n, a.ldv, a.H * D)))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = ensure_smem_attr(delta_state_kernel<D, KS, RG>, L::SMEM);
+  if (e != cudaSuccess) return e;
+  const StateArgs k = {a.n, a.offsets, a.H, a.Hk, a.scale, blocks, S_in, S_out,
+                       static_cast<__nv_bfloat16*>(O), err};
+  TraceScope ts("delta_state", st);
+  delta_state_kernel<D, KS, RG><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
+                                  L::THREADS, L::SMEM, st>>>(mQ, mK, mV, k);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t delta_prepare(const DeltaArgs& a, bool gradient, uint8_t* blocks, cudaStream_t st) {
+  if (a.n == 0) return cudaSuccess;
+  if (gradient)
+    return a.d == 64    ? launch_chunks<64, true>(a, blocks, st)
+           : a.d == 128 ? launch_chunks<128, true>(a, blocks, st)
+                        : launch_chunks<256, true>(a, blocks, st);
+  return a.d == 64    ? launch_chunks<64, false>(a, blocks, st)
+         : a.d == 128 ? launch_chunks<128, false>(a, blocks, st)
+                      : launch_chunks<256, false>(a, blocks, st);
+}
+
+size_t delta_tc_bytes(const DeltaArgs& a) {
+  return a.n == 0 ? 0 : (size_t)chunk_slots(a) * a.H * chunk_bytes(1);
+}
+
+cudaError_t delta_tc(const DeltaArgs& a, const float* S_in, float* S_out, void* O, void* ws,
+                     cudaStream_t st) {
+  uint8_t* blocks = static_cast<uint8_t*>(ws);
+  const cudaError_t e = delta_prepare(a, false, blocks, st);
+  if (e != cudaSuccess) return e;
+  // Groups of 16 rows of S.  Where there are no more of them than SMs, four warps
+  // share each (one on each quarter of an SM: 74 us against 97 us for a 1,374-token
+  // sequence of 4 heads of 256); else two do, with half the exchange for each product
+  // (16,411 tokens, 13 sequences, 16 heads of 128: 457 us against 596 us).
+  const bool few = a.seqs * a.H * (a.d / 16) <= num_sms();
+  if (a.d == 64)
+    return few ? launch_state<64, 4, 1>(a, S_in, S_out, O, blocks, st)
+               : launch_state<64, 2, 2>(a, S_in, S_out, O, blocks, st);
+  if (a.d == 128)
+    return few ? launch_state<128, 4, 1>(a, S_in, S_out, O, blocks, st)
+               : launch_state<128, 2, 2>(a, S_in, S_out, O, blocks, st);
+  return launch_state<256, 4, 1>(a, S_in, S_out, O, blocks, st);
+}
+
+}  // namespace ttt

@@ -76,7 +76,8 @@ ttt_status check_sequences(const DeltaArgs& a) {
 }
 
 size_t delta_bytes(const DeltaArgs& a, bool backward) {
-  return backward ? ttt::delta_tokens_backward_bytes(a) : 0;
+  if (backward) return ttt::delta_tokens_backward_bytes(a);
+  return a.bf16 ? ttt::delta_tc_bytes(a) : 0;
 }
 
 }  // namespace
@@ -109,7 +110,8 @@ ttt_status ttt_delta_chunk(const ttt_delta_config* cfg, const ttt_delta_tokens* 
   const size_t need = delta_bytes(a, false);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
   if (a.seqs == 0) return TTT_OK;
-  return cuda_status(ttt::delta_tokens(a, S_in, S_out, O, cs(stream)));
+  return cuda_status(a.bf16 ? ttt::delta_tc(a, S_in, S_out, O, workspace, cs(stream))
+                            : ttt::delta_tokens(a, S_in, S_out, O, cs(stream)));
 }
 
 ttt_status ttt_delta_step(const ttt_delta_config* cfg, const ttt_delta_tokens* tok,

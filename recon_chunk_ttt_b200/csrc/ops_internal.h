@@ -34,6 +34,11 @@ cudaError_t delta_tokens_backward(const DeltaArgs& a, const float* S_in, const v
 cudaError_t delta_share(const DeltaArgs& a, const float* part_q, const float* part_k, void* dQ,
                         void* dK, cudaStream_t st);
 
+// ---- tensor cores, chunks of 64 tokens (kernels_delta_tc.cu): bf16 tokens ---------
+size_t delta_tc_bytes(const DeltaArgs& a);
+cudaError_t delta_tc(const DeltaArgs& a, const float* S_in, float* S_out, void* O, void* ws,
+                     cudaStream_t st);
+
 // ---- rotary positions (kernels_rope.cu) --------------------------------------
 struct RopeArgs {
   int d, rot[3];
