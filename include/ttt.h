@@ -413,8 +413,9 @@ ttt_status ttt_delta_backward(const ttt_delta_config* cfg, const ttt_delta_token
  *   TTT_ROPE_FREQ_HEAD: e = j / (R/2), over the whole head
  *   (x, y) -> (x cos - y sin, y cos + x sin); inverse != 0 turns back, which
  * is also the gradient: it maps dQ_out, dK_out to dQ, dK.
- * Angles are formed and reduced in fp64, the rotation is fp32, rounded once.
- *  - d = 64, 128 or 256; rot[] even, >= 0, sum 2..d; base[] finite, > 0.  With
+ * Angles are formed and reduced exactly to 2^-32 of a turn, the rotation is
+ * fp32, rounded once.
+ *  - d = 64, 128 or 256; rot[] even, >= 0, sum 2..d; base[] finite, >= 1.  With
  *    FREQ_HEAD every pair still uses its own axis' base.
  *  - positions: float [n][3] (whole numbers are exact to 2^24); fractions and
  *    negative positions are fine.  A position of infinity or NaN gives NaN.

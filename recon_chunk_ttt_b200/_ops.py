@@ -41,13 +41,13 @@ DEVICE_ERR_OFFSETS = 8  # TTT_DEVICE_ERR_OFFSETS
 ROPE_HALF, ROPE_PAIRS = 0, 1
 ROPE_FREQ_AXIS, ROPE_FREQ_HEAD = 0, 1
 
-_typed = False
+_typed = None
 
 
 def _lib():
     global _typed
-    L = B.lib()
-    if not _typed:
+    if _typed is None:
+        L = B.lib()
         dc, dt = ctypes.POINTER(ttt_delta_config), ctypes.POINTER(ttt_delta_tokens)
         rc, nc = ctypes.POINTER(ttt_rope_config), ctypes.POINTER(ttt_norm_config)
         for name, args, res in (
@@ -63,8 +63,8 @@ def _lib():
                                              _SZ, _P], ctypes.c_int)):
             f = getattr(L, name)
             f.argtypes, f.restype = args, res
-        _typed = True
-    return L
+        _typed = L
+    return _typed
 
 
 def _want(ok, what, why):
@@ -76,53 +76,67 @@ def _token(precision):
     return torch.float32 if precision == B.PREC_FP32_CHECK else torch.bfloat16
 
 
-class _Call:
-    """One call's checks: every tensor on the first one's device, of its type
-    and shape; the device is made current around the library's call."""
+def _device(what, t):
+    """The index of the GPU a call's first tensor is on; every other tensor
+    must be there too."""
+    _want(isinstance(t, torch.Tensor) and t.is_cuda, what, "tensors must be on a GPU")
+    return t.get_device()
 
-    def __init__(self, what, first):
-        self.what = what
-        _want(isinstance(first, torch.Tensor) and first.is_cuda, what, "tensors must be on a GPU")
-        self.device = first.device
 
-    def check(self, name, t, dtype, shape, optional=False, rows=False):
-        """The tensor's pointer.  `rows`: a matrix whose rows may lie apart."""
-        if t is None:
-            _want(optional, self.what, f"{name} is missing")
-            return None
-        _want(t.device == self.device, self.what, f"{name} is on {t.device}, not {self.device}")
-        _want(t.dtype == dtype, self.what, f"{name} is {t.dtype}, not {dtype}")
-        _want(tuple(t.shape) == tuple(shape), self.what,
-              f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+def _check(what, dev, name, t, dtype, shape, rows=False):
+    """The tensor's pointer.  `rows`: a matrix whose rows may lie apart.  One-token
+    calls cost microseconds: the messages are put together only when one is due."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr()
         if rows:
-            _want(t.stride(1) == 1 or t.shape[1] <= 1, self.what, f"{name}: a row's values lie apart")
-            _want(t.shape[0] <= 1 or t.stride(0) >= t.shape[1], self.what, f"{name}: rows overlap")
-        else:
-            _want(t.is_contiguous(), self.what, f"{name} is not contiguous")
-        return t.data_ptr()
+            _want(t.stride(1) == 1 or shape[1] <= 1, what, f"{name}: a row's values lie apart")
+            _want(shape[0] <= 1 or t.stride(0) >= shape[1], what, f"{name}: rows overlap")
+            return t.data_ptr()
+    _want(t.get_device() == dev, what, f"{name} is on {t.device}, not on GPU {dev}")
+    _want(t.dtype == dtype, what, f"{name} is {t.dtype}, not {dtype}")
+    _want(t.shape == shape, what, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    _want(False, what, f"{name} is not contiguous")
 
-    def out(self, name, t, dtype, shape):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        self.check(name, t, dtype, shape)
-        return t
 
-    def workspace(self, t, nbytes):
-        if t is None:
-            t = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device)
-        _want(t.device == self.device and t.is_contiguous(), self.what,
-              "workspace must be contiguous, on the tensors' device")
-        return t, t.numel() * t.element_size()
+def _maybe(what, dev, name, t, dtype, shape):
+    return None if t is None else _check(what, dev, name, t, dtype, shape)
 
-    def run(self, fn, args, stream):
-        with torch.cuda.device(self.device):
-            st = torch.cuda.current_stream().cuda_stream if stream is None else B._stream(stream)
-            B._check(fn(*args, st), self.what)
+
+def _out(what, dev, name, t, dtype, shape):
+    """An output and its pointer, allocated if it is not given."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _check(what, dev, name, t, dtype, shape)
+
+
+def _space(what, dev, t, nbytes):
+    if t is None:
+        t = torch.empty(max(nbytes(), 1), dtype=torch.uint8, device=dev)
+    _want(t.get_device() == dev and t.is_contiguous(), what,
+          "workspace must be contiguous, on the tensors' device")
+    return t, t.data_ptr(), t.numel() * t.element_size()
+
+
+def _run(what, dev, fn, args, stream):
+    """The library's call with the tensors' device current, on `stream` or that
+    device's current stream."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run(what, dev, fn, args, stream)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    status = fn(*args, stream)
+    if status != B.TTT_OK:
+        raise B.TTTError(status, what)
 
 
 def _ld(t):
     """Elements between rows (a single row's stride may be anything)."""
-    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.shape[1]), 1)
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
 # ------------------------------------------------------------------ delta rule
@@ -145,37 +159,35 @@ def alloc_delta_workspace(cfg: ttt_delta_config, n: int, seqs: int = 1, backward
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device or "cuda")
 
 
-def _delta_tokens(c, cfg, Q, K, V, log_decay, beta, offsets, seqs):
-    n, tdt = int(Q.shape[0]), _token(cfg.precision)
-    qk, hv = cfg.qk_heads * cfg.d, cfg.heads * cfg.d
-    t = ttt_delta_tokens()
-    t.Q = c.check("Q", Q, tdt, (n, qk), rows=True)
-    t.K = c.check("K", K, tdt, (n, qk), rows=True)
-    t.V = c.check("V", V, tdt, (n, hv), rows=True)
-    t.log_decay = c.check("log_decay", log_decay, torch.float32, (n, cfg.heads))
-    t.beta = c.check("beta", beta, torch.float32, (n, cfg.heads))
-    t.ldq, t.ldk, t.ldv, t.n = _ld(Q), _ld(K), _ld(V), n
-    if offsets is not None:
-        t.offsets = c.check("offsets", offsets, torch.int64, (seqs + 1,))
-    t.seqs = seqs
-    return t
+def _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs):
+    """(device, tokens of the call, token type)."""
+    dev, tdt = _device(what, Q), _token(cfg.precision)
+    n, heads, d = Q.shape[0], cfg.heads, cfg.d
+    qk, hv, per = (n, cfg.qk_heads * d), (n, heads * d), (n, heads)
+    f32 = torch.float32
+    return dev, ttt_delta_tokens(
+        _check(what, dev, "Q", Q, tdt, qk, True), _check(what, dev, "K", K, tdt, qk, True),
+        _check(what, dev, "V", V, tdt, hv, True),
+        _check(what, dev, "log_decay", log_decay, f32, per), _check(what, dev, "beta", beta, f32, per),
+        _ld(Q), _ld(K), _ld(V), n,
+        _maybe(what, dev, "offsets", offsets, torch.int64, (seqs + 1,)), seqs), tdt
 
 
 def ttt_delta_chunk(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S=None, offsets=None,
                     S_out=None, O=None, workspace=None, stream=None):
     """The gated delta rule over packed sequences (offsets int64 [seqs + 1] on
     the device, or one sequence); returns (O, S_out).  S_out may be S."""
-    c = _Call("ttt_delta_chunk", Q)
-    seqs = 1 if offsets is None else int(offsets.shape[0]) - 1
-    t = _delta_tokens(c, cfg, Q, K, V, log_decay, beta, offsets, seqs)
-    shape = (seqs, cfg.heads, cfg.d, cfg.d)
-    c.check("S", S, torch.float32, shape, optional=True)
-    S_out = c.out("S_out", S_out, torch.float32, shape)
-    O = c.out("O", O, _token(cfg.precision), (t.n, cfg.heads * cfg.d))
-    ws, nbytes = c.workspace(workspace, ttt_delta_workspace_bytes(cfg, t.n, seqs)
-                             if workspace is None else 0)
-    c.run(_lib().ttt_delta_chunk, (ctypes.byref(cfg), ctypes.byref(t), B._ptr(S), B._ptr(S_out),
-                                   B._ptr(O), B._ptr(ws), nbytes), stream)
+    what = "ttt_delta_chunk"
+    seqs = 1 if offsets is None else offsets.shape[0] - 1
+    dev, t, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs)
+    shape, f32 = (seqs, cfg.heads, cfg.d, cfg.d), torch.float32
+    pS = _maybe(what, dev, "S", S, f32, shape)
+    S_out, pSo = _out(what, dev, "S_out", S_out, f32, shape)
+    O, pO = _out(what, dev, "O", O, tdt, (t.n, cfg.heads * cfg.d))
+    workspace, pW, nbytes = _space(what, dev, workspace,
+                                   lambda: ttt_delta_workspace_bytes(cfg, t.n, seqs))
+    _run(what, dev, _lib().ttt_delta_chunk,
+         (ctypes.byref(cfg), ctypes.byref(t), pS, pSo, pO, pW, nbytes), stream)
     return O, S_out
 
 
@@ -184,17 +196,17 @@ def ttt_delta_step(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S, slots=Non
     """One token for each request on a pool of states S [pool, heads, d, d]
     (slots: int32 [n], -1 for padding; without them request i has state i).
     The new states go to S_out, or into S where that is not given; returns O."""
-    c = _Call("ttt_delta_step", Q)
-    t = _delta_tokens(c, cfg, Q, K, V, log_decay, beta, None, int(Q.shape[0]))
-    _want(isinstance(S, torch.Tensor) and S.dim() == 4, c.what, "S must be [pool, heads, d, d]")
-    pool = int(S.shape[0])
-    shape = (pool, cfg.heads, cfg.d, cfg.d)
-    c.check("S", S, torch.float32, shape)
-    S_out = S if S_out is None else c.out("S_out", S_out, torch.float32, shape)
-    c.check("slots", slots, torch.int32, (t.n,), optional=True)
-    O = c.out("O", O, _token(cfg.precision), (t.n, cfg.heads * cfg.d))
-    c.run(_lib().ttt_delta_step, (ctypes.byref(cfg), ctypes.byref(t), B._ptr(slots), pool,
-                                  B._ptr(S), B._ptr(S_out), B._ptr(O)), stream)
+    what = "ttt_delta_step"
+    dev, t, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, None, Q.shape[0])
+    _want(isinstance(S, torch.Tensor) and S.dim() == 4, what, "S must be [pool, heads, d, d]")
+    pool = S.shape[0]
+    shape, f32 = (pool, cfg.heads, cfg.d, cfg.d), torch.float32
+    pS = _check(what, dev, "S", S, f32, shape)
+    pSo = pS if S_out is None else _check(what, dev, "S_out", S_out, f32, shape)
+    pI = _maybe(what, dev, "slots", slots, torch.int32, (t.n,))
+    O, pO = _out(what, dev, "O", O, tdt, (t.n, cfg.heads * cfg.d))
+    _run(what, dev, _lib().ttt_delta_step,
+         (ctypes.byref(cfg), ctypes.byref(t), pI, pool, pS, pSo, pO), stream)
     return O
 
 
@@ -203,26 +215,26 @@ def ttt_delta_backward(cfg: ttt_delta_config, Q, K, V, log_decay, beta, dO, S=No
                        dS=None, workspace=None, stream=None):
     """Gradients of sum(dO * O) + sum(dS_out * S_out) of ttt_delta_chunk:
     (dQ, dK, dV, dlog_decay, dbeta, dS).  dS may be dS_out."""
-    c = _Call("ttt_delta_backward", Q)
-    seqs = 1 if offsets is None else int(offsets.shape[0]) - 1
-    t = _delta_tokens(c, cfg, Q, K, V, log_decay, beta, offsets, seqs)
-    tdt, n = _token(cfg.precision), t.n
+    what = "ttt_delta_backward"
+    seqs = 1 if offsets is None else offsets.shape[0] - 1
+    dev, t, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs)
+    n, f32 = t.n, torch.float32
+    qk, hv, per = (n, cfg.qk_heads * cfg.d), (n, cfg.heads * cfg.d), (n, cfg.heads)
     shape = (seqs, cfg.heads, cfg.d, cfg.d)
-    c.check("S", S, torch.float32, shape, optional=True)
-    c.check("dO", dO, tdt, (n, cfg.heads * cfg.d))
-    c.check("dS_out", dS_out, torch.float32, shape, optional=True)
-    dQ = c.out("dQ", dQ, tdt, (n, cfg.qk_heads * cfg.d))
-    dK = c.out("dK", dK, tdt, (n, cfg.qk_heads * cfg.d))
-    dV = c.out("dV", dV, tdt, (n, cfg.heads * cfg.d))
-    dlog_decay = c.out("dlog_decay", dlog_decay, torch.float32, (n, cfg.heads))
-    dbeta = c.out("dbeta", dbeta, torch.float32, (n, cfg.heads))
-    dS = c.out("dS", dS, torch.float32, shape)
-    ws, nbytes = c.workspace(workspace, ttt_delta_workspace_bytes(cfg, n, seqs, True)
-                             if workspace is None else 0)
-    c.run(_lib().ttt_delta_backward,
-          (ctypes.byref(cfg), ctypes.byref(t), B._ptr(S), B._ptr(dO), B._ptr(dS_out), B._ptr(dQ),
-           B._ptr(dK), B._ptr(dV), B._ptr(dlog_decay), B._ptr(dbeta), B._ptr(dS), B._ptr(ws),
-           nbytes), stream)
+    pS = _maybe(what, dev, "S", S, f32, shape)
+    pG = _check(what, dev, "dO", dO, tdt, hv)
+    pE = _maybe(what, dev, "dS_out", dS_out, f32, shape)
+    dQ, p1 = _out(what, dev, "dQ", dQ, tdt, qk)
+    dK, p2 = _out(what, dev, "dK", dK, tdt, qk)
+    dV, p3 = _out(what, dev, "dV", dV, tdt, hv)
+    dlog_decay, p4 = _out(what, dev, "dlog_decay", dlog_decay, f32, per)
+    dbeta, p5 = _out(what, dev, "dbeta", dbeta, f32, per)
+    dS, p6 = _out(what, dev, "dS", dS, f32, shape)
+    workspace, pW, nbytes = _space(what, dev, workspace,
+                                   lambda: ttt_delta_workspace_bytes(cfg, n, seqs, True))
+    _run(what, dev, _lib().ttt_delta_backward,
+         (ctypes.byref(cfg), ctypes.byref(t), pS, pG, pE, p1, p2, p3, p4, p5, p6, pW, nbytes),
+         stream)
     return dQ, dK, dV, dlog_decay, dbeta, dS
 
 
@@ -241,29 +253,28 @@ def ttt_rope(cfg: ttt_rope_config, Q, K, positions, Q_out=None, K_out=None, inve
     """Rotate the heads of Q [n, q_heads*d] and K [n, k_heads*d] (or None) by
     positions float [n, 3]; returns (Q_out, K_out).  Q_out may be Q and K_out
     K.  inverse=True turns back: the gradient."""
-    c = _Call("ttt_rope", Q)
-    n, tdt = int(Q.shape[0]), _token(cfg.precision)
+    what = "ttt_rope"
+    dev, tdt = _device(what, Q), _token(cfg.precision)
+    n = Q.shape[0]
 
     def side(name, x, y):
+        """(heads, input pointer and row distance, output, its pointer and distance)"""
         if x is None:
-            _want(y is None, c.what, f"{name}_out without {name}")
-            return 0, None
-        _want(x.dim() == 2 and x.shape[1] % cfg.d == 0, c.what, f"{name} must be [n, heads * d]")
-        c.check(name, x, tdt, (n, int(x.shape[1])), rows=True)
+            _want(y is None, what, f"{name}_out without {name}")
+            return 0, None, 0, None, None, 0
+        _want(x.dim() == 2 and x.shape[1] % cfg.d == 0, what, f"{name} must be [n, heads * d]")
+        w = x.shape[1]
+        p = _check(what, dev, name, x, tdt, (n, w), True)
         if y is None:
-            y = torch.empty((n, int(x.shape[1])), dtype=tdt, device=c.device)
-        else:
-            c.check(name + "_out", y, tdt, (n, int(x.shape[1])), rows=True)
-        return int(x.shape[1]) // cfg.d, y
+            y = torch.empty((n, w), dtype=tdt, device=dev)
+            return w // cfg.d, p, _ld(x), y, y.data_ptr(), w
+        return w // cfg.d, p, _ld(x), y, _check(what, dev, name + "_out", y, tdt, (n, w), True), _ld(y)
 
-    hq, Q_out = side("Q", Q, Q_out)
-    hk, K_out = side("K", K, K_out)
-    c.check("positions", positions, torch.float32, (n, 3))
-    none = hk == 0
-    c.run(_lib().ttt_rope,
-          (ctypes.byref(cfg), B._ptr(Q), _ld(Q), hq, None if none else B._ptr(K),
-           0 if none else _ld(K), hk, B._ptr(positions), n, B._ptr(Q_out), _ld(Q_out),
-           None if none else B._ptr(K_out), 0 if none else _ld(K_out), 1 if inverse else 0), stream)
+    hq, pQ, lq, Q_out, pQo, lqo = side("Q", Q, Q_out)
+    hk, pK, lk, K_out, pKo, lko = side("K", K, K_out)
+    pP = _check(what, dev, "positions", positions, torch.float32, (n, 3))
+    _run(what, dev, _lib().ttt_rope, (ctypes.byref(cfg), pQ, lq, hq, pK, lk, hk, pP, n, pQo, lqo, pKo,
+                                      lko, 1 if inverse else 0), stream)
     return Q_out, K_out
 
 
@@ -281,33 +292,35 @@ def ttt_layer_norm(cfg: ttt_norm_config, X, weight=None, bias=None, Y=None, stat
                    stream=None):
     """Layer norm of the rows of X [rows, dim]; returns (Y, stats), stats
     float [rows, 2] holding each row's mean and 1/sqrt(var + eps)."""
-    c = _Call("ttt_layer_norm", X)
-    rows, dim, tdt = int(X.shape[0]), int(cfg.dim), _token(cfg.precision)
-    c.check("X", X, tdt, (rows, dim), rows=True)
-    c.check("weight", weight, torch.float32, (dim,), optional=True)
-    c.check("bias", bias, torch.float32, (dim,), optional=True)
-    Y = c.out("Y", Y, tdt, (rows, dim))
-    stats = c.out("stats", stats, torch.float32, (rows, 2))
-    c.run(_lib().ttt_layer_norm, (ctypes.byref(cfg), B._ptr(X), _ld(X), rows, B._ptr(weight),
-                                  B._ptr(bias), B._ptr(Y), B._ptr(stats)), stream)
+    what = "ttt_layer_norm"
+    dev, tdt, f32 = _device(what, X), _token(cfg.precision), torch.float32
+    dim = cfg.dim
+    rows = X.shape[0]
+    pX = _check(what, dev, "X", X, tdt, (rows, dim), True)
+    pw = _maybe(what, dev, "weight", weight, f32, (dim,))
+    pb = _maybe(what, dev, "bias", bias, f32, (dim,))
+    Y, pY = _out(what, dev, "Y", Y, tdt, (rows, dim))
+    stats, ps = _out(what, dev, "stats", stats, f32, (rows, 2))
+    _run(what, dev, _lib().ttt_layer_norm, (ctypes.byref(cfg), pX, _ld(X), rows, pw, pb, pY, ps),
+         stream)
     return Y, stats
 
 
 def ttt_layer_norm_backward(cfg: ttt_norm_config, X, dY, stats, weight=None, dX=None,
                             dweight=None, dbias=None, workspace=None, stream=None):
     """(dX, dweight, dbias) from the forward call's X and stats."""
-    c = _Call("ttt_layer_norm_backward", X)
-    rows, dim, tdt = int(X.shape[0]), int(cfg.dim), _token(cfg.precision)
-    c.check("X", X, tdt, (rows, dim), rows=True)
-    c.check("dY", dY, tdt, (rows, dim), rows=True)
-    c.check("stats", stats, torch.float32, (rows, 2))
-    c.check("weight", weight, torch.float32, (dim,), optional=True)
-    dX = c.out("dX", dX, tdt, (rows, dim))
-    dweight = c.out("dweight", dweight, torch.float32, (dim,))
-    dbias = c.out("dbias", dbias, torch.float32, (dim,))
-    ws, nbytes = c.workspace(workspace, ttt_norm_workspace_bytes(cfg, rows)
-                             if workspace is None else 0)
-    c.run(_lib().ttt_layer_norm_backward,
-          (ctypes.byref(cfg), B._ptr(X), _ld(X), B._ptr(dY), _ld(dY), rows, B._ptr(weight),
-           B._ptr(stats), B._ptr(dX), B._ptr(dweight), B._ptr(dbias), B._ptr(ws), nbytes), stream)
+    what = "ttt_layer_norm_backward"
+    dev, tdt, f32 = _device(what, X), _token(cfg.precision), torch.float32
+    dim = cfg.dim
+    rows = X.shape[0]
+    pX = _check(what, dev, "X", X, tdt, (rows, dim), True)
+    pY = _check(what, dev, "dY", dY, tdt, (rows, dim), True)
+    ps = _check(what, dev, "stats", stats, f32, (rows, 2))
+    pw = _maybe(what, dev, "weight", weight, f32, (dim,))
+    dX, p1 = _out(what, dev, "dX", dX, tdt, (rows, dim))
+    dweight, p2 = _out(what, dev, "dweight", dweight, f32, (dim,))
+    dbias, p3 = _out(what, dev, "dbias", dbias, f32, (dim,))
+    workspace, pW, nbytes = _space(what, dev, workspace, lambda: ttt_norm_workspace_bytes(cfg, rows))
+    _run(what, dev, _lib().ttt_layer_norm_backward,
+         (ctypes.byref(cfg), pX, _ld(X), pY, _ld(dY), rows, pw, ps, p1, p2, p3, pW, nbytes), stream)
     return dX, dweight, dbias

@@ -14,6 +14,7 @@ namespace ttt {
 namespace {
 
 constexpr int kC = 64;  // tokens of a chunk
+constexpr float kNoBeta = 0x1p-64f;  // what stands for a beta of 0 in the gradient's chains
 
 // The tokens of sequence i, and its first chunk slot: start / kC + i leaves
 // room for the chunks of every sequence before it (ceil(len / kC) <= end / kC -
@@ -157,6 +158,77 @@ __device__ __forceinline__ uint32_t tri(int row, int col) {
          (col & 7) * 2;
 }
 
+// Every kAnchor-th chunk the state is kept in fp32: there the gradient of the decays,
+// a running sum over tokens, starts anew.
+constexpr int kAnchor = 8;
+
+// Stores of accumulators for a later kernel, as bf16 in blocks of 8 x 8 values (8
+// rows of 16 bytes: what ldmatrix reads, and a whole line for a warp to write).
+// The state [D rows][DK columns from c0]: blocks [column / 32][row / 8][column / 8 % 4].
+template <int D, int DK>
+__device__ __forceinline__ void keep_state(__nv_bfloat16* to, const float (&s)[DK / 8][4], int r0,
+                                           int c0, int lane) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(to);
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j) {
+    const int c = c0 / 8 + j;
+    const int block = (c / 4 * (D / 8) + r0 / 8) * 4 + c % 4;
+    w[block * 32 + lane] = pack_bf16x2(s[j][0], s[j][1]);
+    w[(block + 4) * 32 + lane] = pack_bf16x2(s[j][2], s[j][3]);
+  }
+}
+// 16 rows of the transpose of a [64 tokens][D] array, token tile t: blocks [row / 8][token / 8].
+template <int D>
+__device__ __forceinline__ void keep_tile(__nv_bfloat16* to, const float (&u)[4], int r0, int t,
+                                          int lane) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(to) + (r0 / 8 * 8 + t) * 32 + lane;
+  w[0] = pack_bf16x2(u[0], u[1]);
+  w[8 * 32] = pack_bf16x2(u[2], u[3]);
+}
+// The state in fp32, as the registers lie.
+template <int N>
+__device__ __forceinline__ void keep_anchor(float* to, const float (&s)[N][4], int first,
+                                            int lane) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    reinterpret_cast<float4*>(to)[(first + j) * 32 + lane] =
+        make_float4(s[j][0], s[j][1], s[j][2], s[j][3]);
+}
+template <int N>
+__device__ __forceinline__ float dot_anchor(const float* from, const float (&s)[N][4], int first,
+                                            int lane) {
+  float x = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float4 v = reinterpret_cast<const float4*>(from)[(first + j) * 32 + lane];
+    x = fmaf(s[j][0], v.x, fmaf(s[j][1], v.y, fmaf(s[j][2], v.z, fmaf(s[j][3], v.w, x))));
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+  return x;
+}
+// Sums over 16 rows of an accumulator times the tile's bf16 values (w0: rows 0-7,
+// w1: rows 8-15), of the lane's two tokens; in every lane of the column.
+__device__ __forceinline__ float2 rows_sum(float2 x) {
+#pragma unroll
+  for (int m = 4; m < 32; m *= 2) {
+    x.x += __shfl_xor_sync(0xffffffffu, x.x, m);
+    x.y += __shfl_xor_sync(0xffffffffu, x.y, m);
+  }
+  return x;
+}
+__device__ __forceinline__ float2 dot_pair(const float (&y)[4], uint32_t w0, uint32_t w1) {
+  return rows_sum(make_float2(
+      fmaf(y[0], __uint_as_float(w0 << 16), y[2] * __uint_as_float(w1 << 16)),
+      fmaf(y[1], __uint_as_float(w0 & 0xffff0000u), y[3] * __uint_as_float(w1 & 0xffff0000u))));
+}
+__device__ __forceinline__ void put_dots(float* to, float2 x, int t, int valid, int lane) {
+  if (lane < 4) {
+    if (t + 2 * lane < valid) to[2 * lane] = x.x;
+    if (t + 2 * lane + 1 < valid) to[2 * lane + 1] = x.y;
+  }
+}
+
 inline int64_t chunk_slots(const DeltaArgs& a) { return a.n / kC + a.seqs; }
 
 // Token rows as boxes of 64 tokens: all columns of a head, as [d / 64][64][64];
@@ -176,7 +248,22 @@ inline bool strip_map(CUtensorMap* m, const void* base, int64_t n, int64_t ld, i
 
 }  // namespace
 
+// What the forward pass leaves for the gradient, by chunk slot and head.
+struct DeltaKept {
+  __nv_bfloat16* S0;  // the state before the chunk
+  __nv_bfloat16* U;   // [d][64 tokens]
+  float* U32;         // U in fp32, as registers lie
+  float* anchors;     // the state before every kAnchor-th chunk of a sequence
+  float* last;        // the last states, or nullptr
+  float* dots;        // [d / 16][H][n]: dO . O over 16 columns
+};
+
 // Inverses, P and gates of every chunk into `blocks` (kernels_delta_tc.cu).
 cudaError_t delta_prepare(const DeltaArgs& a, bool gradient, uint8_t* blocks, cudaStream_t st);
+// The chain of states for the gradient.
+cudaError_t delta_states_kept(const DeltaArgs& a, const float* S_in, const void* dO,
+                              const uint8_t* blocks, const DeltaKept& kept, cudaStream_t st);
+// Which form of the chain's kernels a call takes (both directions the same).
+bool delta_few_rows(const DeltaArgs& a);
 
 }  // namespace ttt

@@ -13,8 +13,6 @@
 namespace ttt {
 namespace {
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
@@ -202,10 +200,10 @@ __global__ void __launch_bounds__(32 * kWarps)
 // time (`hist`).  Rows of S and A stay with one warp; sums over rows are taken
 // in a warp first, then over the warps in order.
 constexpr int kBW = 16;  // warps
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(32 * kBW)
-    delta_tokens_backward_kernel(TokArgs a, const T* dO, const float* dS_out, const float* keep,
-                                 float* hist, float* A, float* dq_out, float* dk_out, T* dV,
+    delta_tokens_backward_kernel(TokArgs a, const float* dO, const float* dS_out, const float* keep,
+                                 float* hist, float* A, float* dq_out, float* dk_out, float* dV,
                                  float* dg_out, float* db_out) {
   constexpr int NC = D / 32;
   __shared__ float red[kBW][2][D];
@@ -231,16 +229,16 @@ __global__ void __launch_bounds__(32 * kBW)
         s[c] = keep[((sq.slot + blk) * a.H + h) * DD + (size_t)row * D + c * 32 + lane];
       for (int64_t t = b0; t < b1; ++t) {
         const float eg = expf(a.g[t * a.H + h]), b = a.b[t * a.H + h];
-        const T* kp = static_cast<const T*>(a.K) + t * a.ldk + hk * D;
+        const float* kp = static_cast<const float*>(a.K) + t * a.ldk + hk * D;
         float sk = 0.f;
         for (int c = 0; c < NC; ++c) {
           hs[(t - b0) * DD + (size_t)row * D + c * 32 + lane] = s[c];
           s[c] *= eg;
-          sk = fmaf(s[c], to_f(kp[c * 32 + lane]), sk);
+          sk = fmaf(s[c], kp[c * 32 + lane], sk);
         }
         for (int m = 16; m > 0; m /= 2) sk += __shfl_xor_sync(0xffffffffu, sk, m);
-        const float u = b * (to_f(static_cast<const T*>(a.V)[t * a.ldv + h * D + row]) - sk);
-        for (int c = 0; c < NC; ++c) s[c] = fmaf(u, to_f(kp[c * 32 + lane]), s[c]);
+        const float u = b * (static_cast<const float*>(a.V)[t * a.ldv + h * D + row] - sk);
+        for (int c = 0; c < NC; ++c) s[c] = fmaf(u, kp[c * 32 + lane], s[c]);
       }
     }
     for (int64_t t = b1 - 1; t >= b0; --t) {
@@ -248,13 +246,12 @@ __global__ void __launch_bounds__(32 * kBW)
       float k[NC], q[NC], dq[NC] = {}, dk[NC] = {}, dg = 0.f, db = 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        k[c] = to_f(static_cast<const T*>(a.K)[t * a.ldk + hk * D + c * 32 + lane]);
-        q[c] = to_f(static_cast<const T*>(a.Q)[t * a.ldq + hk * D + c * 32 + lane]);
+        k[c] = static_cast<const float*>(a.K)[t * a.ldk + hk * D + c * 32 + lane];
+        q[c] = static_cast<const float*>(a.Q)[t * a.ldq + hk * D + c * 32 + lane];
       }
       for (int row = warp; row < D; row += kBW) {
-        const float go =
-            a.scale * to_f(dO[t * (int64_t)a.H * D + h * D + row]);
-        const float v = to_f(static_cast<const T*>(a.V)[t * a.ldv + h * D + row]);
+        const float go = a.scale * dO[t * (int64_t)a.H * D + h * D + row];
+        const float v = static_cast<const float*>(a.V)[t * a.ldv + h * D + row];
         float s[NC], A_[NC], du = 0.f, sk = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -269,7 +266,7 @@ __global__ void __launch_bounds__(32 * kBW)
           du += __shfl_xor_sync(0xffffffffu, du, m);
         }
         const float u = b * (v - sk), dv = b * du;
-        if (lane == 0) put(dV + t * (int64_t)a.H * D + h * D + row, dv);
+        if (lane == 0) dV[t * (int64_t)a.H * D + h * D + row] = dv;
         db = fmaf(du, v - sk, db);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -355,10 +352,12 @@ template <bool STEP, bool KEEP>
 cudaError_t by_type(const DeltaArgs& a, const TokArgs& k, int64_t blocks, const float* S_in,
                     float* S_out, void* O, float* keep, cudaStream_t st) {
   using B = __nv_bfloat16;
-  if (a.bf16) {
-    if (a.d == 64) return launch_tokens<B, 64, STEP, KEEP>(k, blocks, S_in, S_out, O, keep, st);
-    if (a.d == 128) return launch_tokens<B, 128, STEP, KEEP>(k, blocks, S_in, S_out, O, keep, st);
-    return launch_tokens<B, 256, STEP, KEEP>(k, blocks, S_in, S_out, O, keep, st);
+  if constexpr (!KEEP) {  // states are kept for the fp32 gradient alone
+    if (a.bf16) {
+      if (a.d == 64) return launch_tokens<B, 64, STEP, KEEP>(k, blocks, S_in, S_out, O, keep, st);
+      if (a.d == 128) return launch_tokens<B, 128, STEP, KEEP>(k, blocks, S_in, S_out, O, keep, st);
+      return launch_tokens<B, 256, STEP, KEEP>(k, blocks, S_in, S_out, O, keep, st);
+    }
   }
   if (a.d == 64) return launch_tokens<float, 64, STEP, KEEP>(k, blocks, S_in, S_out, O, keep, st);
   if (a.d == 128) return launch_tokens<float, 128, STEP, KEEP>(k, blocks, S_in, S_out, O, keep, st);
@@ -386,15 +385,15 @@ BackPlan back_plan(const DeltaArgs& a) {
   return p;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_backward(const DeltaArgs& a, const TokArgs& k, const void* dO,
                             const float* dS_out, void* dV, float* dg, float* db, char* w,
                             const BackPlan& p, cudaStream_t st) {
   TraceScope ts("delta_tokens_backward", st);
-  delta_tokens_backward_kernel<T, D><<<dim3((unsigned)a.H, (unsigned)a.seqs), 32 * kBW, 0, st>>>(
-      k, static_cast<const T*>(dO), dS_out, reinterpret_cast<const float*>(w + p.keep),
+  delta_tokens_backward_kernel<D><<<dim3((unsigned)a.H, (unsigned)a.seqs), 32 * kBW, 0, st>>>(
+      k, static_cast<const float*>(dO), dS_out, reinterpret_cast<const float*>(w + p.keep),
       reinterpret_cast<float*>(w + p.hist), reinterpret_cast<float*>(w + p.A),
-      reinterpret_cast<float*>(w + p.pq), reinterpret_cast<float*>(w + p.pk), static_cast<T*>(dV),
+      reinterpret_cast<float*>(w + p.pq), reinterpret_cast<float*>(w + p.pk), static_cast<float*>(dV),
       dg, db);
   return cudaGetLastError();
 }
@@ -445,15 +444,9 @@ cudaError_t delta_tokens_backward(const DeltaArgs& a, const float* S_in, const v
   cudaError_t e = by_type<false, true>(a, k, a.seqs, S_in, nullptr, nullptr,
                                        reinterpret_cast<float*>(w + p.keep), st);
   if (e != cudaSuccess) return e;
-  using B = __nv_bfloat16;
-  if (a.bf16)
-    e = a.d == 64    ? launch_backward<B, 64>(a, k, dO, dS_out, dV, dg, db, w, p, st)
-        : a.d == 128 ? launch_backward<B, 128>(a, k, dO, dS_out, dV, dg, db, w, p, st)
-                     : launch_backward<B, 256>(a, k, dO, dS_out, dV, dg, db, w, p, st);
-  else
-    e = a.d == 64    ? launch_backward<float, 64>(a, k, dO, dS_out, dV, dg, db, w, p, st)
-        : a.d == 128 ? launch_backward<float, 128>(a, k, dO, dS_out, dV, dg, db, w, p, st)
-                     : launch_backward<float, 256>(a, k, dO, dS_out, dV, dg, db, w, p, st);
+  e = a.d == 64    ? launch_backward<64>(a, k, dO, dS_out, dV, dg, db, w, p, st)
+      : a.d == 128 ? launch_backward<128>(a, k, dO, dS_out, dV, dg, db, w, p, st)
+                   : launch_backward<256>(a, k, dO, dS_out, dV, dg, db, w, p, st);
   if (e != cudaSuccess) return e;
   if (dS_in != nullptr) {
     e = cudaMemcpyAsync(dS_in, w + p.A, (size_t)a.seqs * a.H * a.d * a.d * 4,

@@ -1,0 +1,922 @@
+// Gradient of the gated delta rule in chunks of 64 tokens (the notation of
+// kernels_delta_tc.cu; E is the gradient of the state behind a chunk, dO that
+// of the outputs).  With u_t = beta_t w_t:
+//   dU = P^T dO + rest (K E^T),   X = T^T dU,   dV = beta X,   dbeta = X . w
+//   E <- gamma_64 E + (scale gamma dO)^T Q - (gamma dV)^T K
+//   dQ = scale gamma (dO S) + A K,              A = lower part of scale Gamma (dO U^T)
+//   dK = A^T Q + (M + M^T) K + rest (U E) - gamma (dV S),
+//        M = strictly lower part of -Gamma (dV U^T)
+// The decays' gradient needs none of these products: scaling S and its gradient
+// against each other shows that <E_t, S_t>, the gradient of token t+1's decay,
+// changes from token to token by dO_t . O_t - dV_t . V_t alone, so it is a running sum
+// from the end, started anew from a product of the two states every 512 tokens.
+//
+// Five kernels: the inverses of all chunks; the forward chain once more, which
+// keeps each chunk's state and U (rounded to bf16: they only enter dQ and dK,
+// which are bf16) and the sums of dO . O; delta_reverse_kernel, the chain of E from
+// the last chunk to the first; delta_tokens_grad_kernel, dQ and dK of all chunks
+// at once; and the running sums.  The chains carry fp32 in three bf16 parts
+// (the gates' gradients and dS are fp32 results), the rest is bf16 products
+// summed in fp32.
+
+#include <type_traits>
+
+#include "delta_tc.cuh"
+
+namespace ttt {
+namespace {
+
+// ----------------------------------------------------------------------------
+// delta_reverse_kernel: as delta_state_kernel, KS warps share 16 rows of E.
+// ----------------------------------------------------------------------------
+template <int D, int KS, int RG>
+struct RK {
+  static constexpr int WARPS = KS * RG;
+  static constexpr int KQ = kC * D * 2;
+  static constexpr int BLOCK = chunk_bytes(3);
+  static constexpr int V = kC * 32;
+  static constexpr int STAGE = 2 * KQ + 2 * RG * V + BLOCK;
+  // exchange of a group: partial K E^T, dU in parts, gamma dV in parts
+  static constexpr int X_PART = 8 * (KS - 1) * 32 * 16, X_U = 8 * 3 * 32 * 8;
+  static constexpr int X = X_PART + 2 * X_U;
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int OFF_X = 2 * STAGE;
+  static constexpr int OFF_BAR = OFF_X + RG * X;
+  static constexpr int SMEM = OFF_BAR + 192 + 1024;
+  static_assert((KS == 2 || KS == 4) && RG <= 2, "tiles and barriers of a group");
+  static_assert(STAGE % 1024 == 0, "tiles are aligned to the swizzle");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct ReverseArgs {
+  int64_t n;
+  const int64_t* offsets;
+  int H, Hk;
+  float scale;
+  const uint8_t* blocks;
+  DeltaKept kept;
+  const float* dS_out;
+  float* dS_in;
+  __nv_bfloat16* dV;
+  __nv_bfloat16* E;    // the gradient behind each chunk, blocked as S0
+  __nv_bfloat16* dVt;  // dV, blocked as U
+  float *dots_v, *dots_x;        // [d / 16][H][n]: dV . V, X . w
+  float *hold, *hold_last;       // [anchors or sequences][H][d / 16][KS]: <E, S>
+  int* err;
+};
+
+template <int D, int KS, int RG>
+__global__ void __launch_bounds__(RK<D, KS, RG>::THREADS, 1)
+    delta_reverse_kernel(const __grid_constant__ CUtensorMap mQ,
+                         const __grid_constant__ CUtensorMap mK,
+                         const __grid_constant__ CUtensorMap mV,
+                         const __grid_constant__ CUtensorMap mG, const ReverseArgs a) {
+  using L = RK<D, KS, RG>;
+  constexpr int DK = D / KS, NT = 8 / KS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* empty = full + 2;
+  uint64_t* met = empty + 2;  // 3 for each group: partial sums, dU, dV are written
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(met + 3 * RG);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int h = blockIdx.y, hk = h / (a.H / a.Hk);
+  const int64_t seq = blockIdx.z;
+  const SeqRange sr = seq_range(a.offsets, a.n, seq);
+  const int64_t len = sr.t1 - sr.t0;
+  const int64_t nc = (len + kC - 1) / kC;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], L::WARPS);
+    }
+    for (int i = 0; i < 3 * RG; ++i) mbar_init(&met[i], KS);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == L::WARPS) {  // ------------------------------------------------ loads
+    if (lane == 0) {
+      int64_t issued = 0;
+      for (int64_t i = 0; i < nc; ++i) {
+        const int s = (int)(i & 1);
+        if (!mbar_wait(&empty[s], (uint32_t)((i >> 1) & 1) ^ 1, abort_flag, a.err, kErrWaitEmpty))
+          break;
+        uint8_t* st = smem + s * L::STAGE;
+        const int64_t c = nc - 1 - i;
+        const int t = (int)(sr.t0 + c * kC);
+        mbar_arrive_expect_tx(&full[s], L::STAGE);
+        tma_load_3d(st, &mK, &full[s], 0, t, hk * (D / 64));
+        tma_load_3d(st + L::KQ, &mQ, &full[s], 0, t, hk * (D / 64));
+        for (int g = 0; g < RG; ++g) {
+          const int x = h * D + ((int)blockIdx.x * RG + g) * 16;
+          tma_load_2d(st + 2 * L::KQ + g * L::V, &mV, &full[s], x, t);
+          tma_load_2d(st + 2 * L::KQ + (RG + g) * L::V, &mG, &full[s], x, t);
+        }
+        bulk_load(st + L::STAGE - L::BLOCK,
+                  a.blocks + ((sr.slot + c) * a.H + h) * (int64_t)L::BLOCK, L::BLOCK, &full[s]);
+        ++issued;
+      }
+      drain_ring(full, 2, issued, a.err);
+    }
+    return;
+  }
+
+  const int grp = warp / KS, kw = warp % KS;
+  const int r0 = ((int)blockIdx.x * RG + grp) * 16, c0 = kw * DK;
+  const int row = lane / 4, col = 2 * (lane % 4);
+  uint8_t* x_part = smem + L::OFF_X + grp * L::X;
+  uint8_t* x_u = x_part + L::X_PART;
+  uint8_t* x_v = x_u + L::X_U;
+  // token tiles of this warp, as in delta_state_kernel
+  const auto tile = [&](int j) { return j / 2 * 2 * KS + (j % 2 == 0 ? kw : 2 * KS - 1 - kw); };
+  const auto owner = [](int t) { return t % (2 * KS) < KS ? t % (2 * KS) : 2 * KS - 1 - t % (2 * KS); };
+  const auto pair_row = [&](int p) { return tile(2 * p + lane / 16) * 8 + lane % 8; };
+  met += 3 * grp;
+  const auto arrive = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&met[i]);
+  };
+  const auto wait = [&](int i, int64_t n) {
+    return __all_sync(0xffffffffu,
+                      mbar_wait(&met[i], (uint32_t)(n & 1), abort_flag, a.err, kErrWaitOperand));
+  };
+  float s[DK / 8][4];  // E
+  const int64_t state = ((seq * a.H + h) * D + r0) * (int64_t)D + c0;
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j) {
+    float2 x = make_float2(0.f, 0.f), y = x;
+    if (a.dS_out != nullptr) {
+      x = *reinterpret_cast<const float2*>(a.dS_out + state + row * D + j * 8 + col);
+      y = *reinterpret_cast<const float2*>(a.dS_out + state + (row + 8) * D + j * 8 + col);
+    }
+    s[j][0] = x.x, s[j][1] = x.y, s[j][2] = y.x, s[j][3] = y.y;
+  }
+  const int first = (r0 / 16 * KS + kw) * (DK / 8);  // this warp's place in an anchor
+  if (a.dS_out != nullptr) {
+    const float x = dot_anchor(a.kept.last + (seq * a.H + h) * (int64_t)D * D, s, first, lane);
+    if (lane == 0) a.hold_last[(seq * a.H + h) * (D / 16) * KS + r0 / 16 * KS + kw] = x;
+  }
+  const int nk_r = (lane / 16) * 8 + lane % 8, nk_c = lane / 8 % 2;
+  const int kn_r = lane % 16, kn_c = (lane / 16) * 8;
+
+  for (int64_t i = 0; i < nc; ++i) {
+    const int64_t c = nc - 1 - i;
+    const int st = (int)(i & 1);
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (uint32_t)((i >> 1) & 1), abort_flag, a.err,
+                                           kErrWaitFull)))
+      break;
+    uint8_t* base = smem + st * L::STAGE;
+    uint8_t* vp = base + 2 * L::KQ + grp * L::V;
+    const uint32_t sK = smem_u32(base), sQ = sK + L::KQ, sV = smem_u32(vp), sG = sV + RG * L::V,
+                   sT = sK + L::STAGE - L::BLOCK, sP = sT + 3 * kTri;
+    const float* gates = reinterpret_cast<const float*>(base + L::STAGE - kGates);
+    const int valid = len - c * kC < kC ? (int)(len - c * kC) : kC;
+    const int64_t at = (sr.slot + c) * a.H + h;
+    keep_state<D, DK>(a.E + at * D * D, s, r0, c0, lane);
+
+    // K E^T over this warp's columns of E
+    float du[NT][4];
+    {
+      float r[8][4] = {}, rs[8][4] = {};
+      uint32_t b[2][4];
+      ldsm4(sK + sw(kC, nk_r, c0 + nk_c * 8), b[0]);
+#pragma unroll
+      for (int k = 0; k < DK / 16; ++k) {
+        uint32_t hi[4], mid[4], lo[4];
+        split_a(s[2 * k], s[2 * k + 1], hi, mid, lo);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int f = k * 4 + p + 1;
+          uint32_t(&x)[4] = b[p % 2];
+          if (f < DK / 4)
+            ldsm4(sK + sw(kC, f % 4 * 16 + nk_r, c0 + f / 4 * 16 + nk_c * 8), b[f % 2]);
+          mma(rs[2 * p], mid, x[0], x[1]);
+          mma(rs[2 * p + 1], mid, x[2], x[3]);
+          mma(r[2 * p], hi, x[0], x[1]);
+          mma(r[2 * p + 1], hi, x[2], x[3]);
+          mma(rs[2 * p], lo, x[0], x[1]);
+          mma(rs[2 * p + 1], lo, x[2], x[3]);
+        }
+      }
+      float4* xp = reinterpret_cast<float4*>(x_part);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) r[t][y] += rs[t][y];
+        if (owner(t) != kw)
+          xp[(t * (KS - 1) + (kw < owner(t) ? kw : kw - 1)) * 32 + lane] =
+              make_float4(r[t][0], r[t][1], r[t][2], r[t][3]);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int w = 0; w < KS; ++w)
+          if (w == kw)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              du[j][y] = r[j / 2 * 2 * KS + (j % 2 == 0 ? w : 2 * KS - 1 - w)][y];
+      arrive(0);
+    }
+    // dO^T of the group's rows as A operands (rows behind the sequence count as zero), and
+    // P^T dO of this warp's tokens: tokens j take tokens i >= j
+    uint32_t go[4][4];
+    float pd[NT][4] = {};
+    {
+      float ps[NT][4] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ldsm4_t(sG + sw32(k * 16 + nk_r, nk_c), go[k]);
+        const uint32_t k0 = keep_pair(k * 16 + col, valid), k1 = keep_pair(k * 16 + 8 + col, valid);
+        go[k][0] &= k0, go[k][1] &= k0, go[k][2] &= k1, go[k][3] &= k1;
+#pragma unroll
+        for (int p = 0; p < NT / 2; ++p) {
+          if (k < tile(2 * p) / 2) continue;
+          const bool second = k >= tile(2 * p + 1) / 2;
+          // rows 16 k .. of the two tiles' strips; one that starts below is not used
+          const int tj = lane / 16 == 0 || second ? tile(2 * p + lane / 16) : tile(2 * p);
+          const uint32_t from = sP + tri(k * 16 + kn_r, tj * 8);
+          uint32_t b[4];
+#pragma unroll
+          for (int x = 2; x >= 0; --x) {
+            ldsm4_t(from + x * kTri, b);
+            mma(x == 0 ? pd[2 * p] : ps[2 * p], go[k], b[0], b[1]);
+            if (second) mma(x == 0 ? pd[2 * p + 1] : ps[2 * p + 1], go[k], b[2], b[3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) pd[j][y] += ps[j][y];
+    }
+    if (!wait(0, i)) break;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int w = 0; w < KS - 1; ++w) {
+        const float4 v =
+            reinterpret_cast<const float4*>(x_part)[(tile(j) * (KS - 1) + w) * 32 + lane];
+        du[j][0] += v.x, du[j][1] += v.y, du[j][2] += v.z, du[j][3] += v.w;
+      }
+      const int t = tile(j) * 8 + col;
+      const float2 re = *reinterpret_cast<const float2*>(gates + kC + t);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        du[j][y] = t + y % 2 < valid ? fmaf(y % 2 ? re.y : re.x, du[j][y], pd[j][y]) : 0.f;
+    }
+    // the parts of an array's tiles as A operands [tokens / 16][part][lane]
+    const auto put_parts = [&](uint8_t* to, const float(&x)[NT][4]) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint32_t hi[2], mid[2], lo[2];
+        split3(x[j][0], x[j][1], hi[0], mid[0], lo[0]);
+        split3(x[j][2], x[j][3], hi[1], mid[1], lo[1]);
+        const int t = tile(j);
+        uint2* d = reinterpret_cast<uint2*>(to) + (t / 2 * 3 * 32 + lane) * 2 + t % 2;
+        d[0] = make_uint2(hi[0], hi[1]);
+        d[64] = make_uint2(mid[0], mid[1]);
+        d[128] = make_uint2(lo[0], lo[1]);
+      }
+    };
+    put_parts(x_u, du);
+    arrive(1);
+    // U of this warp's tiles, for X . w
+    float4 u32[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      u32[j] = reinterpret_cast<const float4*>(
+          a.kept.U32)[((at * (D / 16) + r0 / 16) * 8 + tile(j)) * 32 + lane];
+    if (!wait(1, i)) break;
+    // X = T^T dU
+    float xt[NT][4] = {};
+    {
+      float xs[2][NT][4] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k < tile(0) / 2) continue;
+        uint32_t hi[4], mid[4], lo[4];
+        const uint4* d = reinterpret_cast<const uint4*>(x_u) + k * 3 * 32 + lane;
+        load_a(d, hi);
+        load_a(d + 32, mid);
+        load_a(d + 64, lo);
+#pragma unroll
+        for (int p = 0; p < NT / 2; ++p) {
+          if (k < tile(2 * p) / 2) continue;
+          const bool second = k >= tile(2 * p + 1) / 2;
+          const int tj = lane / 16 == 0 || second ? tile(2 * p + lane / 16) : tile(2 * p);
+          const uint32_t from = sT + tri(k * 16 + kn_r, tj * 8);
+          uint32_t b[3][4];
+#pragma unroll
+          for (int x = 0; x < 3; ++x) ldsm4_t(from + x * kTri, b[x]);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            if (z == 1 && !second) continue;
+            const int j = 2 * p + z;
+            mma(xt[j], hi, b[0][2 * z], b[0][2 * z + 1]);
+            mma(xs[0][j], mid, b[0][2 * z], b[0][2 * z + 1]);
+            mma(xs[1][j], hi, b[1][2 * z], b[1][2 * z + 1]);
+            mma(xs[0][j], lo, b[0][2 * z], b[0][2 * z + 1]);
+            mma(xs[1][j], mid, b[1][2 * z], b[1][2 * z + 1]);
+            mma(xs[0][j], hi, b[2][2 * z], b[2][2 * z + 1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) xt[j][y] += xs[0][j][y] + xs[1][j][y];
+    }
+    // dV = beta X; the gates' sums over these 16 columns
+    float gd[NT][4];  // -gamma dV
+    const int64_t dots = ((r0 / 16) * (int64_t)a.H + h) * a.n + sr.t0 + c * kC;
+#pragma unroll
+    for (int p = 0; p < NT / 2; ++p) {
+      uint32_t v[4];
+      ldsm4_t(sV + sw32(pair_row(p), nk_c), v);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int j = 2 * p + z, t = tile(j) * 8 + col;
+        const float2 be = *reinterpret_cast<const float2*>(gates + 2 * kC + t);
+        const float2 ga = *reinterpret_cast<const float2*>(gates + t);
+        float2 xw = make_float2(fmaf(xt[j][0], u32[j].x, xt[j][2] * u32[j].z),
+                                fmaf(xt[j][1], u32[j].y, xt[j][3] * u32[j].w));
+        xw = rows_sum(xw);
+        put_dots(a.dots_x + dots + tile(j) * 8, make_float2(xw.x / be.x, xw.y / be.y), tile(j) * 8,
+                 valid, lane);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float b = y % 2 ? be.y : be.x;
+          xt[j][y] *= b == kNoBeta ? 0.f : b;
+          gd[j][y] = -(y % 2 ? ga.y : ga.x) * xt[j][y];
+        }
+        put_dots(a.dots_v + dots + tile(j) * 8, dot_pair(xt[j], v[2 * z], v[2 * z + 1]), tile(j) * 8,
+                 valid, lane);
+        keep_tile<D>(a.dVt + at * kC * D, xt[j], r0, tile(j), lane);
+      }
+    }
+    put_parts(x_v, gd);
+    arrive(2);
+    // dV over this group's V (each warp over the tokens it has read), then out
+#pragma unroll
+    for (int p = 0; p < NT / 2; ++p) {
+      const uint32_t w[4] = {pack_bf16x2(xt[2 * p][0], xt[2 * p][1]),
+                             pack_bf16x2(xt[2 * p][2], xt[2 * p][3]),
+                             pack_bf16x2(xt[2 * p + 1][0], xt[2 * p + 1][1]),
+                             pack_bf16x2(xt[2 * p + 1][2], xt[2 * p + 1][3])};
+      stsm4_t(sV + sw32(pair_row(p), nk_c), w);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < NT / 2; ++p) {
+      const int t = tile(2 * p + lane / 16) * 8 + lane / 2 % 8;
+      const uint4 w = *reinterpret_cast<const uint4*>(vp + sw32(t, lane % 2));
+      if (t < valid)
+        *reinterpret_cast<uint4*>(a.dV + (sr.t0 + c * kC + t) * (int64_t)a.H * D + h * D + r0 +
+                                  (lane % 2) * 8) = w;
+    }
+    // E = gamma_64 E + (scale gamma dO)^T Q - (gamma dV)^T K; rows of Q and K behind the
+    // sequence may hold anything and count as zero
+    const float gl = gates[kC - 1];
+    const auto add = [&](uint32_t from, const uint32_t(&hi)[4][4], const uint32_t(&mid)[4][4],
+                         const uint32_t(&lo)[4][4], float fade, auto tail) {
+      uint32_t b[2][4];
+      ldsm4_t(from + sw(kC, kn_r, c0 + kn_c), b[0]);
+      float d0[4] = {}, d1[4] = {}, e0[4] = {}, e1[4] = {};
+#pragma unroll
+      for (int e = 0; e < DK / 4; ++e) {
+        const int j = e / 4, k = e % 4, f = e + 1;
+        uint32_t(&x)[4] = b[e % 2];
+        if (f < DK / 4)
+          ldsm4_t(from + sw(kC, f % 4 * 16 + kn_r, c0 + f / 4 * 16 + kn_c), b[f % 2]);
+        if (decltype(tail)::value) {
+          const uint32_t k0 = keep_pair(k * 16 + col, valid),
+                         k1 = keep_pair(k * 16 + 8 + col, valid);
+          x[0] &= k0, x[1] &= k1, x[2] &= k0, x[3] &= k1;
+        }
+        mma(e0, mid[k], x[0], x[1]);
+        mma(e1, mid[k], x[2], x[3]);
+        mma(d0, hi[k], x[0], x[1]);
+        mma(d1, hi[k], x[2], x[3]);
+        mma(e0, lo[k], x[0], x[1]);
+        mma(e1, lo[k], x[2], x[3]);
+        if (k == 3)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            s[2 * j][y] = fmaf(fade, s[2 * j][y], d0[y] + e0[y]);
+            s[2 * j + 1][y] = fmaf(fade, s[2 * j + 1][y], d1[y] + e1[y]);
+            d0[y] = d1[y] = e0[y] = e1[y] = 0.f;
+          }
+      }
+    };
+    const auto add_any = [&](uint32_t from, const uint32_t(&hi)[4][4], const uint32_t(&mid)[4][4],
+                             const uint32_t(&lo)[4][4], float fade) {
+      if (valid == kC)
+        add(from, hi, mid, lo, fade, std::false_type());
+      else
+        add(from, hi, mid, lo, fade, std::true_type());
+    };
+    uint32_t hi[4][4], mid[4][4], lo[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {  // operand register x: tokens 16 k + 8 (x / 2) + col
+        const float2 ga =
+            *reinterpret_cast<const float2*>(gates + k * 16 + x / 2 * 8 + col);
+        split3(__uint_as_float(go[k][x] << 16) * (a.scale * ga.x),
+               __uint_as_float(go[k][x] & 0xffff0000u) * (a.scale * ga.y), hi[k][x], mid[k][x],
+               lo[k][x]);
+      }
+    add_any(sQ, hi, mid, lo, gl);
+    if (!wait(2, i)) break;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4* d = reinterpret_cast<const uint4*>(x_v) + k * 3 * 32 + lane;
+      load_a(d, hi[k]);
+      load_a(d + 32, mid[k]);
+      load_a(d + 64, lo[k]);
+    }
+    add_any(sK, hi, mid, lo, 1.f);
+    if (c % kAnchor == 0) {  // <E, S> before the chunk: where the decays' running sum starts anew
+      const int64_t slot = (sr.t0 / (kC * kAnchor) + seq + c / kAnchor) * a.H + h;
+      const float x = dot_anchor(a.kept.anchors + slot * D * D, s, first, lane);
+      if (lane == 0) a.hold[slot * (D / 16) * KS + r0 / 16 * KS + kw] = x;
+    }
+    fence_proxy_async_smem();  // dV's stores into the stage come before the next loads
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+  }
+
+  if (a.dS_in != nullptr) {
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j) {
+      *reinterpret_cast<float2*>(a.dS_in + state + row * D + j * 8 + col) =
+          make_float2(s[j][0], s[j][1]);
+      *reinterpret_cast<float2*>(a.dS_in + state + (row + 8) * D + j * 8 + col) =
+          make_float2(s[j][2], s[j][3]);
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------
+// delta_tokens_grad_kernel: dQ and dK of one chunk and head.  8 warps: 4 blocks
+// of 16 tokens x 2 halves of the columns at hand.
+// ----------------------------------------------------------------------------
+constexpr int kGW = 8;
+
+template <int D>
+struct GK {
+  static constexpr int TOK = kC * D * 2;    // one of dO, Q, K, U, dV
+  static constexpr int STRIP = D * 32 * 2;  // 32 columns of S or E
+  static constexpr int OFF_S = 5 * TOK;
+  static constexpr int OFF_A = OFF_S + 2 * STRIP;
+  static constexpr int OFF_BAR = OFF_A + 2 * kC * 128;
+  static constexpr int SMEM = OFF_BAR + 64 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct TokensGradArgs {
+  int64_t n;
+  const int64_t* offsets;
+  int64_t seqs;
+  int H, Hk;
+  float scale;
+  const float* g;
+  const __nv_bfloat16 *S0, *E, *U, *dVt;
+  __nv_bfloat16 *dQ, *dK;  // heads of their own
+  float *pq, *pk;          // shared heads: each head's share, [n][H * d]
+  int* err;
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * kGW)
+    delta_tokens_grad_kernel(const __grid_constant__ CUtensorMap mQ,
+                             const __grid_constant__ CUtensorMap mK,
+                             const __grid_constant__ CUtensorMap mG, const TokensGradArgs a) {
+  using L = GK<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  __shared__ double G[kC];
+  uint8_t *pG = smem, *pQ = smem + L::TOK, *pK = smem + 2 * L::TOK, *pU = smem + 3 * L::TOK,
+          *pV = smem + 4 * L::TOK, *pS = smem + L::OFF_S, *pE = pS + L::STRIP,
+          *pA = smem + L::OFF_A, *pM = pA + kC * 128;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);  // tokens, strips
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 2);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int64_t slot = blockIdx.x;
+  const int h = blockIdx.y, hk = h / (a.H / a.Hk);
+  const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
+  if (c.len == 0) return;
+  const int64_t at = slot * a.H + h;
+  if (tid == 0) {
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&bar[0], 5 * L::TOK);
+    tma_load_3d(pG, &mG, &bar[0], 0, (int)c.t0, h * (D / 64));
+    tma_load_3d(pQ, &mQ, &bar[0], 0, (int)c.t0, hk * (D / 64));
+    tma_load_3d(pK, &mK, &bar[0], 0, (int)c.t0, hk * (D / 64));
+    bulk_load(pU, a.U + at * kC * D, L::TOK, &bar[0]);
+    bulk_load(pV, a.dVt + at * kC * D, L::TOK, &bar[0]);
+    mbar_arrive_expect_tx(&bar[1], 2 * L::STRIP);
+    bulk_load(pS, a.S0 + at * D * D, L::STRIP, &bar[1]);
+    bulk_load(pE, a.E + at * D * D, L::STRIP, &bar[1]);
+  }
+  if (warp == 1) {
+    double x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = 2 * lane + i;
+      const float g = j < c.len ? a.g[(c.t0 + j) * a.H + h] : 0.f;
+      x[i] = g < -1e4f ? -1e4 : (double)g;
+    }
+    double s = x[0] + x[1];
+    for (int m = 1; m < 32; m *= 2) {
+      const double o = __shfl_up_sync(0xffffffffu, s, m);
+      if (lane >= m) s += o;
+    }
+    G[2 * lane] = s - x[1];
+    G[2 * lane + 1] = s;
+  }
+  __syncthreads();
+  bool ok = mbar_wait(&bar[0], 0, abort_flag, a.err, kErrWaitFull);
+  if (c.len < kC) {  // rows behind the sequence count as zero
+    for (int e = tid; e < (kC - c.len) * (D / 8); e += 32 * kGW) {
+      const uint32_t o = sw(kC, c.len + e / (D / 8), e % (D / 8) * 8);
+      *reinterpret_cast<uint4*>(pG + o) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(pQ + o) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(pK + o) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  __syncthreads();
+  const uint32_t sG = smem_u32(pG), sQ = smem_u32(pQ), sK = smem_u32(pK), sU = smem_u32(pU),
+                 sV = smem_u32(pV), sS = smem_u32(pS), sE = smem_u32(pE), sA = smem_u32(pA),
+                 sM = smem_u32(pM);
+  const int m0 = warp / 2 * 16, half = warp % 2;
+  const int row = lane / 4, col = 2 * (lane % 4);
+  const int nk_r = (lane / 16) * 8 + lane % 8, nk_c = (lane / 8 % 2) * 8;
+  const int kn_r = lane % 16, kn_c = (lane / 16) * 8;
+  // this lane's row address in a transposed array of 8 x 8 blocks [d / 8][token / 8]: for
+  // (16 d from k, 16 tokens from t) as A (tokens are rows) and as B (tokens are columns)
+  const auto blk_a = [&](int k, int t) {
+    return (uint32_t)(((k / 8 + lane / 16) * 8 + t / 8 + lane / 8 % 2) * 128 + lane % 8 * 16);
+  };
+  const auto blk_b = [&](int k, int t) {
+    return (uint32_t)(((k / 8 + lane / 8 % 2) * 8 + t / 8 + lane / 16) * 128 + lane % 8 * 16);
+  };
+
+  // dO U^T and dV U^T: 16 tokens i x 32 tokens j
+  {
+    float dp[4][4] = {}, dl[4][4] = {};
+#pragma unroll 4
+    for (int k = 0; k < D; k += 16) {
+      uint32_t ag[4], av[4], b[4];
+      ldsm4(sG + sw(kC, m0 + kn_r, k + kn_c), ag);
+      ldsm4_t(sV + blk_a(k, m0), av);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        ldsm4_t(sU + blk_b(k, half * 32 + p * 16), b);
+        mma(dp[2 * p], ag, b[0], b[1]);
+        mma(dp[2 * p + 1], ag, b[2], b[3]);
+        mma(dl[2 * p], av, b[0], b[1]);
+        mma(dl[2 * p + 1], av, b[2], b[3]);
+      }
+    }
+    // A, and M with its transpose: every (i, j) of the lower part is this warp's alone
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = m0 + row + 8 * y, j = half * 32 + q * 8 + col;
+        float x[2], m[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float e = j + z <= i ? expf((float)(G[i] - G[j + z])) : 0.f;
+          x[z] = j + z <= i ? a.scale * e * dp[q][2 * y + z] : 0.f;
+          m[z] = -e * dl[q][2 * y + z];
+          __nv_bfloat16 v = __float2bfloat16_rn(m[z]);
+          if (j + z < i) {
+            *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, i, j + z)) = v;
+            *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, j + z, i)) = v;
+          } else if (j + z == i) {
+            *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, i, i)) = __float2bfloat16_rn(0.f);
+          }
+        }
+        *reinterpret_cast<uint32_t*>(pA + sw(kC, i, j)) = pack_bf16x2(x[0], x[1]);
+      }
+  }
+  __syncthreads();
+
+  const float gi[2] = {expf((float)G[m0 + row]), expf((float)G[m0 + row + 8])};
+  const float re[2] = {expf((float)(G[kC - 1] - G[m0 + row])),
+                       expf((float)(G[kC - 1] - G[m0 + row + 8]))};
+  for (int s = 0; s < D / 32; ++s) {  // 32 columns of dQ, dK at a time; 16 a warp
+    ok = mbar_wait(&bar[1], (uint32_t)(s & 1), abort_flag, a.err, kErrWaitFull) && ok;
+    const int cw = half * 16, cs = s * 32 + cw;  // in the strip; in the head
+    float dq[2][4] = {}, dk[2][4] = {}, ve[2][4] = {};
+#pragma unroll 4
+    for (int k = 0; k < D; k += 16) {
+      uint32_t ag[4], av[4], au[4], b[4];
+      ldsm4(sG + sw(kC, m0 + kn_r, k + kn_c), ag);
+      ldsm4_t(sV + blk_a(k, m0), av);
+      ldsm4_t(sU + blk_a(k, m0), au);
+      // 16 rows x 16 columns of a strip [row / 8][4 column blocks]: stored [k][n]
+      const uint32_t o = (uint32_t)(((k / 8 + lane / 8 % 2) * 4 + cw / 8 + lane / 16) * 128 +
+                                    lane % 8 * 16);
+      ldsm4_t(sS + o, b);
+      mma(dq[0], ag, b[0], b[1]);
+      mma(dq[1], ag, b[2], b[3]);
+      mma(ve[0], av, b[0], b[1]);
+      mma(ve[1], av, b[2], b[3]);
+      ldsm4_t(sE + o, b);
+      mma(dk[0], au, b[0], b[1]);
+      mma(dk[1], au, b[2], b[3]);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        dq[x][y] *= a.scale * gi[y / 2];
+        dk[x][y] = re[y / 2] * dk[x][y] - gi[y / 2] * ve[x][y];
+      }
+    __syncthreads();  // the strip has been read
+    if (tid == 0 && s + 1 < D / 32) {
+      mbar_arrive_expect_tx(&bar[1], 2 * L::STRIP);
+      bulk_load(pS, a.S0 + at * D * D + (s + 1) * (D * 32), L::STRIP, &bar[1]);
+      bulk_load(pE, a.E + at * D * D + (s + 1) * (D * 32), L::STRIP, &bar[1]);
+    }
+#pragma unroll
+    for (int k = 0; k < kC; k += 16) {
+      uint32_t aa[4], at_[4], am[4], bk[4], bq[4];
+      ldsm4(sA + sw(kC, m0 + kn_r, k + kn_c), aa);
+      // the transpose of A: rows are its columns
+      ldsm4_t(sA + sw(kC, k + nk_r, m0 + nk_c), at_);
+      ldsm4(sM + sw(kC, m0 + kn_r, k + kn_c), am);
+      ldsm4_t(sK + sw(kC, k + kn_r, cs + kn_c), bk);
+      ldsm4_t(sQ + sw(kC, k + kn_r, cs + kn_c), bq);
+      mma(dq[0], aa, bk[0], bk[1]);
+      mma(dq[1], aa, bk[2], bk[3]);
+      mma(dk[0], at_, bq[0], bq[1]);
+      mma(dk[1], at_, bq[2], bq[3]);
+      mma(dk[0], am, bk[0], bk[1]);
+      mma(dk[1], am, bk[2], bk[3]);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = m0 + row + 8 * y;
+        if (i >= c.len) continue;
+        const int64_t t = c.t0 + i;
+        if (a.pq != nullptr) {
+          const int64_t o = t * a.H * D + h * D + cs + x * 8 + col;
+          *reinterpret_cast<float2*>(a.pq + o) = make_float2(dq[x][2 * y], dq[x][2 * y + 1]);
+          *reinterpret_cast<float2*>(a.pk + o) = make_float2(dk[x][2 * y], dk[x][2 * y + 1]);
+        } else {
+          const int64_t o = t * a.Hk * D + h * D + cs + x * 8 + col;
+          *reinterpret_cast<uint32_t*>(a.dQ + o) = pack_bf16x2(dq[x][2 * y], dq[x][2 * y + 1]);
+          *reinterpret_cast<uint32_t*>(a.dK + o) = pack_bf16x2(dk[x][2 * y], dk[x][2 * y + 1]);
+        }
+      }
+  }
+  if (!ok) {  // a wait gave up: the copies must land before the block is gone
+    volatile int never = 0;
+    mbar_wait(&bar[0], 0, &never, a.err, kErrWaitFinal);
+    mbar_wait(&bar[1], (uint32_t)((D / 32 - 1) & 1), &never, a.err, kErrWaitFinal);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// delta_gates_kernel: dlog_decay and dbeta of 512 tokens of a sequence and head
+// (from one anchor to the next): sums over the d / 16 groups of columns, and
+// the running sum from the stretch's end.
+// ----------------------------------------------------------------------------
+constexpr int kStretch = kC * kAnchor;
+constexpr int kStretchThreads = 128;
+
+struct GateArgs {
+  int64_t n;
+  const int64_t* offsets;
+  int64_t seqs;
+  int H, groups, ks;
+  const float *dots_o, *dots_v, *dots_x, *hold, *hold_last;  // hold_last: or nullptr (zeros)
+  float *dg, *db;
+};
+
+__global__ void __launch_bounds__(kStretchThreads) delta_gates_kernel(const GateArgs a) {
+  const int64_t slot = blockIdx.x;
+  const int h = blockIdx.y, tid = threadIdx.x;
+  // the sequence of this stretch
+  int64_t lo = 0, hi = a.seqs;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (seq_range(a.offsets, a.n, mid).t0 / kStretch + mid <= slot)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const SeqRange s = seq_range(a.offsets, a.n, lo);
+  const int64_t b0 = s.t0 + (slot - (s.t0 / kStretch + lo)) * kStretch;
+  if (b0 < s.t0 || b0 >= s.t1) return;
+  const int64_t b1 = b0 + kStretch < s.t1 ? b0 + kStretch : s.t1;
+  // <E, S> at the end: the next anchor's, or the last states'
+  const int parts = a.groups * a.ks;
+  const float* end = b1 < s.t1 ? a.hold + ((slot + 1) * a.H + h) * parts
+                     : a.hold_last != nullptr ? a.hold_last + (lo * a.H + h) * parts
+                                              : nullptr;
+  float x = 0.f;
+  if (end != nullptr)
+    for (int i = 0; i < parts; ++i) x += end[i];
+  constexpr int PER = kStretch / kStretchThreads;
+  float v[PER], sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int64_t t = b0 + tid * PER + q;
+    float o = 0.f, w = 0.f, b = 0.f;
+    if (t < b1) {
+      for (int r = 0; r < a.groups; ++r) {
+        const int64_t at = (r * (int64_t)a.H + h) * a.n + t;
+        o += a.dots_o[at];
+        w += a.dots_v[at];
+        b += a.dots_x[at];
+      }
+      a.db[t * a.H + h] = b;
+    }
+    v[q] = o - w;
+    sum += v[q];
+  }
+  // sums of the threads behind this one
+  __shared__ float warp_sum[kStretchThreads / 32];
+  const int lane = tid % 32, warp = tid / 32;
+  float behind = sum;
+  for (int m = 1; m < 32; m *= 2) {
+    const float y = __shfl_down_sync(0xffffffffu, behind, m);
+    if (lane + m < 32) behind += y;
+  }
+  if (lane == 0) warp_sum[warp] = behind;
+  __syncthreads();
+  behind -= sum;
+  for (int w = warp + 1; w < kStretchThreads / 32; ++w) behind += warp_sum[w];
+  x += behind;
+#pragma unroll
+  for (int q = PER - 1; q >= 0; --q) {
+    const int64_t t = b0 + tid * PER + q;
+    x += v[q];
+    if (t < b1) a.dg[t * a.H + h] = x;
+  }
+}
+
+// ----------------------------------------------------------------------------
+struct Plan {  // byte offsets in the workspace, and the whole
+  size_t blocks, S0, E, U, dVt, U32, anchors, last, dots_o, dots_v, dots_x, hold, hold_last, pq, pk,
+      total;
+};
+int64_t stretches(const DeltaArgs& a) { return a.n / kStretch + a.seqs; }
+Plan plan_of(const DeltaArgs& a) {
+  const size_t D = a.d, DD = D * D, ch = (size_t)chunk_slots(a) * a.H,
+               an = (size_t)stretches(a) * a.H, sq = (size_t)a.seqs * a.H, ks = 4;
+  Plan p;
+  size_t o = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes, 1024);
+    return at;
+  };
+  p.blocks = take(ch * chunk_bytes(3));
+  p.S0 = take(ch * DD * 2);
+  p.E = take(ch * DD * 2);
+  p.U = take(ch * kC * D * 2);
+  p.dVt = take(ch * kC * D * 2);
+  p.U32 = take(ch * kC * D * 4);
+  p.anchors = take(an * DD * 4);
+  p.last = take(sq * DD * 4);
+  p.dots_o = take(D / 16 * a.H * (size_t)a.n * 4);
+  p.dots_v = take(D / 16 * a.H * (size_t)a.n * 4);
+  p.dots_x = take(D / 16 * a.H * (size_t)a.n * 4);
+  p.hold = take(an * (D / 16) * ks * 4);
+  p.hold_last = take(sq * (D / 16) * ks * 4);
+  const size_t share = a.H == a.Hk ? 0 : (size_t)a.n * a.H * D * 4;
+  p.pq = take(share);
+  p.pk = take(share);
+  p.total = o;
+  return p;
+}
+
+struct Call {
+  const float* dS_out;
+  const void* dO;
+  void *dQ, *dK, *dV;
+  float *dg, *db, *dS_in;
+};
+
+template <int D, int KS, int RG>
+cudaError_t launch_reverse(const DeltaArgs& a, const Call& x, char* w, const Plan& p,
+                           const DeltaKept& kept, cudaStream_t st) {
+  using L = RK<D, KS, RG>;
+  CUtensorMap mQ = {}, mK = {}, mV = {}, mG = {};
+  if (a.n > 0 && (!head_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D, D) ||
+                  !head_map(&mK, a.K, a.n, a.ldk, a.Hk * D, D) ||
+                  !strip_map(&mV, a.V, a.n, a.ldv, a.H * D) ||
+                  !strip_map(&mG, x.dO, a.n, (int64_t)a.H * D, a.H * D)))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = ensure_smem_attr(delta_reverse_kernel<D, KS, RG>, L::SMEM);
+  if (e != cudaSuccess) return e;
+  const ReverseArgs k = {a.n, a.offsets, a.H, a.Hk, a.scale,
+                         reinterpret_cast<const uint8_t*>(w + p.blocks), kept, x.dS_out, x.dS_in,
+                         static_cast<__nv_bfloat16*>(x.dV),
+                         reinterpret_cast<__nv_bfloat16*>(w + p.E),
+                         reinterpret_cast<__nv_bfloat16*>(w + p.dVt),
+                         reinterpret_cast<float*>(w + p.dots_v),
+                         reinterpret_cast<float*>(w + p.dots_x), reinterpret_cast<float*>(w + p.hold),
+                         reinterpret_cast<float*>(w + p.hold_last), device_error_ptr()};
+  TraceScope ts("delta_reverse", st);
+  delta_reverse_kernel<D, KS, RG><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
+                                    L::THREADS, L::SMEM, st>>>(mQ, mK, mV, mG, k);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_tokens(const DeltaArgs& a, const Call& x, char* w, const Plan& p,
+                          cudaStream_t st) {
+  using L = GK<D>;
+  CUtensorMap mQ, mK, mG;
+  if (!head_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D, D) || !head_map(&mK, a.K, a.n, a.ldk, a.Hk * D, D) ||
+      !head_map(&mG, x.dO, a.n, (int64_t)a.H * D, a.H * D, D))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = ensure_smem_attr(delta_tokens_grad_kernel<D>, L::SMEM);
+  if (e != cudaSuccess) return e;
+  const bool own = a.H == a.Hk;
+  const TokensGradArgs k = {a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, a.g,
+                            reinterpret_cast<const __nv_bfloat16*>(w + p.S0),
+                            reinterpret_cast<const __nv_bfloat16*>(w + p.E),
+                            reinterpret_cast<const __nv_bfloat16*>(w + p.U),
+                            reinterpret_cast<const __nv_bfloat16*>(w + p.dVt),
+                            static_cast<__nv_bfloat16*>(x.dQ), static_cast<__nv_bfloat16*>(x.dK),
+                            own ? nullptr : reinterpret_cast<float*>(w + p.pq),
+                            own ? nullptr : reinterpret_cast<float*>(w + p.pk), device_error_ptr()};
+  TraceScope ts("delta_tokens_grad", st);
+  delta_tokens_grad_kernel<D><<<dim3((unsigned)chunk_slots(a), (unsigned)a.H), 32 * kGW, L::SMEM,
+                                st>>>(mQ, mK, mG, k);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t delta_grad_bytes(const DeltaArgs& a) { return plan_of(a).total; }
+
+cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, const float* dS_out,
+                       void* dQ, void* dK, void* dV, float* dg, float* db, float* dS_in, void* ws,
+                       cudaStream_t st) {
+  if (device_error_ptr() == nullptr) return cudaErrorInvalidDevice;
+  const Plan p = plan_of(a);
+  char* w = static_cast<char*>(ws);
+  uint8_t* blocks = reinterpret_cast<uint8_t*>(w + p.blocks);
+  const DeltaKept kept = {reinterpret_cast<__nv_bfloat16*>(w + p.S0),
+                          reinterpret_cast<__nv_bfloat16*>(w + p.U),
+                          reinterpret_cast<float*>(w + p.U32),
+                          reinterpret_cast<float*>(w + p.anchors),
+                          dS_out != nullptr ? reinterpret_cast<float*>(w + p.last) : nullptr,
+                          reinterpret_cast<float*>(w + p.dots_o)};
+  const Call x = {dS_out, dO, dQ, dK, dV, dg, db, dS_in};
+  cudaError_t e = delta_prepare(a, true, blocks, st);
+  if (e != cudaSuccess) return e;
+  e = delta_states_kept(a, S_in, dO, blocks, kept, st);
+  if (e != cudaSuccess) return e;
+  const bool few = delta_few_rows(a);
+  int ks = 4;
+  if (a.d == 64) {
+    e = few ? launch_reverse<64, 4, 1>(a, x, w, p, kept, st)
+            : launch_reverse<64, 2, 2>(a, x, w, p, kept, st);
+    if (!few) ks = 2;
+  } else if (a.d == 128) {
+    e = few ? launch_reverse<128, 4, 1>(a, x, w, p, kept, st)
+            : launch_reverse<128, 2, 2>(a, x, w, p, kept, st);
+    if (!few) ks = 2;
+  } else {
+    e = launch_reverse<256, 4, 1>(a, x, w, p, kept, st);
+  }
+  if (e != cudaSuccess || a.n == 0) return e;
+  e = a.d == 64    ? launch_tokens<64>(a, x, w, p, st)
+      : a.d == 128 ? launch_tokens<128>(a, x, w, p, st)
+                   : launch_tokens<256>(a, x, w, p, st);
+  if (e != cudaSuccess) return e;
+  const GateArgs k = {a.n, a.offsets, a.seqs, a.H, a.d / 16, ks,
+                      reinterpret_cast<const float*>(w + p.dots_o),
+                      reinterpret_cast<const float*>(w + p.dots_v),
+                      reinterpret_cast<const float*>(w + p.dots_x),
+                      reinterpret_cast<const float*>(w + p.hold),
+                      dS_out != nullptr ? reinterpret_cast<const float*>(w + p.hold_last) : nullptr,
+                      dg, db};
+  {
+    TraceScope ts("delta_gates", st);
+    delta_gates_kernel<<<dim3((unsigned)stretches(a), (unsigned)a.H), kStretchThreads, 0, st>>>(k);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess || a.H == a.Hk) return e;
+  return delta_share(a, reinterpret_cast<const float*>(w + p.pq),
+                     reinterpret_cast<const float*>(w + p.pk), dQ, dK, st);
+}
+
+}  // namespace ttt

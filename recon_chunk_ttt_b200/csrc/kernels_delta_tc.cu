@@ -94,10 +94,10 @@ __global__ void __launch_bounds__(kChunkThreads)
   } else if (warp == 1) {
     for (int j = lane; j < kC; j += 32) {
       float b = j < c.len ? a.b[(c.t0 + j) * a.H + h] : 0.f;
-      // The gradient divides U by beta.  A beta of nothing becomes 2^-100: the
+      // The gradient divides U by beta.  A beta of nothing becomes 2^-64: the
       // token's U is then that small (its part in any sum rounds away), but
       // U / beta has all its digits.
-      if (GRAD && j < c.len && fabsf(b) < 0x1p-100f) b = 0x1p-100f;
+      if (GRAD && j < c.len && fabsf(b) <= kNoBeta) b = kNoBeta;
       beta[j] = b;
     }
   }
@@ -238,19 +238,22 @@ __global__ void __launch_bounds__(kChunkThreads)
 // add to it (measured: 1 + 0.75 ulp stays 1), so small parts are summed apart
 // from large ones, and the state takes one fp32 addition a chunk.
 // ----------------------------------------------------------------------------
-template <int D, int KS, int RG>
+template <int D, int KS, int RG, bool GRAD>
 struct SK {
   static constexpr int WARPS = KS * RG;
   static constexpr int KQ = kC * D * 2;               // one of K, Q
-  static constexpr int BLOCK = chunk_bytes(1);
-  static constexpr int V = kC * 32;                   // 16 columns
-  static constexpr int STAGE = 2 * KQ + RG * V + BLOCK;
+  static constexpr int BLOCK = chunk_bytes(GRAD ? 3 : 1);
+  static constexpr int V = kC * 32;                   // 16 columns of V (or dO)
+  static constexpr int STAGE = KQ + (GRAD ? 2 : 1) * RG * V + BLOCK;
   // exchange of a group: partial r, partial o (each warp's for the others'
   // tiles), r in parts, u in parts
-  static constexpr int X_PART = 8 * (KS - 1) * 32 * 16, X_R = 8 * 3 * 32 * 8, X_U = 8 * 5 * 32 * 8;
+  static constexpr int U_PARTS = GRAD ? 6 : 5;
+  static constexpr int X_PART = 8 * (KS - 1) * 32 * 16, X_R = 8 * 3 * 32 * 8,
+                       X_U = 8 * U_PARTS * 32 * 8;
   static constexpr int X = 2 * X_PART + X_R + X_U;
   static constexpr int THREADS = 32 * (WARPS + 1);
-  static constexpr int OFF_X = 2 * STAGE;
+  static constexpr int OFF_Q = 2 * STAGE;             // Q is free again early in a step: one stage
+  static constexpr int OFF_X = OFF_Q + KQ;
   static constexpr int OFF_BAR = OFF_X + RG * X;
   static constexpr int SMEM = OFF_BAR + 192 + 1024;
   static_assert((KS == 2 || KS == 4) && RG <= 2, "tiles and barriers of a group");
@@ -267,21 +270,25 @@ struct StateArgs {
   const float* S_in;
   float* S_out;
   __nv_bfloat16* O;
+  DeltaKept kept;  // for the gradient
   int* err;
 };
 
-template <int D, int KS, int RG>
-__global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
+template <int D, int KS, int RG, bool GRAD>
+__global__ void __launch_bounds__(SK<D, KS, RG, GRAD>::THREADS, 1)
     delta_state_kernel(const __grid_constant__ CUtensorMap mQ,
                        const __grid_constant__ CUtensorMap mK,
-                       const __grid_constant__ CUtensorMap mV, const StateArgs a) {
-  using L = SK<D, KS, RG>;
+                       const __grid_constant__ CUtensorMap mV,
+                       const __grid_constant__ CUtensorMap mG, const StateArgs a) {
+  using L = SK<D, KS, RG, GRAD>;
   constexpr int DK = D / KS, NT = 8 / KS;  // a warp's columns of S; its token tiles of r, u, o
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* empty = full + 2;
-  uint64_t* met = empty + 2;  // 3 for each group: partial sums, r, u are written
+  uint64_t* qfull = empty + 2;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* met = qempty + 1;  // 3 for each group: partial sums, r, u are written
   volatile int* abort_flag = reinterpret_cast<volatile int*>(met + 3 * RG);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int h = blockIdx.y, hk = h / (a.H / a.Hk);
@@ -295,6 +302,8 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], L::WARPS);
     }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, L::WARPS);
     for (int i = 0; i < 3 * RG; ++i) mbar_init(&met[i], KS);
     *abort_flag = 0;
     fence_mbar_init();
@@ -303,7 +312,7 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
 
   if (warp == L::WARPS) {  // ------------------------------------------------ loads
     if (lane == 0) {
-      int64_t issued = 0;
+      int64_t issued = 0, q_issued = 0;
       for (int64_t c = 0; c < nc; ++c) {
         const int s = (int)(c & 1);
         if (!mbar_wait(&empty[s], (uint32_t)((c >> 1) & 1) ^ 1, abort_flag, a.err, kErrWaitEmpty))
@@ -312,15 +321,21 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
         const int t = (int)(sr.t0 + c * kC);
         mbar_arrive_expect_tx(&full[s], L::STAGE);
         tma_load_3d(st, &mK, &full[s], 0, t, hk * (D / 64));
-        tma_load_3d(st + L::KQ, &mQ, &full[s], 0, t, hk * (D / 64));
-        for (int g = 0; g < RG; ++g)
-          tma_load_2d(st + 2 * L::KQ + g * L::V, &mV, &full[s],
-                      h * D + ((int)blockIdx.x * RG + g) * 16, t);
-        bulk_load(st + 2 * L::KQ + RG * L::V,
+        for (int g = 0; g < RG; ++g) {
+          const int x = h * D + ((int)blockIdx.x * RG + g) * 16;
+          tma_load_2d(st + L::KQ + g * L::V, &mV, &full[s], x, t);
+          if (GRAD) tma_load_2d(st + L::KQ + (RG + g) * L::V, &mG, &full[s], x, t);
+        }
+        bulk_load(st + L::STAGE - L::BLOCK,
                   a.blocks + ((sr.slot + c) * a.H + h) * (int64_t)L::BLOCK, L::BLOCK, &full[s]);
         ++issued;
+        if (!mbar_wait(qempty, (uint32_t)(c & 1) ^ 1, abort_flag, a.err, kErrWaitEmpty)) break;
+        mbar_arrive_expect_tx(qfull, L::KQ);
+        tma_load_3d(smem + L::OFF_Q, &mQ, qfull, 0, t, hk * (D / 64));
+        ++q_issued;
       }
       drain_ring(full, 2, issued, a.err);
+      drain_ring(qfull, 1, q_issued, a.err);
     }
     return;
   }
@@ -370,16 +385,23 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
                                            kErrWaitFull)))
       break;
     uint8_t* base = smem + st * L::STAGE;
-    uint8_t* vp = base + 2 * L::KQ + grp * L::V;
-    const uint32_t sK = smem_u32(base), sQ = sK + L::KQ, sV = smem_u32(vp),
-                   sT = sK + 2 * L::KQ + RG * L::V, sP = sT + 3 * kTri;
-    const float* gates =
-        reinterpret_cast<const float*>(base + 2 * L::KQ + RG * L::V + 4 * kTri);
+    uint8_t* vp = base + L::KQ + grp * L::V;
+    const uint32_t sK = smem_u32(base), sQ = smem_u32(smem + L::OFF_Q), sV = smem_u32(vp),
+                   sT = sK + L::STAGE - L::BLOCK, sP = sT + 3 * kTri;
+    const float* gates = reinterpret_cast<const float*>(base + L::STAGE - kGates);
+    const int64_t at = (sr.slot + c) * a.H + h;  // this chunk's place among the kept arrays
     const int valid = len - c * kC < kC ? (int)(len - c * kC) : kC;
 
-    // r = S K^T (three parts of S), o = S Q^T (two), both [16 rows x 64 tokens], over this
+    if (GRAD) {
+      keep_state<D, DK>(a.kept.S0 + at * D * D, s, r0, c0, lane);
+      if (c % kAnchor == 0)
+        keep_anchor(a.kept.anchors + ((sr.t0 / (kC * kAnchor) + seq + c / kAnchor) * a.H + h) *
+                                         (int64_t)D * D, s, ((r0 / 16) * KS + kw) * (DK / 8), lane);
+    }
+
+    // r = S K^T (three parts of S), o = S Q^T (two; for the gradient three), both [16 rows x 64 tokens], over this
     // warp's columns of S.  The parts of r are sent off before the turn to o.
-    uint32_t sh[DK / 16][4], sm[DK / 16][4];
+    uint32_t sh[DK / 16][4], sm[DK / 16][4], sl[GRAD ? DK / 16 : 1][4];
     float rt[NT][4], ot[NT][4];  // this warp's tiles of the group's sums
     {
       float r[8][4] = {}, rs[8][4] = {};  // of the first part of S, of the small ones
@@ -387,7 +409,7 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
       ldsm4(sK + sw(kC, nk_r, c0 + nk_c * 8), b[0]);
 #pragma unroll
       for (int k = 0; k < DK / 16; ++k) {
-        uint32_t lo[4];
+        uint32_t(&lo)[4] = sl[GRAD ? k : 0];
         split_a(s[2 * k], s[2 * k + 1], sh[k], sm[k], lo);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
@@ -425,16 +447,33 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
     {
       float o[8][4] = {};
       uint32_t b[2][4];
-      ldsm4(sQ + sw(kC, nk_r, c0 + nk_c * 8), b[0]);
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(qfull, (uint32_t)(c & 1), abort_flag, a.err, kErrWaitFull)))
+        break;
 #pragma unroll
-      for (int e = 0; e < DK / 4; ++e) {  // 4 pairs of tiles for each 16 columns
-        const int k = e / 4, p = e % 4, f = e + 1;
-        if (f < DK / 4) ldsm4(sQ + sw(kC, f % 4 * 16 + nk_r, c0 + f / 4 * 16 + nk_c * 8), b[f % 2]);
-        mma(o[2 * p], sh[k], b[e % 2][0], b[e % 2][1]);
-        mma(o[2 * p + 1], sh[k], b[e % 2][2], b[e % 2][3]);
-        mma(o[2 * p], sm[k], b[e % 2][0], b[e % 2][1]);
-        mma(o[2 * p + 1], sm[k], b[e % 2][2], b[e % 2][3]);
+      for (int pass = GRAD ? 0 : 1; pass < 2; ++pass) {  // small parts first
+        ldsm4(sQ + sw(kC, nk_r, c0 + nk_c * 8), b[0]);
+#pragma unroll
+        for (int e = 0; e < DK / 4; ++e) {  // 4 pairs of tiles for each 16 columns
+          const int k = e / 4, p = e % 4, f = e + 1;
+          if (f < DK / 4)
+            ldsm4(sQ + sw(kC, f % 4 * 16 + nk_r, c0 + f / 4 * 16 + nk_c * 8), b[f % 2]);
+          uint32_t(&x)[4] = b[e % 2];
+          if (pass == 0) {
+            mma(o[2 * p], sl[GRAD ? k : 0], x[0], x[1]);
+            mma(o[2 * p + 1], sl[GRAD ? k : 0], x[2], x[3]);
+          } else {
+            mma(o[2 * p], sh[k], x[0], x[1]);
+            mma(o[2 * p + 1], sh[k], x[2], x[3]);
+          }
+          if (pass == (GRAD ? 0 : 1)) {
+            mma(o[2 * p], sm[k], x[0], x[1]);
+            mma(o[2 * p + 1], sm[k], x[2], x[3]);
+          }
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qempty);
       float4* xp = reinterpret_cast<float4*>(x_part + L::X_PART);
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -543,11 +582,17 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
     for (int j = 0; j < NT; ++j) {
       const int t = tile(j);
       uint32_t hi[2], mid[2], lo[2];
-      uint2* d = reinterpret_cast<uint2*>(xu) + (t / 2 * 5 * 32 + lane) * 2 + t % 2;
+      uint2* d = reinterpret_cast<uint2*>(xu) + (t / 2 * L::U_PARTS * 32 + lane) * 2 + t % 2;
       split3(ut[j][0], ut[j][1], hi[0], mid[0], lo[0]);
       split3(ut[j][2], ut[j][3], hi[1], mid[1], lo[1]);
       d[0] = make_uint2(hi[0], hi[1]);
       d[64] = make_uint2(mid[0], mid[1]);
+      if (GRAD) {
+        d[320] = make_uint2(lo[0], lo[1]);
+        keep_tile<D>(a.kept.U + at * kC * D, ut[j], r0, t, lane);
+        reinterpret_cast<float4*>(a.kept.U32)[((at * (D / 16) + r0 / 16) * 8 + t) * 32 + lane] =
+            make_float4(ut[j][0], ut[j][1], ut[j][2], ut[j][3]);
+      }
       const float2 re = *reinterpret_cast<const float2*>(gates + kC + t * 8 + col);
       split3(ut[j][0] * re.x, ut[j][1] * re.y, hi[0], mid[0], lo[0]);
       split3(ut[j][2] * re.x, ut[j][3] * re.y, hi[1], mid[1], lo[1]);
@@ -565,51 +610,87 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
       for (int y = 0; y < 4; ++y) ot[j][y] *= a.scale * (y % 2 ? ga.y : ga.x);
     }
     if (!wait(2, c)) break;
+    float os[GRAD ? NT : 1][4] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (k > tile(NT - 1) / 2) break;
-      uint32_t hi[4], mid[4];
-      load_a(xu + k * 5 * 32 + lane, hi);
-      load_a(xu + k * 5 * 32 + 32 + lane, mid);
+      uint32_t hi[4], mid[4], lo[4];
+      load_a(xu + k * L::U_PARTS * 32 + lane, hi);
+      load_a(xu + k * L::U_PARTS * 32 + 32 + lane, mid);
+      if (GRAD) load_a(xu + k * L::U_PARTS * 32 + 160 + lane, lo);
 #pragma unroll
       for (int p = 0; p < NT / 2; ++p) {
         if (k > tile(2 * p + 1) / 2) continue;
         uint32_t b[4];
         const int tr = pair_row(p) < 16 * k ? 16 * k : pair_row(p);
-        ldsm4(sP + tri(tr, k * 16 + nk_c * 8), b);
+        const uint32_t from = sP + tri(tr, k * 16 + nk_c * 8);
+        ldsm4(from, b);
         const bool first = k <= tile(2 * p) / 2;
+        float(&s0)[4] = GRAD ? os[GRAD ? 2 * p : 0] : ot[2 * p];
+        float(&s1)[4] = GRAD ? os[GRAD ? 2 * p + 1 : 0] : ot[2 * p + 1];
         mma(ot[2 * p + 1], hi, b[2], b[3]);
         if (first) mma(ot[2 * p], hi, b[0], b[1]);
-        mma(ot[2 * p + 1], mid, b[2], b[3]);
-        if (first) mma(ot[2 * p], mid, b[0], b[1]);
+        mma(s1, mid, b[2], b[3]);
+        if (first) mma(s0, mid, b[0], b[1]);
+        if (GRAD) {
+          mma(s1, lo, b[2], b[3]);
+          if (first) mma(s0, lo, b[0], b[1]);
+          ldsm4(from + kTri, b);
+          mma(s1, hi, b[2], b[3]);
+          if (first) mma(s0, hi, b[0], b[1]);
+          mma(s1, mid, b[2], b[3]);
+          if (first) mma(s0, mid, b[0], b[1]);
+          ldsm4(from + 2 * kTri, b);
+          mma(s1, hi, b[2], b[3]);
+          if (first) mma(s0, hi, b[0], b[1]);
+        }
       }
     }
-    // O over this group's V (each warp over the tokens it has read), then out
+    if (GRAD) {
+      // this group's share of dO . O, for the gradient of the decays
+      const uint32_t sG = sV + RG * L::V;
 #pragma unroll
-    for (int p = 0; p < NT / 2; ++p) {
-      const uint32_t w[4] = {pack_bf16x2(ot[2 * p][0], ot[2 * p][1]),
-                             pack_bf16x2(ot[2 * p][2], ot[2 * p][3]),
-                             pack_bf16x2(ot[2 * p + 1][0], ot[2 * p + 1][1]),
-                             pack_bf16x2(ot[2 * p + 1][2], ot[2 * p + 1][3])};
-      stsm4_t(sV + sw32(pair_row(p), nk_c), w);
-    }
-    __syncwarp();
+      for (int p = 0; p < NT / 2; ++p) {
+        uint32_t w[4];
+        ldsm4_t(sG + sw32(pair_row(p), nk_c), w);
 #pragma unroll
-    for (int p = 0; p < NT / 2; ++p) {
-      const int t = tile(2 * p + lane / 16) * 8 + lane / 2 % 8;
-      const uint4 w = *reinterpret_cast<const uint4*>(vp + sw32(t, lane % 2));
-      if (t < valid)
-        *reinterpret_cast<uint4*>(a.O + (sr.t0 + c * kC + t) * (int64_t)a.H * D + h * D + r0 +
-                                  (lane % 2) * 8) = w;
+        for (int x = 0; x < 2; ++x) {
+          const int j = 2 * p + x;
+          float y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = ot[j][q] + os[GRAD ? j : 0][q];
+          put_dots(a.kept.dots + ((r0 / 16) * (int64_t)a.H + h) * a.n + sr.t0 + c * kC + tile(j) * 8,
+                   dot_pair(y, w[2 * x], w[2 * x + 1]), tile(j) * 8, valid, lane);
+        }
+      }
+    } else {
+      // O over this group's V (each warp over the tokens it has read), then out
+#pragma unroll
+      for (int p = 0; p < NT / 2; ++p) {
+        const uint32_t w[4] = {pack_bf16x2(ot[2 * p][0], ot[2 * p][1]),
+                               pack_bf16x2(ot[2 * p][2], ot[2 * p][3]),
+                               pack_bf16x2(ot[2 * p + 1][0], ot[2 * p + 1][1]),
+                               pack_bf16x2(ot[2 * p + 1][2], ot[2 * p + 1][3])};
+        stsm4_t(sV + sw32(pair_row(p), nk_c), w);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int p = 0; p < NT / 2; ++p) {
+        const int t = tile(2 * p + lane / 16) * 8 + lane / 2 % 8;
+        const uint4 w = *reinterpret_cast<const uint4*>(vp + sw32(t, lane % 2));
+        if (t < valid)
+          *reinterpret_cast<uint4*>(a.O + (sr.t0 + c * kC + t) * (int64_t)a.H * D + h * D + r0 +
+                                    (lane % 2) * 8) = w;
+      }
     }
     // S = gamma_64 S + (rest u) K
     {
       uint32_t hi[4][4], mid[4][4], lo[4][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        load_a(xu + k * 5 * 32 + 64 + lane, hi[k]);
-        load_a(xu + k * 5 * 32 + 96 + lane, mid[k]);
-        load_a(xu + k * 5 * 32 + 128 + lane, lo[k]);
+        load_a(xu + k * L::U_PARTS * 32 + 64 + lane, hi[k]);
+        load_a(xu + k * L::U_PARTS * 32 + 96 + lane, mid[k]);
+        load_a(xu + k * L::U_PARTS * 32 + 128 + lane, lo[k]);
       }
       const float gl = gates[kC - 1];
       // Rows of K behind the sequence may hold anything: they count as zero here, where
@@ -654,6 +735,9 @@ __global__ void __launch_bounds__(SK<D, KS, RG>::THREADS, 1)
     if (lane == 0) mbar_arrive(&empty[st]);
   }
 
+  if (GRAD && a.kept.last != nullptr)
+    keep_anchor(a.kept.last + (seq * a.H + h) * (int64_t)D * D, s, ((r0 / 16) * KS + kw) * (DK / 8),
+                lane);
   if (a.S_out != nullptr) {
     float* So = a.S_out + ((seq * a.H + h) * D + r0) * (int64_t)D + c0;
 #pragma unroll
@@ -678,25 +762,41 @@ cudaError_t launch_chunks(const DeltaArgs& a, uint8_t* blocks, cudaStream_t st) 
   return cudaGetLastError();
 }
 
-template <int D, int KS, int RG>
+template <int D, int KS, int RG, bool GRAD>
 cudaError_t launch_state(const DeltaArgs& a, const float* S_in, float* S_out, void* O,
-                         const uint8_t* blocks, cudaStream_t st) {
-  using L = SK<D, KS, RG>;
+                         const uint8_t* blocks, const void* dO, const DeltaKept* kept,
+                         cudaStream_t st) {
+  using L = SK<D, KS, RG, GRAD>;
   int* err = device_error_ptr();
   if (err == nullptr) return cudaErrorInvalidDevice;
-  CUtensorMap mQ = {}, mK = {}, mV = {};
+  CUtensorMap mQ = {}, mK = {}, mV = {}, mG = {};
   if (a.n > 0 && (!head_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D, D) ||
                   !head_map(&mK, a.K, a.n, a.ldk, a.Hk * D, D) ||
-                  !strip_map(&mV, a.V, a.n, a.ldv, a.H * D)))
+                  !strip_map(&mV, a.V, a.n, a.ldv, a.H * D) ||
+                  (GRAD && !strip_map(&mG, dO, a.n, (int64_t)a.H * D, a.H * D))))
     return cudaErrorInvalidValue;
-  const cudaError_t e = ensure_smem_attr(delta_state_kernel<D, KS, RG>, L::SMEM);
+  const cudaError_t e = ensure_smem_attr(delta_state_kernel<D, KS, RG, GRAD>, L::SMEM);
   if (e != cudaSuccess) return e;
-  const StateArgs k = {a.n, a.offsets, a.H, a.Hk, a.scale, blocks, S_in, S_out,
-                       static_cast<__nv_bfloat16*>(O), err};
-  TraceScope ts("delta_state", st);
-  delta_state_kernel<D, KS, RG><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
-                                  L::THREADS, L::SMEM, st>>>(mQ, mK, mV, k);
+  const StateArgs k = {a.n,  a.offsets, a.H,   a.Hk, a.scale, blocks, S_in, S_out,
+                       static_cast<__nv_bfloat16*>(O), kept ? *kept : DeltaKept{}, err};
+  TraceScope ts(GRAD ? "delta_state_kept" : "delta_state", st);
+  delta_state_kernel<D, KS, RG, GRAD><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
+                                        L::THREADS, L::SMEM, st>>>(mQ, mK, mV, mG, k);
   return cudaGetLastError();
+}
+
+template <bool GRAD>
+cudaError_t state_by_size(const DeltaArgs& a, const float* S_in, float* S_out, void* O,
+                          const uint8_t* blocks, const void* dO, const DeltaKept* kept,
+                          cudaStream_t st) {
+  const bool few = delta_few_rows(a);
+  if (a.d == 64)
+    return few ? launch_state<64, 4, 1, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st)
+               : launch_state<64, 2, 2, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
+  if (a.d == 128)
+    return few ? launch_state<128, 4, 1, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st)
+               : launch_state<128, 2, 2, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
+  return launch_state<256, 4, 1, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
 }
 
 }  // namespace
@@ -721,18 +821,18 @@ cudaError_t delta_tc(const DeltaArgs& a, const float* S_in, float* S_out, void* 
   uint8_t* blocks = static_cast<uint8_t*>(ws);
   const cudaError_t e = delta_prepare(a, false, blocks, st);
   if (e != cudaSuccess) return e;
-  // Groups of 16 rows of S.  Where there are no more of them than SMs, four warps
-  // share each (one on each quarter of an SM: 74 us against 97 us for a 1,374-token
-  // sequence of 4 heads of 256); else two do, with half the exchange for each product
-  // (16,411 tokens, 13 sequences, 16 heads of 128: 457 us against 596 us).
-  const bool few = a.seqs * a.H * (a.d / 16) <= num_sms();
-  if (a.d == 64)
-    return few ? launch_state<64, 4, 1>(a, S_in, S_out, O, blocks, st)
-               : launch_state<64, 2, 2>(a, S_in, S_out, O, blocks, st);
-  if (a.d == 128)
-    return few ? launch_state<128, 4, 1>(a, S_in, S_out, O, blocks, st)
-               : launch_state<128, 2, 2>(a, S_in, S_out, O, blocks, st);
-  return launch_state<256, 4, 1>(a, S_in, S_out, O, blocks, st);
+  return state_by_size<false>(a, S_in, S_out, O, blocks, nullptr, nullptr, st);
+}
+
+// Groups of 16 rows of S.  Where there are no more of them than SMs, four warps
+// share each (one on each quarter of an SM: 74 us against 97 us for a 1,374-token
+// sequence of 4 heads of 256); else two do, with half the exchange for each product
+// (16,411 tokens, 13 sequences, 16 heads of 128: 457 us against 596 us).
+bool delta_few_rows(const DeltaArgs& a) { return a.seqs * a.H * (a.d / 16) <= num_sms(); }
+
+cudaError_t delta_states_kept(const DeltaArgs& a, const float* S_in, const void* dO,
+                              const uint8_t* blocks, const DeltaKept& kept, cudaStream_t st) {
+  return state_by_size<true>(a, S_in, nullptr, nullptr, blocks, dO, &kept, st);
 }
 
 }  // namespace ttt

@@ -4,7 +4,7 @@
 //
 // Bound by memory: forward reads x and writes y, backward reads x and dy and
 // writes dx, each once.  A row lies in the registers of a group of threads
-// (a warp, 4 or 16 of them), so the mean, then the squares about the mean, then
+// (1, 4 or 16 warps), so the mean, then the squares about the mean, then
 // the result are taken from one read.  In the backward kernel a thread keeps
 // its columns' sums of dy and dy xh in registers over all rows of its block;
 // the blocks' sums meet in the workspace and a second kernel adds them in
@@ -61,6 +61,32 @@ struct Ld<__nv_bfloat16, 1> {
   static __device__ __forceinline__ void put(__nv_bfloat16* p, const float* x) {
     *p = __float2bfloat16_rn(x[0]);
   }
+};
+// A vector as it lies in memory: what waits in registers for its turn.
+template <typename T, int V>
+struct Raw {
+  uint4 v;
+  __device__ __forceinline__ void get(const T* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void none() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void unpack(float* x) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (V == 8) {
+        x[2 * i % V] = __uint_as_float(w[i] << 16);
+        x[(2 * i + 1) % V] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        x[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T v;
+  __device__ __forceinline__ void get(const T* p) { v = *p; }
+  __device__ __forceinline__ void none() { v = T(0.f); }
+  __device__ __forceinline__ void unpack(float* x) const { x[0] = (float)v; }
 };
 // w, b: floats, as many as the token vector holds
 template <int V>
@@ -174,57 +200,123 @@ __global__ void __launch_bounds__(512)
   if (stats != nullptr && threadIdx.x == 0) stats[2 * row] = mean, stats[2 * row + 1] = rstd;
 }
 
+// Sums of N values over the G threads of a group at once; one barrier.
+template <int G, int N>
+__device__ __forceinline__ void group_sums(float (&x)[N], float (*red)[G / 32]) {
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], m);
+  if (G > 32) {
+    if (threadIdx.x % 32 == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[i][threadIdx.x / 32] = x[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) x[i] += red[i][w];
+    }
+  }
+}
+
 // One block's sums over its rows, columns in place: part[2][blocks][dim], dw then db.
-template <typename T, int V, int G, int NV, bool COLS>
+// A group takes R rows at a time, whose 2 R sums share a barrier; the next R rows
+// are loaded meanwhile.  Rows wait as they lie in memory and are unpacked when
+// they are used (twice): registers for rows in flight, not for their conversion.
+template <typename T, int V, int G, int NV, int R, bool COLS>
 __global__ void __launch_bounds__(block_of(G))
     norm_backward_kernel(const T* X, int64_t ldx, const T* dY, int64_t lddy, int64_t rows, int dim,
                          const float* __restrict__ w, const float* __restrict__ stats, T* dX,
                          float* part) {
-  constexpr int RB = block_of(G) / G;  // rows a block works on at a time
-  __shared__ float red[2][2][G / 32];
-  extern __shared__ float cols[];  // [RB > 1 ? dim : 0]
+  constexpr int GR = block_of(G) / G;  // groups of a block
+  __shared__ float red[2][2 * R][G / 32];
+  extern __shared__ float cols[];  // [GR > 1 ? dim : 0]
   const int l = threadIdx.x % G, nv = dim / V;
   const float inv = 1.f / dim;
-  float aw[COLS ? NV : 1][V] = {}, ab[COLS ? NV : 1][V] = {};
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RB + threadIdx.x / G; row < rows;
-       row += (int64_t)gridDim.x * RB) {
-    const float mean = stats[2 * row], rstd = stats[2 * row + 1];
-    float xh[NV][V], g[NV][V], s1 = 0.f, s2 = 0.f;
+  float aw[COLS ? NV : 1][V] = {}, ab[COLS ? NV : 1][V] = {}, ww[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (l + i * G < nv) {
-        Ld<T, V>::get(X + row * ldx + (l + i * G) * V, xh[i]);
-        Ld<T, V>::get(dY + row * lddy + (l + i * G) * V, g[i]);
-      }
+  for (int i = 0; i < NV; ++i) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (l + i * G < nv) {
-        float ww[V];
-        if (w != nullptr) get_f<V>(w + (l + i * G) * V, ww);
+    for (int c = 0; c < V; ++c) ww[i][c] = 1.f;
+    if (w != nullptr && l + i * G < nv) get_f<V>(w + (l + i * G) * V, ww[i]);
+  }
+  struct Rows {
+    Raw<T, V> x[R][NV], g[R][NV];
+    float mean[R], rstd[R];
+  };
+  const auto load = [&](Rows& n, int64_t row) {
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-          xh[i][c] = (xh[i][c] - mean) * rstd;
-          if (COLS) {
-            aw[i][c] = fmaf(g[i][c], xh[i][c], aw[i][c]);
-            ab[i][c] += g[i][c];
-          }
-          if (w != nullptr) g[i][c] *= ww[c];
-          s1 += g[i][c];
-          s2 = fmaf(g[i][c], xh[i][c], s2);
+    for (int r = 0; r < R; ++r) {
+      const bool live = row + r < rows;
+      n.mean[r] = live ? stats[2 * (row + r)] : 0.f;
+      n.rstd[r] = live ? stats[2 * (row + r) + 1] : 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (live && l + i * G < nv) {
+          n.x[r][i].get(X + (row + r) * ldx + (l + i * G) * V);
+          n.g[r][i].get(dY + (row + r) * lddy + (l + i * G) * V);
+        } else {
+          n.x[r][i].none();
+          n.g[r][i].none();
         }
-      }
-    if (dX == nullptr) continue;  // the same for the whole grid
-    s1 = group_sum<G>(s1, red[turn][0]) * inv;
-    s2 = group_sum<G>(s2, red[turn][1]) * inv;
-    turn ^= 1;
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * GR * R;
+  int64_t row = ((int64_t)blockIdx.x * GR + threadIdx.x / G) * R;
+  Rows now, next;
+  load(now, row);
+  int turn = 0;
+  for (; row < rows; row += step) {
+    // in place is in order: dX's rows are this step's, the loads the next one's
+    load(next, row + step);
+    float sums[2 * R];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (l + i * G < nv) {
+    for (int r = 0; r < R; ++r) {
+      float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-        for (int c = 0; c < V; ++c) g[i][c] = rstd * (g[i][c] - s1 - xh[i][c] * s2);
-        Ld<T, V>::put(dX + row * dim + (l + i * G) * V, g[i]);
-      }
+      for (int i = 0; i < NV; ++i)
+        if (l + i * G < nv) {
+          float x[V], g[V];
+          now.x[r][i].unpack(x);
+          now.g[r][i].unpack(g);
+#pragma unroll
+          for (int c = 0; c < V; ++c) {
+            x[c] = (x[c] - now.mean[r]) * now.rstd[r];
+            if (COLS) {
+              aw[i][c] = fmaf(g[c], x[c], aw[i][c]);
+              ab[i][c] += g[c];
+            }
+            g[c] *= ww[i][c];
+            s1 += g[c];
+            s2 = fmaf(g[c], x[c], s2);
+          }
+        }
+      sums[2 * r] = s1;
+      sums[2 * r + 1] = s2;
+    }
+    if (dX != nullptr) {  // the same for the whole grid
+      group_sums<G, 2 * R>(sums, red[turn]);
+      turn ^= 1;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (row + r < rows && l + i * G < nv) {
+            float x[V], g[V];
+            now.x[r][i].unpack(x);
+            now.g[r][i].unpack(g);
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+              x[c] = (x[c] - now.mean[r]) * now.rstd[r];
+              g[c] = now.rstd[r] *
+                     (g[c] * ww[i][c] - sums[2 * r] * inv - x[c] * (sums[2 * r + 1] * inv));
+            }
+            Ld<T, V>::put(dX + (row + r) * dim + (l + i * G) * V, g);
+          }
+    }
+    now = next;
   }
   if (COLS) {
     float* pw = part + (size_t)blockIdx.x * dim;
@@ -232,14 +324,14 @@ __global__ void __launch_bounds__(block_of(G))
     for (int which = 0; which < 2; ++which) {
       float(&acc)[COLS ? NV : 1][V] = which == 0 ? aw : ab;
       float* out = which == 0 ? pw : pb;
-      if (RB == 1) {
+      if (GR == 1) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (l + i * G < nv)
 #pragma unroll
             for (int c = 0; c < V; ++c) out[(l + i * G) * V + c] = acc[i][c];
-      } else {  // the block's warps in turn
-        for (int r = 0; r < RB; ++r) {
+      } else {  // the block's groups in turn
+        for (int r = 0; r < GR; ++r) {
           if ((int)threadIdx.x / G == r)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -305,101 +397,153 @@ __global__ void __launch_bounds__(256)
   part[((size_t)gridDim.y + blockIdx.y) * dim + c] = sb;
 }
 
-// dw, db = the blocks' sums, added in order: 32 columns a block, 8 rows of
-// threads take every 8th block's sum, then their 8 sums in order.
-__global__ void __launch_bounds__(256)
+// dw, db = the blocks' sums, added in order: 32 columns a block, 32 rows of
+// threads take every 32nd block's sum, then their 32 sums in order.
+__global__ void __launch_bounds__(1024)
     norm_columns_kernel(const float* __restrict__ part, int blocks, int dim, float* dw, float* db) {
-  __shared__ float red[8][32];
+  __shared__ float red[32][33];
   float* out = blockIdx.y == 0 ? dw : db;
   if (out == nullptr) return;
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
+  const int x = threadIdx.x % 32, r = threadIdx.x / 32, c = blockIdx.x * 32 + x;
   const float* p = part + (size_t)blockIdx.y * blocks * dim + c;
   float s = 0.f;
   if (c < dim)
-    for (int k = r; k < blocks; k += 8) s += p[(size_t)k * dim];
-  red[r][threadIdx.x % 32] = s;
+#pragma unroll 4
+    for (int k = r; k < blocks; k += 32) s += p[(size_t)k * dim];
+  red[r][x] = s;
   __syncthreads();
   if (r == 0 && c < dim) {
-    for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) s += red[k][x];
     out[c] = s;
   }
 }
 
-// How a row is laid over threads: G threads, NV vectors of V values each.  The
-// smallest group that holds the row in at most 4 vectors a thread (registers:
-// 32 values; the backward kernel keeps 4 such arrays), except the largest
-// group, which takes up to 8.  G = 0: too wide.
+// How a row is laid over threads: G threads, NV vectors of V values each (R rows at
+// a time, backward).  G = 0: too wide for registers.
 struct Shape {
-  int V, G, NV;
+  int V, G, NV, R;
 };
-Shape shape_of(const NormArgs& a, bool aligned) {
-  Shape s;
+int vector_of(const NormArgs& a, bool aligned) {
   const int full = a.bf16 ? 8 : 4;
-  s.V = aligned && a.dim % full == 0 ? full : 1;
-  const int64_t nv = (a.dim + s.V - 1) / s.V;
-  s.G = nv <= 32 * 4 ? 32 : nv <= 128 * 4 ? 128 : nv <= 512 * 8 ? 512 : 0;
-  if (s.G == 512 && s.V == 8 && nv > 512 * 4) s.G = 0;
+  return aligned && a.dim % full == 0 ? full : 1;
+}
+int pow2_at_least(int64_t x) {
+  int p = 1;
+  while (p < x) p *= 2;
+  return p;
+}
+// Forward: rows in flight are what counts (a row's time is a chain of latencies),
+// so few registers: a warp for each row up to 32 values a lane (16 where they are
+// loaded one by one), then 4 warps, then 16; few rows take the larger group that
+// still has a vector for every thread.
+Shape forward_shape(const NormArgs& a, bool aligned) {
+  Shape s = {vector_of(a, aligned), 0, 0, 1};
+  const int64_t nv = a.dim / s.V;
+  const int64_t most = (s.V == 1 ? 16 : 32) / s.V;
+  s.G = nv <= 32 * most ? 32 : nv <= 128 * most ? 128 : nv <= 512 * most ? 512 : 0;
   if (s.G == 0) return s;
-  const int64_t per = (nv + s.G - 1) / s.G;
-  s.NV = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8;
+  while (s.G < 512 && a.rows * (s.G / 32) < 148 * 8 && nv >= s.G * 4) s.G *= 4;
+  s.NV = pow2_at_least((nv + s.G - 1) / s.G);
+  return s;
+}
+// Backward: a thread holds its columns' two sums and the weight besides, so at most
+// 8 to 16 values, and R rows so that 32 values are in flight.
+constexpr int rows_at_once(int nv, int v) {
+  const int r = (v == 1 ? 16 : 32) / (nv * v);  // single values take a register each
+  return r < 1 ? 1 : r > 4 ? 4 : r;
+}
+Shape backward_shape(const NormArgs& a, bool aligned) {
+  Shape s = {vector_of(a, aligned), 0, 0, 1};
+  const int64_t nv = a.dim / s.V;
+  const int most = 16 / s.V;  // vectors a thread: 16 values (fp32: 4 vectors, bf16: 2)
+  s.G = nv <= 32 * most ? 32 : nv <= 128 * most ? 128 : nv <= 512 * most ? 512 : 0;
+  if (s.G == 0) return s;
+  s.NV = pow2_at_least((nv + s.G - 1) / s.G);
+  s.R = rows_at_once(s.NV, s.V);
   return s;
 }
 
-bool vector_rows(const NormArgs& a, const void* X, int64_t ldx, const void* Y, int64_t ldy) {
-  const int full = a.bf16 ? 8 : 4;
-  (void)X, (void)Y;  // 16-byte aligned, checked at the entry
+bool vector_rows(const NormArgs& a, int64_t ldx, int64_t ldy) {
+  const int full = a.bf16 ? 8 : 4;  // the pointers are 16-byte aligned, checked at the entry
   return ldx % full == 0 && ldy % full == 0;
 }
 
-constexpr int kBlocksPerSM = 8;
-
 // Blocks of the backward kernel (and the rows of its partial sums).
 int backward_blocks(const NormArgs& a, const Shape& s) {
-  const int rb = s.G == 32 ? 8 : 1;
+  const int64_t rb = (s.G == 32 ? 8 : 1) * s.R;
   const int64_t need = (a.rows + rb - 1) / rb;
-  const int64_t most = 148 * (s.G == 512 ? 2 : s.G == 128 ? kBlocksPerSM : 3);
+  const int64_t most = 148 * (s.G == 512 ? 2 : s.G == 128 ? 5 : 3);
   return (int)(need < most ? (need < 1 ? 1 : need) : most);
 }
 int wide_blocks(const NormArgs& a) { return (int)(a.rows < 64 ? (a.rows < 1 ? 1 : a.rows) : 64); }
 
+struct Forward {
+  const void* X;
+  int64_t ldx;
+  const float *w, *b;
+  void* Y;
+  float* stats;
+};
 template <typename T, int V, int G, int NV>
-cudaError_t launch_forward(const NormArgs& a, const void* X, int64_t ldx, const float* w,
-                           const float* b, void* Y, float* stats, cudaStream_t st) {
+cudaError_t launch_forward(const NormArgs& a, const Forward& f, cudaStream_t st) {
   constexpr int rb = block_of(G) / G;
   norm_kernel<T, V, G, NV><<<(unsigned)((a.rows + rb - 1) / rb), block_of(G), 0, st>>>(
-      static_cast<const T*>(X), ldx, a.rows, (int)a.dim, a.eps, w, b, static_cast<T*>(Y), stats);
+      static_cast<const T*>(f.X), f.ldx, a.rows, (int)a.dim, a.eps, f.w, f.b,
+      static_cast<T*>(f.Y), f.stats);
   return cudaGetLastError();
 }
+// NV = 1, 2, 4, .. MOST
+template <typename T, int V, int G, int MOST, int NV = 1>
+cudaError_t forward_by_nv(int nv, const NormArgs& a, const Forward& f, cudaStream_t st) {
+  if constexpr (NV < MOST)
+    if (nv > NV) return forward_by_nv<T, V, G, MOST, 2 * NV>(nv, a, f, st);
+  return launch_forward<T, V, G, NV>(a, f, st);
+}
+template <typename T, int V>
+cudaError_t forward_by_g(const Shape& s, const NormArgs& a, const Forward& f, cudaStream_t st) {
+  constexpr int MOST = (V == 1 ? 16 : 32) / V;
+  return s.G == 32    ? forward_by_nv<T, V, 32, MOST>(s.NV, a, f, st)
+         : s.G == 128 ? forward_by_nv<T, V, 128, MOST>(s.NV, a, f, st)
+                      : forward_by_nv<T, V, 512, MOST>(s.NV, a, f, st);
+}
 
+struct Backward {
+  const void* X;
+  int64_t ldx;
+  const void* dY;
+  int64_t lddy;
+  const float *w, *stats;
+  void* dX;
+  float* part;
+  int blocks;
+};
 template <typename T, int V, int G, int NV>
-cudaError_t launch_backward(const NormArgs& a, const void* X, int64_t ldx, const void* dY,
-                            int64_t lddy, const float* w, const float* stats, void* dX,
-                            float* part, int blocks, cudaStream_t st) {
-  const int smem = G == 32 && part != nullptr ? (int)a.dim * 4 : 0;
-  if (part != nullptr)
-    norm_backward_kernel<T, V, G, NV, true><<<blocks, block_of(G), smem, st>>>(
-        static_cast<const T*>(X), ldx, static_cast<const T*>(dY), lddy, a.rows, (int)a.dim, w,
-        stats, static_cast<T*>(dX), part);
-  else
-    norm_backward_kernel<T, V, G, NV, false><<<blocks, block_of(G), 0, st>>>(
-        static_cast<const T*>(X), ldx, static_cast<const T*>(dY), lddy, a.rows, (int)a.dim, w,
-        stats, static_cast<T*>(dX), part);
-  return cudaGetLastError();
+cudaError_t launch_backward(const NormArgs& a, const Backward& b, cudaStream_t st) {
+  constexpr int R = rows_at_once(NV, V);
+  const auto go = [&](auto kernel, int smem) {
+    kernel<<<b.blocks, block_of(G), smem, st>>>(static_cast<const T*>(b.X), b.ldx,
+                                                static_cast<const T*>(b.dY), b.lddy, a.rows,
+                                                (int)a.dim, b.w, b.stats, static_cast<T*>(b.dX),
+                                                b.part);
+    return cudaGetLastError();
+  };
+  if (b.part != nullptr)
+    return go(norm_backward_kernel<T, V, G, NV, R, true>, G == 32 ? (int)a.dim * 4 : 0);
+  return go(norm_backward_kernel<T, V, G, NV, R, false>, 0);
 }
-
-// f(T, V, G, NV) for a shape.
-#define TTT_NORM_NV(T, V, G, CALL)       \
-  (s.NV == 1   ? CALL<T, V, G, 1> NORM_ARGS   \
-   : s.NV == 2 ? CALL<T, V, G, 2> NORM_ARGS   \
-               : CALL<T, V, G, 4> NORM_ARGS)
-#define TTT_NORM_G(T, V, CALL)                                  \
-  (s.G == 32    ? TTT_NORM_NV(T, V, 32, CALL)                   \
-   : s.G == 128 ? TTT_NORM_NV(T, V, 128, CALL)                  \
-   : s.NV == 8  ? CALL<T, V == 8 ? 1 : V, 512, 8> NORM_ARGS     \
-                : TTT_NORM_NV(T, V, 512, CALL))
-#define TTT_NORM(CALL)                                                                  \
-  (a.bf16 ? (s.V == 8 ? TTT_NORM_G(__nv_bfloat16, 8, CALL) : TTT_NORM_G(__nv_bfloat16, 1, CALL)) \
-          : (s.V == 4 ? TTT_NORM_G(float, 4, CALL) : TTT_NORM_G(float, 1, CALL)))
+template <typename T, int V, int G, int NV = 1>
+cudaError_t backward_by_nv(int nv, const NormArgs& a, const Backward& b, cudaStream_t st) {
+  if constexpr (NV < 16 / V)
+    if (nv > NV) return backward_by_nv<T, V, G, 2 * NV>(nv, a, b, st);
+  return launch_backward<T, V, G, NV>(a, b, st);
+}
+template <typename T, int V>
+cudaError_t backward_by_g(const Shape& s, const NormArgs& a, const Backward& b, cudaStream_t st) {
+  return s.G == 32    ? backward_by_nv<T, V, 32>(s.NV, a, b, st)
+         : s.G == 128 ? backward_by_nv<T, V, 128>(s.NV, a, b, st)
+                      : backward_by_nv<T, V, 512>(s.NV, a, b, st);
+}
 
 }  // namespace
 
@@ -407,7 +551,7 @@ size_t norm_workspace_bytes(const NormArgs& a) {
   // the largest of the plans that strides may ask for
   size_t most = (size_t)wide_blocks(a);
   for (int aligned = 0; aligned < 2; ++aligned) {
-    const Shape s = shape_of(a, aligned != 0);
+    const Shape s = backward_shape(a, aligned != 0);
     if (s.G != 0 && (size_t)backward_blocks(a, s) > most) most = (size_t)backward_blocks(a, s);
   }
   return most * 2 * (size_t)a.dim * 4;
@@ -416,7 +560,7 @@ size_t norm_workspace_bytes(const NormArgs& a) {
 cudaError_t norm_forward(const NormArgs& a, const void* X, int64_t ldx, const float* w,
                          const float* b, void* Y, float* stats, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
-  const Shape s = shape_of(a, vector_rows(a, X, ldx, Y, a.dim));
+  const Shape s = forward_shape(a, vector_rows(a, ldx, a.dim));
   TraceScope ts("layer_norm", st);
   if (s.G == 0) {
     if (a.bf16)
@@ -429,9 +573,11 @@ cudaError_t norm_forward(const NormArgs& a, const void* X, int64_t ldx, const fl
                                                          static_cast<float*>(Y), stats);
     return cudaGetLastError();
   }
-#define NORM_ARGS (a, X, ldx, w, b, Y, stats, st)
-  return TTT_NORM(launch_forward);
-#undef NORM_ARGS
+  const Forward f = {X, ldx, w, b, Y, stats};
+  if (a.bf16)
+    return s.V == 8 ? forward_by_g<__nv_bfloat16, 8>(s, a, f, st)
+                    : forward_by_g<__nv_bfloat16, 1>(s, a, f, st);
+  return s.V == 4 ? forward_by_g<float, 4>(s, a, f, st) : forward_by_g<float, 1>(s, a, f, st);
 }
 
 cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const void* dY,
@@ -444,7 +590,7 @@ cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const v
     if (e == cudaSuccess && db != nullptr) e = cudaMemsetAsync(db, 0, (size_t)a.dim * 4, st);
     return e;
   }
-  const Shape s = shape_of(a, vector_rows(a, X, ldx, dY, lddy));
+  const Shape s = backward_shape(a, vector_rows(a, ldx, lddy));
   float* part = cols ? static_cast<float*>(ws) : nullptr;
   cudaError_t e = cudaSuccess;
   int blocks;
@@ -475,13 +621,16 @@ cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const v
   } else {
     blocks = backward_blocks(a, s);
     TraceScope ts("layer_norm_backward", st);
-#define NORM_ARGS (a, X, ldx, dY, lddy, w, stats, dX, part, blocks, st)
-    e = TTT_NORM(launch_backward);
-#undef NORM_ARGS
+    const Backward b = {X, ldx, dY, lddy, w, stats, dX, part, blocks};
+    if (a.bf16)
+      e = s.V == 8 ? backward_by_g<__nv_bfloat16, 8>(s, a, b, st)
+                   : backward_by_g<__nv_bfloat16, 1>(s, a, b, st);
+    else
+      e = s.V == 4 ? backward_by_g<float, 4>(s, a, b, st) : backward_by_g<float, 1>(s, a, b, st);
   }
   if (e != cudaSuccess || !cols) return e;
   TraceScope ts("layer_norm_columns", st);
-  norm_columns_kernel<<<dim3((unsigned)((a.dim + 31) / 32), 2), 256, 0, st>>>(part, blocks,
+  norm_columns_kernel<<<dim3((unsigned)((a.dim + 31) / 32), 2), 1024, 0, st>>>(part, blocks,
                                                                               (int)a.dim, dw, db);
   return cudaGetLastError();
 }

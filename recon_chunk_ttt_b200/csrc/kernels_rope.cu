@@ -2,11 +2,13 @@
 // position * frequency, (x, y) -> (x cos - y sin, y cos + x sin).
 //
 // Bound by memory: q and k are read and written once.  The angles depend on
-// the token and the pair alone, so a block forms the d/2 sines and cosines of
-// each of its tokens once, in shared memory, and all heads of q and k use
-// them.  Angles are taken in turns (position * frequency / 2 pi) in fp64 and
-// reduced there (t - rint(t)), so far positions keep all of fp32's bits; the
-// reduced angle goes through sincospi in fp32.
+// the token and the pair alone, so a block forms the sines and cosines of its
+// tokens once, in shared memory, and all heads of q and k use them; a thread's
+// first loads are on their way meanwhile.  Angles are taken in turns (position
+// * frequency / 2 pi) in fixed point: a position is a 24-bit integer times a
+// power of two, a frequency 64 bits of a turn; of their product the whole turns
+// fall off and the next 32 bits stay, however far the position (error below
+// 2^-32 turns = 1.5e-9).  The angle goes through sincospi in fp32.
 
 #include <cuda_bf16.h>
 
@@ -24,8 +26,7 @@ constexpr int kMaxPairs = 128;
 constexpr int kTok = 8;  // tokens of a block, at most: 8 KB of angles
 
 struct RopeParams {
-  double turns[kMaxPairs];   // turns per unit of position, by pair
-  unsigned char axis[kMaxPairs];
+  uint64_t turns[kMaxPairs];  // by pair: turns per unit of position * 2^64; the axis in the last 2 bits
   const void* X[2];  // q, k
   void* Y[2];
   int64_t ld[2], ldo[2];
@@ -33,6 +34,8 @@ struct RopeParams {
   const float* pos;
   int64_t n;
   int pairs;  // rotated pairs (R / 2)
+  int per;    // items of a head: what a thread takes at a time
+  uint32_t per_inv, row_inv, pair_inv;  // 2^32 / x + 1 of per, heads * per, pairs: for e / x
   float sign;
 };
 
@@ -67,8 +70,23 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-__device__ __forceinline__ float2 turn(float2 cs, float x, float y) {
-  return make_float2(x * cs.x - y * cs.y, y * cs.x + x * cs.y);
+__device__ __forceinline__ float2 turn(float c, float s, float x, float y) {
+  return make_float2(x * c - y * s, y * c + x * s);
+}
+// N angles' values from shared memory, 16 bytes at a time where there are as many: lanes
+// side by side read side by side (cosines and sines interleaved would not).
+template <int N>
+__device__ __forceinline__ void angles(const float* p, float* x) {
+  if (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    }
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x, x[1] = v.y;
+  }
 }
 
 __device__ __forceinline__ float ld1(const float* p) { return *p; }
@@ -76,86 +94,154 @@ __device__ __forceinline__ float ld1(const __nv_bfloat16* p) { return __bfloat16
 __device__ __forceinline__ void st1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// PAIRS: values 2j, 2j+1; a 16-byte vector holds whole pairs.  Otherwise (HALF)
-// a thread takes the vector at j and the one at j + pairs; where the half is
-// no multiple of the vector (VEC = false) it takes single values.
+// A value of the parameters by a lane's own index, through its generic address: as a
+// constant, 32 indexes would be 32 reads one after another (84% of that unit's time
+// before; 194 us against 142 us for 137,400 tokens of 10 heads of 128).
+__device__ __forceinline__ uint64_t table(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.u64 %0, [%1];" : "=l"(v) : "l"(p));
+  return v;
+}
+
+// position * turns, reduced to [-1/2, 1/2) turns, times 2.
+__device__ __forceinline__ float half_turns(float pos, uint64_t turns) {
+  const uint32_t bits = __float_as_uint(pos), ex = bits >> 23 & 255;
+  if (ex == 255) return __int_as_float(0x7fffffff);  // infinity, NaN
+  const uint32_t m = (bits & 0x7fffff) | (ex != 0 ? 0x800000 : 0);
+  const int e = (ex != 0 ? (int)ex : 1) - 150;  // |pos| = m 2^e
+  // m * turns = (b 2^32 + low) 2^-64 turns
+  const uint64_t a = (uint64_t)m * (uint32_t)turns;
+  const uint64_t b = (uint64_t)m * (uint32_t)(turns >> 32) + (a >> 32);
+  uint32_t f;
+  if (e <= 0)
+    f = e > -64 ? (uint32_t)(b >> -e) : 0;
+  else
+    f = e < 64 ? (uint32_t)(((b << 32 | (uint32_t)a) << e) >> 32) : 0;
+  if (bits >> 31) f = 0u - f;
+  return (float)(int32_t)f * 0x1p-31f;
+}
+
+// An item is PAIRS: a 16-byte vector (whole pairs); else (HALF) the vector at j
+// and the one at j + pairs, then vectors that pass; where the half is no multiple of
+// the vector (VEC = false) the same with single values.
 template <typename T, int D, bool PAIRS, bool VEC>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p,
-                                                        int tok) {
-  __shared__ float2 cs[kTok][D / 2];
+__global__ void __launch_bounds__(kThreads)
+    rope_kernel(const __grid_constant__ RopeParams p, int tok) {
+  constexpr int N = Vec<T>::N, BATCH = 4;
+  __shared__ __align__(16) float cosines[kTok][D / 2], sines[kTok][D / 2];
   const int64_t t0 = (int64_t)blockIdx.x * tok;
   const int m = p.n - t0 < tok ? (int)(p.n - t0) : tok;
-  for (int e = threadIdx.x; e < m * p.pairs; e += kThreads) {
-    const int t = e / p.pairs, j = e % p.pairs;
-    const double a = (double)p.pos[(t0 + t) * 3 + p.axis[j]] * p.turns[j];
-    float s, c;
-    sincospif((float)(2.0 * (a - rint(a))), &s, &c);
-    cs[t][j] = make_float2(c, p.sign * s);
-  }
-  __syncthreads();
-  constexpr int N = Vec<T>::N;
-  const int half = p.pairs;
-  // items of a head: PAIRS d/N vectors; HALF half/N pairs of vectors, then the
-  // vectors (or single values) that pass
-  const int per = PAIRS ? D / N : VEC ? half / N + (D - 2 * half) / N : half + (D - 2 * half);
-  const int heads = p.heads[0] + p.heads[1];
-  for (int e = threadIdx.x; e < m * heads * per; e += kThreads) {
-    const int i = e % per, hh = e / per % heads, t = e / per / heads;
-    const int w = hh >= p.heads[0], h = w ? hh - p.heads[0] : hh;
-    const T* x = static_cast<const T*>(p.X[w]) + (t0 + t) * p.ld[w] + h * D;
-    T* y = static_cast<T*>(p.Y[w]) + (t0 + t) * p.ldo[w] + h * D;
+  const int half = p.pairs, row = (p.heads[0] + p.heads[1]) * p.per, total = m * row;
+
+  struct Item {
+    int t, i;  // token, item of the head (-1: none)
+    const T* x;
+    T* y;
+    uint4 lo, hi;
+  };
+  const auto load = [&](Item& it, int e) {
+    it.i = -1;
+    if (e >= total) return;
+    it.t = (int)__umulhi((uint32_t)e, p.row_inv);
+    const int f = e - it.t * row;
+    int hh = (int)__umulhi((uint32_t)f, p.per_inv);
+    it.i = f - hh * p.per;
+    const int w = hh >= p.heads[0];
+    if (w) hh -= p.heads[0];
+    it.x = static_cast<const T*>(w ? p.X[1] : p.X[0]) + (t0 + it.t) * (w ? p.ld[1] : p.ld[0]) + hh * D;
+    it.y = static_cast<T*>(w ? p.Y[1] : p.Y[0]) + (t0 + it.t) * (w ? p.ldo[1] : p.ldo[0]) + hh * D;
     if (PAIRS) {
-      const uint4 in = *reinterpret_cast<const uint4*>(x + i * N);
-      float a[N];
-      Vec<T>::unpack(in, a);
-#pragma unroll
-      for (int c = 0; c < N; c += 2)
-        if (i * (N / 2) + c / 2 < half) {
-          const float2 r = turn(cs[t][i * (N / 2) + c / 2], a[c], a[c + 1]);
-          a[c] = r.x, a[c + 1] = r.y;
-        }
-      *reinterpret_cast<uint4*>(y + i * N) = Vec<T>::pack(a);
+      it.lo = *reinterpret_cast<const uint4*>(it.x + it.i * N);
     } else if (VEC) {
-      if (i < half / N) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(x + i * N);
-        const uint4 hi = *reinterpret_cast<const uint4*>(x + half + i * N);
-        float a[N], b[N];
-        Vec<T>::unpack(lo, a);
-        Vec<T>::unpack(hi, b);
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-          const float2 r = turn(cs[t][i * N + c], a[c], b[c]);
-          a[c] = r.x, b[c] = r.y;
-        }
-        *reinterpret_cast<uint4*>(y + i * N) = Vec<T>::pack(a);
-        *reinterpret_cast<uint4*>(y + half + i * N) = Vec<T>::pack(b);
+      if (it.i < half / N) {
+        it.lo = *reinterpret_cast<const uint4*>(it.x + it.i * N);
+        it.hi = *reinterpret_cast<const uint4*>(it.x + half + it.i * N);
       } else {
-        const int c = 2 * half + (i - half / N) * N;
-        *reinterpret_cast<uint4*>(y + c) = *reinterpret_cast<const uint4*>(x + c);
-      }
-    } else {
-      if (i < half) {
-        const float2 r = turn(cs[t][i], ld1(x + i), ld1(x + half + i));
-        st1(y + i, r.x);
-        st1(y + half + i, r.y);
-      } else {
-        y[half + i] = x[half + i];
+        it.lo = *reinterpret_cast<const uint4*>(it.x + half + it.i * N);
       }
     }
+  };
+  const auto finish = [&](const Item& it) {
+    if (it.i < 0) return;
+    if (PAIRS) {
+      float a[N], cs[N / 2], sn[N / 2];
+      Vec<T>::unpack(it.lo, a);
+      if (it.i * (N / 2) < half) {
+        angles<N / 2>(&cosines[it.t][it.i * (N / 2)], cs);
+        angles<N / 2>(&sines[it.t][it.i * (N / 2)], sn);
+#pragma unroll
+        for (int c = 0; c < N / 2; ++c)
+          if (it.i * (N / 2) + c < half) {
+            const float2 r = turn(cs[c], sn[c], a[2 * c], a[2 * c + 1]);
+            a[2 * c] = r.x, a[2 * c + 1] = r.y;
+          }
+      }
+      *reinterpret_cast<uint4*>(it.y + it.i * N) = Vec<T>::pack(a);
+    } else if (VEC) {
+      if (it.i < half / N) {
+        float a[N], b[N], cs[N], sn[N];
+        Vec<T>::unpack(it.lo, a);
+        Vec<T>::unpack(it.hi, b);
+        angles<N>(&cosines[it.t][it.i * N], cs);
+        angles<N>(&sines[it.t][it.i * N], sn);
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const float2 r = turn(cs[c], sn[c], a[c], b[c]);
+          a[c] = r.x, b[c] = r.y;
+        }
+        *reinterpret_cast<uint4*>(it.y + it.i * N) = Vec<T>::pack(a);
+        *reinterpret_cast<uint4*>(it.y + half + it.i * N) = Vec<T>::pack(b);
+      } else {
+        *reinterpret_cast<uint4*>(it.y + half + it.i * N) = it.lo;
+      }
+    } else if (it.i < half) {
+      const float2 r = turn(cosines[it.t][it.i], sines[it.t][it.i], ld1(it.x + it.i),
+                            ld1(it.x + half + it.i));
+      st1(it.y + it.i, r.x);
+      st1(it.y + half + it.i, r.y);
+    } else {
+      it.y[half + it.i] = it.x[half + it.i];
+    }
+  };
+
+  Item items[BATCH];
+#pragma unroll
+  for (int b = 0; b < BATCH; ++b) load(items[b], threadIdx.x + b * kThreads);
+  for (int e = threadIdx.x; e < m * half; e += kThreads) {
+    const int t = (int)__umulhi((uint32_t)e, p.pair_inv), j = e - t * half;
+    float s, c;
+    const uint64_t f = table(&p.turns[j]);
+    sincospif(half_turns(p.pos[(t0 + t) * 3 + (f & 3)], f), &s, &c);
+    cosines[t][j] = c;
+    sines[t][j] = p.sign * s;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < total; e += BATCH * kThreads) {
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) finish(items[b]);
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) load(items[b], e + (BATCH + b) * kThreads);
   }
 }
 
 template <typename T, int D>
-cudaError_t launch(const RopeParams& p, bool pairs, cudaStream_t st) {
-  // tokens of a block: enough values for four vectors a thread, but blocks
-  // for the whole GPU first
-  const int64_t vecs = (int64_t)(p.heads[0] + p.heads[1]) * D / Vec<T>::N;
-  int64_t tok = 4 * kThreads / vecs;
+cudaError_t launch(RopeParams& p, bool pairs, cudaStream_t st) {
+  constexpr int N = Vec<T>::N;
+  const bool vec = p.pairs % N == 0;
+  const int unit = pairs || vec ? N : 1;
+  p.per = pairs ? D / N : (D - p.pairs) / unit;
+  const int64_t row = (int64_t)(p.heads[0] + p.heads[1]) * p.per;
+  p.per_inv = (uint32_t)((1ull << 32) / p.per + 1);
+  p.row_inv = (uint32_t)((1ull << 32) / row + 1);
+  p.pair_inv = (uint32_t)((1ull << 32) / p.pairs + 1);
+  // tokens of a block: four items a thread, but blocks for the whole GPU first.  (One
+  // token may have more items than 2^16, where e / row = 0 all the same and e / per stays
+  // exact: per <= 192 and e < 2^21 keep the product's error below 1 / per.)
+  int64_t tok = 4 * kThreads / row;
   if (tok > p.n / (148 * 4)) tok = p.n / (148 * 4);
   tok = tok < 1 ? 1 : tok > kTok ? kTok : tok;
   const unsigned grid = (unsigned)((p.n + tok - 1) / tok);
   TraceScope ts("rope", st);
-  const bool vec = p.pairs % Vec<T>::N == 0;
   if (pairs)
     rope_kernel<T, D, true, true><<<grid, kThreads, 0, st>>>(p, (int)tok);
   else if (vec)
@@ -175,8 +261,9 @@ cudaError_t rope(const RopeArgs& a, cudaStream_t st) {
   for (int x = 0; x < 3; ++x)
     for (int i = 0; i < a.rot[x] / 2; ++i, ++j) {
       const double e = a.head_freq ? 2.0 * j / total : 2.0 * i / a.rot[x];
-      p.turns[j] = std::pow((double)a.base[x], -e) / 6.283185307179586476925;
-      p.axis[j] = (unsigned char)x;
+      // base >= 1: less than a sixth of a turn
+      const double turns = std::pow((double)a.base[x], -e) / 6.283185307179586476925;
+      p.turns[j] = ((uint64_t)std::llrint(std::ldexp(turns, 62)) << 2) | (uint64_t)x;
     }
   p.X[0] = a.Q, p.X[1] = a.K, p.Y[0] = a.Qo, p.Y[1] = a.Ko;
   p.ld[0] = a.ldq, p.ld[1] = a.ldk, p.ldo[0] = a.ldqo, p.ldo[1] = a.ldko;

@@ -39,6 +39,12 @@ size_t delta_tc_bytes(const DeltaArgs& a);
 cudaError_t delta_tc(const DeltaArgs& a, const float* S_in, float* S_out, void* O, void* ws,
                      cudaStream_t st);
 
+// Its gradient (kernels_delta_grad.cu).
+size_t delta_grad_bytes(const DeltaArgs& a);
+cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, const float* dS_out,
+                       void* dQ, void* dK, void* dV, float* dg, float* db, float* dS_in, void* ws,
+                       cudaStream_t st);
+
 // ---- rotary positions (kernels_rope.cu) --------------------------------------
 struct RopeArgs {
   int d, rot[3];

@@ -71,8 +71,9 @@ def test_delta_outputs_and_workspace_refused():
     c, t = _cfg(), _tok()
     assert _chunk(c, t, O=None) == R.TTT_ERR_INVALID_ARG
     assert _chunk(c, t, S_in=P + 4) == R.TTT_ERR_ALIGNMENT
-    assert _chunk(c, t, ws=None) == R.TTT_ERR_WORKSPACE
-    need = R.ttt_delta_workspace_bytes(c, 10)
+    assert _chunk(c, _tok(n=100), ws=None) == R.TTT_ERR_WORKSPACE
+    t = _tok(n=100)
+    need = R.ttt_delta_workspace_bytes(c, 100)
     assert need > 0 and _chunk(c, t, nbytes=need - 1) == R.TTT_ERR_WORKSPACE
     back = [P] * 10
     for i in (1, 3, 4, 5, 6, 7):  # dO, dQ, dK, dV, dlog_decay, dbeta
@@ -80,7 +81,7 @@ def test_delta_outputs_and_workspace_refused():
         a[i] = None
         assert L.ttt_delta_backward(ctypes.byref(c), ctypes.byref(t), *a, 1 << 40, None) == \
             R.TTT_ERR_INVALID_ARG
-    need = R.ttt_delta_workspace_bytes(c, 10, 1, True)
+    need = R.ttt_delta_workspace_bytes(c, 100, 1, True)
     assert L.ttt_delta_backward(ctypes.byref(c), ctypes.byref(t), *back, need - 1, None) == \
         R.TTT_ERR_WORKSPACE
 
@@ -108,7 +109,7 @@ def _rope(cfg, Q=P, ldq=256, hq=2, K=P, ldk=256, hk=2, pos=P, n=5, Qo=2 * P, ldq
 @pytest.mark.parametrize("bad,want", [
     (dict(rot=(31, 32, 32)), R.TTT_ERR_INVALID_ARG), (dict(rot=(0, 0, 0)), R.TTT_ERR_INVALID_ARG),
     (dict(rot=(64, 64, 2)), R.TTT_ERR_INVALID_ARG), (dict(rot=(-2, 64, 2)), R.TTT_ERR_INVALID_ARG),
-    (dict(base=0.0), R.TTT_ERR_INVALID_ARG), (dict(base=float("inf")), R.TTT_ERR_INVALID_ARG),
+    (dict(base=0.5), R.TTT_ERR_INVALID_ARG), (dict(base=float("inf")), R.TTT_ERR_INVALID_ARG),
     (dict(layout=2), R.TTT_ERR_INVALID_ARG), (dict(freq=-1), R.TTT_ERR_INVALID_ARG),
     (dict(d=80), R.TTT_ERR_UNSUPPORTED_SHAPE), (dict(precision=3), R.TTT_ERR_INVALID_ARG)])
 def test_rope_config_refused(bad, want):

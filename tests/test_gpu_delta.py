@@ -406,17 +406,17 @@ def test_graphs_and_streams(prec):
 
 
 def test_binding_refusals():
-    H, d, n = 2, 64, 10
+    H, d, n = 2, 64, 100
     x, S, dO, _ = _inputs(1, n, H, H, d, BF)
     cfg = R.make_delta_config(H, d)
     bad = [dict(Q=x["Q"].float()), dict(V=x["V"][:5]), dict(beta=x["beta"].t()),
            dict(K=x["K"].t().contiguous().t()), dict(log_decay=x["log_decay"].cpu()),
-           dict(S=S.double()), dict(S=S[:, :1]), dict(offsets=torch.tensor([0, 10]))]
+           dict(S=S.double()), dict(S=S[:, :1]), dict(offsets=torch.tensor([0, 100]))]
     for b in bad:
         with pytest.raises(R.TTTError):
             R.ttt_delta_chunk(cfg, **{**x, **b})
     with pytest.raises(R.TTTError):
         R.ttt_delta_chunk(cfg, **x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(R.TTTError):
-        R.ttt_delta_step(cfg, **x, S=S)  # 10 requests, one state
+        R.ttt_delta_step(cfg, **x, S=S)  # 100 requests, one state
     assert np.isfinite(R.ttt_delta_chunk(cfg, **x, S=S)[0].float().cpu().numpy()).all()
