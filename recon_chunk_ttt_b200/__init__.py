@@ -41,9 +41,10 @@ _OPS_EXPORTS = {
 
 def __getattr__(name):
     if name in _EXPORTS:
-        from . import _binding
-        return getattr(_binding, name)
-    if name in _OPS_EXPORTS:
-        from . import _ops
-        return getattr(_ops, name)
-    raise AttributeError(name)
+        from . import _binding as module
+    elif name in _OPS_EXPORTS:
+        from . import _ops as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)  # found directly from now on
+    return value

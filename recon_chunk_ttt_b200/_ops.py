@@ -126,7 +126,7 @@ def _run(what, dev, fn, args, stream):
         with torch.cuda.device(dev):
             return _run(what, dev, fn, args, stream)
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     status = fn(*args, stream)

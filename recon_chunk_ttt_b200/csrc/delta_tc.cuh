@@ -230,6 +230,17 @@ __device__ __forceinline__ void put_dots(float* to, float2 x, int t, int valid, 
 }
 
 inline int64_t chunk_slots(const DeltaArgs& a) { return a.n / kC + a.seqs; }
+// In front of the blocks: the sequences' ranking by length, for up to kRanked of
+// them (more fill the GPU in any order).
+constexpr int kRanked = 512;
+constexpr int kOrderBytes = kRanked * 4;
+inline size_t blocks_bytes(const DeltaArgs& a, int p_parts) {
+  return kOrderBytes + (size_t)chunk_slots(a) * a.H * chunk_bytes(p_parts);
+}
+inline int32_t* order_of(const DeltaArgs& a, const uint8_t* blocks) {
+  if (a.n == 0 || a.seqs < 2 || a.seqs > kRanked) return nullptr;
+  return reinterpret_cast<int32_t*>(const_cast<uint8_t*>(blocks) - kOrderBytes);
+}
 
 // Token rows as boxes of 64 tokens: all columns of a head, as [d / 64][64][64];
 // or 16 columns, as [64][16].

@@ -54,6 +54,7 @@ struct ReverseArgs {
   int H, Hk;
   float scale;
   const uint8_t* blocks;
+  const int32_t* order;
   DeltaKept kept;
   const float* dS_out;
   float* dS_in;
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(RK<D, KS, RG>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(met + 3 * RG);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int h = blockIdx.y, hk = h / (a.H / a.Hk);
-  const int64_t seq = blockIdx.z;
+  const int64_t seq = a.order != nullptr ? a.order[blockIdx.z] : blockIdx.z;
   const SeqRange sr = seq_range(a.offsets, a.n, seq);
   const int64_t len = sr.t1 - sr.t0;
   const int64_t nc = (len + kC - 1) / kC;
@@ -784,7 +785,7 @@ Plan plan_of(const DeltaArgs& a) {
     o += align_up(bytes, 1024);
     return at;
   };
-  p.blocks = take(ch * chunk_bytes(3));
+  p.blocks = take(blocks_bytes(a, 3)) + kOrderBytes;
   p.S0 = take(ch * DD * 2);
   p.E = take(ch * DD * 2);
   p.U = take(ch * kC * D * 2);
@@ -824,7 +825,8 @@ cudaError_t launch_reverse(const DeltaArgs& a, const Call& x, char* w, const Pla
   const cudaError_t e = ensure_smem_attr(delta_reverse_kernel<D, KS, RG>, L::SMEM);
   if (e != cudaSuccess) return e;
   const ReverseArgs k = {a.n, a.offsets, a.H, a.Hk, a.scale,
-                         reinterpret_cast<const uint8_t*>(w + p.blocks), kept, x.dS_out, x.dS_in,
+                         reinterpret_cast<const uint8_t*>(w + p.blocks),
+                         order_of(a, reinterpret_cast<const uint8_t*>(w + p.blocks)), kept, x.dS_out, x.dS_in,
                          static_cast<__nv_bfloat16*>(x.dV),
                          reinterpret_cast<__nv_bfloat16*>(w + p.E),
                          reinterpret_cast<__nv_bfloat16*>(w + p.dVt),

@@ -43,7 +43,25 @@ struct ChunkArgs {
   int H, Hk;
   float scale;
   uint8_t* blocks;
+  int64_t slots;
+  int32_t* order;  // written where it is not nullptr
 };
+
+// The sequences from the longest to the shortest, equal ones as they come: a chain's
+// time is its length, so the longest has to start first (16,411 tokens in 13 sequences,
+// the longest last: 457 us; first: 340 us).
+__device__ __forceinline__ void rank_sequences(const ChunkArgs& a, int64_t* len, int tid) {
+  for (int i = tid; i < a.seqs; i += kChunkThreads) {
+    const SeqRange s = seq_range(a.offsets, a.n, i);
+    len[i] = s.t1 - s.t0;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.seqs; i += kChunkThreads) {
+    int rank = 0;
+    for (int j = 0; j < a.seqs; ++j) rank += len[j] > len[i] || (len[j] == len[i] && j < i);
+    a.order[rank] = i;
+  }
+}
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -65,6 +83,10 @@ __global__ void __launch_bounds__(kChunkThreads)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t slot = blockIdx.x;
   const int h = blockIdx.y, hk = h / (a.H / a.Hk);
+  if (slot == a.slots) {  // one block more: it ranks the sequences
+    if (h == 0) rank_sequences(a, reinterpret_cast<int64_t*>(smem_raw), tid);
+    return;
+  }
   const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
   if (c.len == 0) return;
 
@@ -238,7 +260,7 @@ __global__ void __launch_bounds__(kChunkThreads)
 // add to it (measured: 1 + 0.75 ulp stays 1), so small parts are summed apart
 // from large ones, and the state takes one fp32 addition a chunk.
 // ----------------------------------------------------------------------------
-template <int D, int KS, int RG, bool GRAD>
+template <int D, int KS, int RG, int ST, bool GRAD>
 struct SK {
   static constexpr int WARPS = KS * RG;
   static constexpr int KQ = kC * D * 2;               // one of K, Q
@@ -252,7 +274,7 @@ struct SK {
                        X_U = 8 * U_PARTS * 32 * 8;
   static constexpr int X = 2 * X_PART + X_R + X_U;
   static constexpr int THREADS = 32 * (WARPS + 1);
-  static constexpr int OFF_Q = 2 * STAGE;             // Q is free again early in a step: one stage
+  static constexpr int OFF_Q = ST * STAGE;             // Q is free again early in a step: one stage
   static constexpr int OFF_X = OFF_Q + KQ;
   static constexpr int OFF_BAR = OFF_X + RG * X;
   static constexpr int SMEM = OFF_BAR + 192 + 1024;
@@ -267,6 +289,7 @@ struct StateArgs {
   int H, Hk;
   float scale;
   const uint8_t* blocks;
+  const int32_t* order;  // sequences from the longest, or nullptr: as they come
   const float* S_in;
   float* S_out;
   __nv_bfloat16* O;
@@ -274,13 +297,13 @@ struct StateArgs {
   int* err;
 };
 
-template <int D, int KS, int RG, bool GRAD>
-__global__ void __launch_bounds__(SK<D, KS, RG, GRAD>::THREADS, 1)
+template <int D, int KS, int RG, int ST, bool GRAD>
+__global__ void __launch_bounds__(SK<D, KS, RG, ST, GRAD>::THREADS, ST == 1 ? 2 : 1)
     delta_state_kernel(const __grid_constant__ CUtensorMap mQ,
                        const __grid_constant__ CUtensorMap mK,
                        const __grid_constant__ CUtensorMap mV,
                        const __grid_constant__ CUtensorMap mG, const StateArgs a) {
-  using L = SK<D, KS, RG, GRAD>;
+  using L = SK<D, KS, RG, ST, GRAD>;
   constexpr int DK = D / KS, NT = 8 / KS;  // a warp's columns of S; its token tiles of r, u, o
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -292,7 +315,7 @@ __global__ void __launch_bounds__(SK<D, KS, RG, GRAD>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(met + 3 * RG);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int h = blockIdx.y, hk = h / (a.H / a.Hk);
-  const int64_t seq = blockIdx.z;
+  const int64_t seq = a.order != nullptr ? a.order[blockIdx.z] : blockIdx.z;
   const SeqRange sr = seq_range(a.offsets, a.n, seq);
   const int64_t len = sr.t1 - sr.t0;
   const int64_t nc = (len + kC - 1) / kC;
@@ -314,8 +337,8 @@ __global__ void __launch_bounds__(SK<D, KS, RG, GRAD>::THREADS, 1)
     if (lane == 0) {
       int64_t issued = 0, q_issued = 0;
       for (int64_t c = 0; c < nc; ++c) {
-        const int s = (int)(c & 1);
-        if (!mbar_wait(&empty[s], (uint32_t)((c >> 1) & 1) ^ 1, abort_flag, a.err, kErrWaitEmpty))
+        const int s = (int)(c % ST);
+        if (!mbar_wait(&empty[s], (uint32_t)(c / ST & 1) ^ 1, abort_flag, a.err, kErrWaitEmpty))
           break;
         uint8_t* st = smem + s * L::STAGE;
         const int t = (int)(sr.t0 + c * kC);
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(SK<D, KS, RG, GRAD>::THREADS, 1)
         tma_load_3d(smem + L::OFF_Q, &mQ, qfull, 0, t, hk * (D / 64));
         ++q_issued;
       }
-      drain_ring(full, 2, issued, a.err);
+      drain_ring(full, ST, issued, a.err);
       drain_ring(qfull, 1, q_issued, a.err);
     }
     return;
@@ -380,8 +403,8 @@ __global__ void __launch_bounds__(SK<D, KS, RG, GRAD>::THREADS, 1)
   const int kn_r = lane % 16, kn_c = (lane / 16) * 8;
 
   for (int64_t c = 0; c < nc; ++c) {
-    const int st = (int)(c & 1);
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (uint32_t)((c >> 1) & 1), abort_flag, a.err,
+    const int st = (int)(c % ST);
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (uint32_t)(c / ST & 1), abort_flag, a.err,
                                            kErrWaitFull)))
       break;
     uint8_t* base = smem + st * L::STAGE;
@@ -755,18 +778,20 @@ cudaError_t launch_chunks(const DeltaArgs& a, uint8_t* blocks, cudaStream_t st) 
   const cudaError_t e = ensure_smem_attr(delta_chunk_kernel<D, GRAD>, smem);
   if (e != cudaSuccess) return e;
   const ChunkArgs k = {static_cast<const __nv_bfloat16*>(a.Q), static_cast<const __nv_bfloat16*>(a.K),
-                       a.g, a.b, a.ldq, a.ldk, a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, blocks};
+                       a.g, a.b, a.ldq, a.ldk, a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, blocks,
+                       chunk_slots(a), order_of(a, blocks)};
   TraceScope ts("delta_chunk", st);
   delta_chunk_kernel<D, GRAD>
-      <<<dim3((unsigned)chunk_slots(a), (unsigned)a.H), kChunkThreads, smem, st>>>(k);
+      <<<dim3((unsigned)(chunk_slots(a) + (k.order != nullptr)), (unsigned)a.H), kChunkThreads, smem,
+         st>>>(k);
   return cudaGetLastError();
 }
 
-template <int D, int KS, int RG, bool GRAD>
+template <int D, int KS, int RG, int ST, bool GRAD>
 cudaError_t launch_state(const DeltaArgs& a, const float* S_in, float* S_out, void* O,
                          const uint8_t* blocks, const void* dO, const DeltaKept* kept,
                          cudaStream_t st) {
-  using L = SK<D, KS, RG, GRAD>;
+  using L = SK<D, KS, RG, ST, GRAD>;
   int* err = device_error_ptr();
   if (err == nullptr) return cudaErrorInvalidDevice;
   CUtensorMap mQ = {}, mK = {}, mV = {}, mG = {};
@@ -775,12 +800,12 @@ cudaError_t launch_state(const DeltaArgs& a, const float* S_in, float* S_out, vo
                   !strip_map(&mV, a.V, a.n, a.ldv, a.H * D) ||
                   (GRAD && !strip_map(&mG, dO, a.n, (int64_t)a.H * D, a.H * D))))
     return cudaErrorInvalidValue;
-  const cudaError_t e = ensure_smem_attr(delta_state_kernel<D, KS, RG, GRAD>, L::SMEM);
+  const cudaError_t e = ensure_smem_attr(delta_state_kernel<D, KS, RG, ST, GRAD>, L::SMEM);
   if (e != cudaSuccess) return e;
-  const StateArgs k = {a.n,  a.offsets, a.H,   a.Hk, a.scale, blocks, S_in, S_out,
+  const StateArgs k = {a.n,  a.offsets, a.H,   a.Hk, a.scale, blocks, order_of(a, blocks), S_in, S_out,
                        static_cast<__nv_bfloat16*>(O), kept ? *kept : DeltaKept{}, err};
   TraceScope ts(GRAD ? "delta_state_kept" : "delta_state", st);
-  delta_state_kernel<D, KS, RG, GRAD><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
+  delta_state_kernel<D, KS, RG, ST, GRAD><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
                                         L::THREADS, L::SMEM, st>>>(mQ, mK, mV, mG, k);
   return cudaGetLastError();
 }
@@ -791,12 +816,12 @@ cudaError_t state_by_size(const DeltaArgs& a, const float* S_in, float* S_out, v
                           cudaStream_t st) {
   const bool few = delta_few_rows(a);
   if (a.d == 64)
-    return few ? launch_state<64, 4, 1, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st)
-               : launch_state<64, 2, 2, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
+    return few ? launch_state<64, 4, 1, 2, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st)
+               : launch_state<64, 2, 2, 1, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
   if (a.d == 128)
-    return few ? launch_state<128, 4, 1, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st)
-               : launch_state<128, 2, 2, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
-  return launch_state<256, 4, 1, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
+    return few ? launch_state<128, 4, 1, 2, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st)
+               : launch_state<128, 2, 2, GRAD ? 2 : 1, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
+  return launch_state<256, 4, 1, 2, GRAD>(a, S_in, S_out, O, blocks, dO, kept, st);
 }
 
 }  // namespace
@@ -812,13 +837,11 @@ cudaError_t delta_prepare(const DeltaArgs& a, bool gradient, uint8_t* blocks, cu
                       : launch_chunks<256, false>(a, blocks, st);
 }
 
-size_t delta_tc_bytes(const DeltaArgs& a) {
-  return a.n == 0 ? 0 : (size_t)chunk_slots(a) * a.H * chunk_bytes(1);
-}
+size_t delta_tc_bytes(const DeltaArgs& a) { return blocks_bytes(a, 1); }
 
 cudaError_t delta_tc(const DeltaArgs& a, const float* S_in, float* S_out, void* O, void* ws,
                      cudaStream_t st) {
-  uint8_t* blocks = static_cast<uint8_t*>(ws);
+  uint8_t* blocks = static_cast<uint8_t*>(ws) + kOrderBytes;
   const cudaError_t e = delta_prepare(a, false, blocks, st);
   if (e != cudaSuccess) return e;
   return state_by_size<false>(a, S_in, S_out, O, blocks, nullptr, nullptr, st);

@@ -258,13 +258,16 @@ cudaError_t rope(const RopeArgs& a, cudaStream_t st) {
   RopeParams p;
   const int total = a.rot[0] + a.rot[1] + a.rot[2];
   int j = 0;
-  for (int x = 0; x < 3; ++x)
-    for (int i = 0; i < a.rot[x] / 2; ++i, ++j) {
-      const double e = a.head_freq ? 2.0 * j / total : 2.0 * i / a.rot[x];
-      // base >= 1: less than a sixth of a turn
-      const double turns = std::pow((double)a.base[x], -e) / 6.283185307179586476925;
-      p.turns[j] = ((uint64_t)std::llrint(std::ldexp(turns, 62)) << 2) | (uint64_t)x;
-    }
+  for (int x = 0; x < 3; ++x) {
+    // a geometric row; with 64 bits of mantissa 128 products keep more than a double has
+    if (a.rot[x] == 0) continue;
+    const long double size = a.head_freq ? total : a.rot[x];
+    const long double ratio = std::pow((long double)a.base[x], -2 / size);
+    long double turns = std::pow((long double)a.base[x], a.head_freq ? -2 * j / size : 0) /
+                        6.283185307179586476925286766559L;  // base >= 1: less than a sixth of a turn
+    for (int i = 0; i < a.rot[x] / 2; ++i, ++j, turns *= ratio)
+      p.turns[j] = ((uint64_t)std::ldexp(turns, 62) << 2) | (uint64_t)x;
+  }
   p.X[0] = a.Q, p.X[1] = a.K, p.Y[0] = a.Qo, p.Y[1] = a.Ko;
   p.ld[0] = a.ldq, p.ld[1] = a.ldk, p.ldo[0] = a.ldqo, p.ldo[1] = a.ldko;
   p.heads[0] = a.Hq, p.heads[1] = a.Hk;
