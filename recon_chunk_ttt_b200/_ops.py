@@ -10,6 +10,7 @@ current stream.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -28,6 +29,10 @@ class ttt_delta_tokens(ctypes.Structure):
                 ("ldk", _I64), ("ldv", _I64), ("n", _I64), ("offsets", _P), ("seqs", _I64)]
 
 
+# the same as bytes: a struct of this size is faster packed than filled field by field
+_pack_tokens = struct.Struct("=QQQQQqqqqQq").pack
+
+
 class ttt_rope_config(ctypes.Structure):
     _fields_ = [("d", _I32), ("rot", _I32 * 3), ("base", ctypes.c_float * 3), ("layout", _I32),
                 ("freq", _I32), ("precision", _I32)]
@@ -37,6 +42,7 @@ class ttt_norm_config(ctypes.Structure):
     _fields_ = [("dim", _I64), ("eps", ctypes.c_float), ("precision", _I32)]
 
 
+_F32 = torch.float32
 DEVICE_ERR_OFFSETS = 8  # TTT_DEVICE_ERR_OFFSETS
 ROPE_HALF, ROPE_PAIRS = 0, 1
 ROPE_FREQ_AXIS, ROPE_FREQ_HEAD = 0, 1
@@ -48,7 +54,7 @@ def _lib():
     global _typed
     if _typed is None:
         L = B.lib()
-        dc, dt = ctypes.POINTER(ttt_delta_config), ctypes.POINTER(ttt_delta_tokens)
+        dc, dt = ctypes.POINTER(ttt_delta_config), _P  # dt: a ttt_delta_tokens, or its bytes
         rc, nc = ctypes.POINTER(ttt_rope_config), ctypes.POINTER(ttt_norm_config)
         for name, args, res in (
                 ("ttt_delta_workspace_bytes", [dc, _I64, _I64, _I32], _SZ),
@@ -103,10 +109,12 @@ def _maybe(what, dev, name, t, dtype, shape):
     return None if t is None else _check(what, dev, name, t, dtype, shape)
 
 
-def _out(what, dev, name, t, dtype, shape):
-    """An output and its pointer, allocated if it is not given."""
+def _out(what, dev, name, t, dtype, shape, like):
+    """An output and its pointer; allocated if it is not given, from a tensor on
+    the same device (`like`: of its type and shape, or at least its type)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty_like(like) if like.shape == shape and like.is_contiguous() \
+            else like.new_empty(shape)
         return t, t.data_ptr()
     return t, _check(what, dev, name, t, dtype, shape)
 
@@ -160,17 +168,17 @@ def alloc_delta_workspace(cfg: ttt_delta_config, n: int, seqs: int = 1, backward
 
 
 def _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs):
-    """(device, tokens of the call, token type)."""
+    """(device, tokens of the call as bytes, their number, token type)."""
     dev, tdt = _device(what, Q), _token(cfg.precision)
     n, heads, d = Q.shape[0], cfg.heads, cfg.d
-    qk, hv, per = (n, cfg.qk_heads * d), (n, heads * d), (n, heads)
-    f32 = torch.float32
-    return dev, ttt_delta_tokens(
+    qk, per = (n, cfg.qk_heads * d), (n, heads)
+    return dev, _pack_tokens(
         _check(what, dev, "Q", Q, tdt, qk, True), _check(what, dev, "K", K, tdt, qk, True),
-        _check(what, dev, "V", V, tdt, hv, True),
-        _check(what, dev, "log_decay", log_decay, f32, per), _check(what, dev, "beta", beta, f32, per),
-        _ld(Q), _ld(K), _ld(V), n,
-        _maybe(what, dev, "offsets", offsets, torch.int64, (seqs + 1,)), seqs), tdt
+        _check(what, dev, "V", V, tdt, (n, heads * d), True),
+        _check(what, dev, "log_decay", log_decay, _F32, per),
+        _check(what, dev, "beta", beta, _F32, per), _ld(Q), _ld(K), _ld(V), n,
+        0 if offsets is None else _check(what, dev, "offsets", offsets, torch.int64, (seqs + 1,)),
+        seqs), n, tdt
 
 
 def ttt_delta_chunk(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S=None, offsets=None,
@@ -179,15 +187,14 @@ def ttt_delta_chunk(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S=None, off
     the device, or one sequence); returns (O, S_out).  S_out may be S."""
     what = "ttt_delta_chunk"
     seqs = 1 if offsets is None else offsets.shape[0] - 1
-    dev, t, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs)
-    shape, f32 = (seqs, cfg.heads, cfg.d, cfg.d), torch.float32
-    pS = _maybe(what, dev, "S", S, f32, shape)
-    S_out, pSo = _out(what, dev, "S_out", S_out, f32, shape)
-    O, pO = _out(what, dev, "O", O, tdt, (t.n, cfg.heads * cfg.d))
+    dev, t, n, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs)
+    shape = (seqs, cfg.heads, cfg.d, cfg.d)
+    pS = _maybe(what, dev, "S", S, _F32, shape)
+    S_out, pSo = _out(what, dev, "S_out", S_out, _F32, shape, beta if S is None else S)
+    O, pO = _out(what, dev, "O", O, tdt, (n, cfg.heads * cfg.d), V)
     workspace, pW, nbytes = _space(what, dev, workspace,
-                                   lambda: ttt_delta_workspace_bytes(cfg, t.n, seqs))
-    _run(what, dev, _lib().ttt_delta_chunk,
-         (ctypes.byref(cfg), ctypes.byref(t), pS, pSo, pO, pW, nbytes), stream)
+                                   lambda: ttt_delta_workspace_bytes(cfg, n, seqs))
+    _run(what, dev, _lib().ttt_delta_chunk, (ctypes.byref(cfg), t, pS, pSo, pO, pW, nbytes), stream)
     return O, S_out
 
 
@@ -197,16 +204,15 @@ def ttt_delta_step(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S, slots=Non
     (slots: int32 [n], -1 for padding; without them request i has state i).
     The new states go to S_out, or into S where that is not given; returns O."""
     what = "ttt_delta_step"
-    dev, t, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, None, Q.shape[0])
+    dev, t, n, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, None, Q.shape[0])
     _want(isinstance(S, torch.Tensor) and S.dim() == 4, what, "S must be [pool, heads, d, d]")
     pool = S.shape[0]
-    shape, f32 = (pool, cfg.heads, cfg.d, cfg.d), torch.float32
-    pS = _check(what, dev, "S", S, f32, shape)
-    pSo = pS if S_out is None else _check(what, dev, "S_out", S_out, f32, shape)
-    pI = _maybe(what, dev, "slots", slots, torch.int32, (t.n,))
-    O, pO = _out(what, dev, "O", O, tdt, (t.n, cfg.heads * cfg.d))
-    _run(what, dev, _lib().ttt_delta_step,
-         (ctypes.byref(cfg), ctypes.byref(t), pI, pool, pS, pSo, pO), stream)
+    shape = (pool, cfg.heads, cfg.d, cfg.d)
+    pS = _check(what, dev, "S", S, _F32, shape)
+    pSo = pS if S_out is None else _check(what, dev, "S_out", S_out, _F32, shape)
+    pI = _maybe(what, dev, "slots", slots, torch.int32, (n,))
+    O, pO = _out(what, dev, "O", O, tdt, (n, cfg.heads * cfg.d), V)
+    _run(what, dev, _lib().ttt_delta_step, (ctypes.byref(cfg), t, pI, pool, pS, pSo, pO), stream)
     return O
 
 
@@ -217,24 +223,22 @@ def ttt_delta_backward(cfg: ttt_delta_config, Q, K, V, log_decay, beta, dO, S=No
     (dQ, dK, dV, dlog_decay, dbeta, dS).  dS may be dS_out."""
     what = "ttt_delta_backward"
     seqs = 1 if offsets is None else offsets.shape[0] - 1
-    dev, t, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs)
-    n, f32 = t.n, torch.float32
+    dev, t, n, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs)
     qk, hv, per = (n, cfg.qk_heads * cfg.d), (n, cfg.heads * cfg.d), (n, cfg.heads)
     shape = (seqs, cfg.heads, cfg.d, cfg.d)
-    pS = _maybe(what, dev, "S", S, f32, shape)
+    pS = _maybe(what, dev, "S", S, _F32, shape)
     pG = _check(what, dev, "dO", dO, tdt, hv)
-    pE = _maybe(what, dev, "dS_out", dS_out, f32, shape)
-    dQ, p1 = _out(what, dev, "dQ", dQ, tdt, qk)
-    dK, p2 = _out(what, dev, "dK", dK, tdt, qk)
-    dV, p3 = _out(what, dev, "dV", dV, tdt, hv)
-    dlog_decay, p4 = _out(what, dev, "dlog_decay", dlog_decay, f32, per)
-    dbeta, p5 = _out(what, dev, "dbeta", dbeta, f32, per)
-    dS, p6 = _out(what, dev, "dS", dS, f32, shape)
+    pE = _maybe(what, dev, "dS_out", dS_out, _F32, shape)
+    dQ, p1 = _out(what, dev, "dQ", dQ, tdt, qk, Q)
+    dK, p2 = _out(what, dev, "dK", dK, tdt, qk, K)
+    dV, p3 = _out(what, dev, "dV", dV, tdt, hv, dO)
+    dlog_decay, p4 = _out(what, dev, "dlog_decay", dlog_decay, _F32, per, beta)
+    dbeta, p5 = _out(what, dev, "dbeta", dbeta, _F32, per, beta)
+    dS, p6 = _out(what, dev, "dS", dS, _F32, shape, beta if S is None else S)
     workspace, pW, nbytes = _space(what, dev, workspace,
                                    lambda: ttt_delta_workspace_bytes(cfg, n, seqs, True))
     _run(what, dev, _lib().ttt_delta_backward,
-         (ctypes.byref(cfg), ctypes.byref(t), pS, pG, pE, p1, p2, p3, p4, p5, p6, pW, nbytes),
-         stream)
+         (ctypes.byref(cfg), t, pS, pG, pE, p1, p2, p3, p4, p5, p6, pW, nbytes), stream)
     return dQ, dK, dV, dlog_decay, dbeta, dS
 
 
@@ -266,13 +270,13 @@ def ttt_rope(cfg: ttt_rope_config, Q, K, positions, Q_out=None, K_out=None, inve
         w = x.shape[1]
         p = _check(what, dev, name, x, tdt, (n, w), True)
         if y is None:
-            y = torch.empty((n, w), dtype=tdt, device=dev)
+            y = torch.empty_like(x) if x.is_contiguous() else x.new_empty((n, w))
             return w // cfg.d, p, _ld(x), y, y.data_ptr(), w
         return w // cfg.d, p, _ld(x), y, _check(what, dev, name + "_out", y, tdt, (n, w), True), _ld(y)
 
     hq, pQ, lq, Q_out, pQo, lqo = side("Q", Q, Q_out)
     hk, pK, lk, K_out, pKo, lko = side("K", K, K_out)
-    pP = _check(what, dev, "positions", positions, torch.float32, (n, 3))
+    pP = _check(what, dev, "positions", positions, _F32, (n, 3))
     _run(what, dev, _lib().ttt_rope, (ctypes.byref(cfg), pQ, lq, hq, pK, lk, hk, pP, n, pQo, lqo, pKo,
                                       lko, 1 if inverse else 0), stream)
     return Q_out, K_out
@@ -293,14 +297,16 @@ def ttt_layer_norm(cfg: ttt_norm_config, X, weight=None, bias=None, Y=None, stat
     """Layer norm of the rows of X [rows, dim]; returns (Y, stats), stats
     float [rows, 2] holding each row's mean and 1/sqrt(var + eps)."""
     what = "ttt_layer_norm"
-    dev, tdt, f32 = _device(what, X), _token(cfg.precision), torch.float32
+    dev, tdt = _device(what, X), _token(cfg.precision)
     dim = cfg.dim
     rows = X.shape[0]
     pX = _check(what, dev, "X", X, tdt, (rows, dim), True)
-    pw = _maybe(what, dev, "weight", weight, f32, (dim,))
-    pb = _maybe(what, dev, "bias", bias, f32, (dim,))
-    Y, pY = _out(what, dev, "Y", Y, tdt, (rows, dim))
-    stats, ps = _out(what, dev, "stats", stats, f32, (rows, 2))
+    pw = _maybe(what, dev, "weight", weight, _F32, (dim,))
+    pb = _maybe(what, dev, "bias", bias, _F32, (dim,))
+    Y, pY = _out(what, dev, "Y", Y, tdt, (rows, dim), X)
+    if stats is None:
+        stats = torch.empty((rows, 2), dtype=_F32, device=X.device)
+    ps = _check(what, dev, "stats", stats, _F32, (rows, 2))
     _run(what, dev, _lib().ttt_layer_norm, (ctypes.byref(cfg), pX, _ld(X), rows, pw, pb, pY, ps),
          stream)
     return Y, stats
@@ -310,16 +316,16 @@ def ttt_layer_norm_backward(cfg: ttt_norm_config, X, dY, stats, weight=None, dX=
                             dweight=None, dbias=None, workspace=None, stream=None):
     """(dX, dweight, dbias) from the forward call's X and stats."""
     what = "ttt_layer_norm_backward"
-    dev, tdt, f32 = _device(what, X), _token(cfg.precision), torch.float32
+    dev, tdt = _device(what, X), _token(cfg.precision)
     dim = cfg.dim
     rows = X.shape[0]
     pX = _check(what, dev, "X", X, tdt, (rows, dim), True)
     pY = _check(what, dev, "dY", dY, tdt, (rows, dim), True)
-    ps = _check(what, dev, "stats", stats, f32, (rows, 2))
-    pw = _maybe(what, dev, "weight", weight, f32, (dim,))
-    dX, p1 = _out(what, dev, "dX", dX, tdt, (rows, dim))
-    dweight, p2 = _out(what, dev, "dweight", dweight, f32, (dim,))
-    dbias, p3 = _out(what, dev, "dbias", dbias, f32, (dim,))
+    ps = _check(what, dev, "stats", stats, _F32, (rows, 2))
+    pw = _maybe(what, dev, "weight", weight, _F32, (dim,))
+    dX, p1 = _out(what, dev, "dX", dX, tdt, (rows, dim), X)
+    dweight, p2 = _out(what, dev, "dweight", dweight, _F32, (dim,), stats if weight is None else weight)
+    dbias, p3 = _out(what, dev, "dbias", dbias, _F32, (dim,), dweight)
     workspace, pW, nbytes = _space(what, dev, workspace, lambda: ttt_norm_workspace_bytes(cfg, rows))
     _run(what, dev, _lib().ttt_layer_norm_backward,
          (ctypes.byref(cfg), pX, _ld(X), pY, _ld(dY), rows, pw, ps, p1, p2, p3, pW, nbytes), stream)

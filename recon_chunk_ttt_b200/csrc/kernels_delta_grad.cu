@@ -29,7 +29,7 @@ namespace {
 // ----------------------------------------------------------------------------
 // delta_reverse_kernel: as delta_state_kernel, KS warps share 16 rows of E.
 // ----------------------------------------------------------------------------
-template <int D, int KS, int RG>
+template <int D, int KS, int RG, int ST>
 struct RK {
   static constexpr int WARPS = KS * RG;
   static constexpr int KQ = kC * D * 2;
@@ -40,7 +40,7 @@ struct RK {
   static constexpr int X_PART = 8 * (KS - 1) * 32 * 16, X_U = 8 * 3 * 32 * 8;
   static constexpr int X = X_PART + 2 * X_U;
   static constexpr int THREADS = 32 * (WARPS + 1);
-  static constexpr int OFF_X = 2 * STAGE;
+  static constexpr int OFF_X = ST * STAGE;
   static constexpr int OFF_BAR = OFF_X + RG * X;
   static constexpr int SMEM = OFF_BAR + 192 + 1024;
   static_assert((KS == 2 || KS == 4) && RG <= 2, "tiles and barriers of a group");
@@ -66,13 +66,13 @@ struct ReverseArgs {
   int* err;
 };
 
-template <int D, int KS, int RG>
-__global__ void __launch_bounds__(RK<D, KS, RG>::THREADS, 1)
+template <int D, int KS, int RG, int ST>
+__global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
     delta_reverse_kernel(const __grid_constant__ CUtensorMap mQ,
                          const __grid_constant__ CUtensorMap mK,
                          const __grid_constant__ CUtensorMap mV,
                          const __grid_constant__ CUtensorMap mG, const ReverseArgs a) {
-  using L = RK<D, KS, RG>;
+  using L = RK<D, KS, RG, ST>;
   constexpr int DK = D / KS, NT = 8 / KS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(RK<D, KS, RG>::THREADS, 1)
     if (lane == 0) {
       int64_t issued = 0;
       for (int64_t i = 0; i < nc; ++i) {
-        const int s = (int)(i & 1);
-        if (!mbar_wait(&empty[s], (uint32_t)((i >> 1) & 1) ^ 1, abort_flag, a.err, kErrWaitEmpty))
+        const int s = (int)(i % ST);
+        if (!mbar_wait(&empty[s], (uint32_t)(i / ST & 1) ^ 1, abort_flag, a.err, kErrWaitEmpty))
           break;
         uint8_t* st = smem + s * L::STAGE;
         const int64_t c = nc - 1 - i;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(RK<D, KS, RG>::THREADS, 1)
                   a.blocks + ((sr.slot + c) * a.H + h) * (int64_t)L::BLOCK, L::BLOCK, &full[s]);
         ++issued;
       }
-      drain_ring(full, 2, issued, a.err);
+      drain_ring(full, ST, issued, a.err);
     }
     return;
   }
@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(RK<D, KS, RG>::THREADS, 1)
 
   for (int64_t i = 0; i < nc; ++i) {
     const int64_t c = nc - 1 - i;
-    const int st = (int)(i & 1);
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (uint32_t)((i >> 1) & 1), abort_flag, a.err,
+    const int st = (int)(i % ST);
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (uint32_t)(i / ST & 1), abort_flag, a.err,
                                            kErrWaitFull)))
       break;
     uint8_t* base = smem + st * L::STAGE;
@@ -812,17 +812,17 @@ struct Call {
   float *dg, *db, *dS_in;
 };
 
-template <int D, int KS, int RG>
+template <int D, int KS, int RG, int ST>
 cudaError_t launch_reverse(const DeltaArgs& a, const Call& x, char* w, const Plan& p,
                            const DeltaKept& kept, cudaStream_t st) {
-  using L = RK<D, KS, RG>;
+  using L = RK<D, KS, RG, ST>;
   CUtensorMap mQ = {}, mK = {}, mV = {}, mG = {};
   if (a.n > 0 && (!head_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D, D) ||
                   !head_map(&mK, a.K, a.n, a.ldk, a.Hk * D, D) ||
                   !strip_map(&mV, a.V, a.n, a.ldv, a.H * D) ||
                   !strip_map(&mG, x.dO, a.n, (int64_t)a.H * D, a.H * D)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = ensure_smem_attr(delta_reverse_kernel<D, KS, RG>, L::SMEM);
+  const cudaError_t e = ensure_smem_attr(delta_reverse_kernel<D, KS, RG, ST>, L::SMEM);
   if (e != cudaSuccess) return e;
   const ReverseArgs k = {a.n, a.offsets, a.H, a.Hk, a.scale,
                          reinterpret_cast<const uint8_t*>(w + p.blocks),
@@ -834,7 +834,7 @@ cudaError_t launch_reverse(const DeltaArgs& a, const Call& x, char* w, const Pla
                          reinterpret_cast<float*>(w + p.dots_x), reinterpret_cast<float*>(w + p.hold),
                          reinterpret_cast<float*>(w + p.hold_last), device_error_ptr()};
   TraceScope ts("delta_reverse", st);
-  delta_reverse_kernel<D, KS, RG><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
+  delta_reverse_kernel<D, KS, RG, ST><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
                                     L::THREADS, L::SMEM, st>>>(mQ, mK, mV, mG, k);
   return cudaGetLastError();
 }
@@ -887,17 +887,15 @@ cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, co
   e = delta_states_kept(a, S_in, dO, blocks, kept, st);
   if (e != cudaSuccess) return e;
   const bool few = delta_few_rows(a);
-  int ks = 4;
+  constexpr int ks = 4;  // of every form of the reverse chain
   if (a.d == 64) {
-    e = few ? launch_reverse<64, 4, 1>(a, x, w, p, kept, st)
-            : launch_reverse<64, 2, 2>(a, x, w, p, kept, st);
-    if (!few) ks = 2;
+    e = few ? launch_reverse<64, 4, 1, 2>(a, x, w, p, kept, st)
+            : launch_reverse<64, 4, 1, 1>(a, x, w, p, kept, st);
   } else if (a.d == 128) {
-    e = few ? launch_reverse<128, 4, 1>(a, x, w, p, kept, st)
-            : launch_reverse<128, 2, 2>(a, x, w, p, kept, st);
-    if (!few) ks = 2;
+    e = few ? launch_reverse<128, 4, 1, 2>(a, x, w, p, kept, st)
+            : launch_reverse<128, 4, 1, 1>(a, x, w, p, kept, st);
   } else {
-    e = launch_reverse<256, 4, 1>(a, x, w, p, kept, st);
+    e = launch_reverse<256, 4, 1, 2>(a, x, w, p, kept, st);
   }
   if (e != cudaSuccess || a.n == 0) return e;
   e = a.d == 64    ? launch_tokens<64>(a, x, w, p, st)
