@@ -158,6 +158,14 @@ __device__ __forceinline__ uint32_t tri(int row, int col) {
          (col & 7) * 2;
 }
 
+// 32 columns, as [64][32] with the 64-byte swizzle.
+inline bool strip32_map(CUtensorMap* m, const void* base, int64_t n, int64_t ld, int cols) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)n};
+  const uint64_t str[1] = {(uint64_t)ld * 2};
+  const uint32_t box[2] = {32, kC};
+  return make_map(m, base, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 // Every kAnchor-th chunk the state is kept in fp32: there the gradient of the decays,
 // a running sum over tokens, starts anew.
 constexpr int kAnchor = 8;

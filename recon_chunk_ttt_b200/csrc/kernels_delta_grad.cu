@@ -11,11 +11,12 @@
 // changes from token to token by dO_t . O_t - dV_t . V_t alone, so it is a running sum
 // from the end, started anew from a product of the two states every 512 tokens.
 //
-// Five kernels: the inverses of all chunks; the forward chain once more, which
+// Four kernels: the inverses of all chunks; the forward chain once more, which
 // keeps each chunk's state and U (rounded to bf16: they only enter dQ and dK,
 // which are bf16) and the sums of dO . O; delta_reverse_kernel, the chain of E from
 // the last chunk to the first; delta_tokens_grad_kernel, dQ and dK of all chunks
-// at once; and the running sums.  The chains carry fp32 in three bf16 parts
+// at once, and the running sums; where heads share a key head a fifth adds their
+// shares.  The chains carry fp32 in three bf16 parts
 // (the gates' gradients and dS are fp32 results), the rest is bf16 products
 // summed in fp32.
 
@@ -461,18 +462,98 @@ __global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
 }
 
 // ----------------------------------------------------------------------------
-// delta_tokens_grad_kernel: dQ and dK of one chunk and head.  8 warps: 4 blocks
-// of 16 tokens x 2 halves of the columns at hand.
+// dlog_decay and dbeta of 512 tokens of a sequence and head (from one anchor to the
+// next): sums over the d / 16 groups of columns, and the running sum from the
+// stretch's end.  A few blocks' work, done beside dQ and dK.
 // ----------------------------------------------------------------------------
-constexpr int kGW = 8;
+constexpr int kGW = 8;  // warps of a block
+constexpr int kStretch = kC * kAnchor;
 
+struct GateArgs {
+  int groups, ks;
+  const float *dots_o, *dots_v, *dots_x, *hold, *hold_last;  // hold_last: or nullptr (zeros)
+  float *dg, *db;
+};
+
+__device__ __forceinline__ void gate_stretch(const GateArgs& a, const int64_t* offsets, int64_t n,
+                                             int64_t seqs, int H, int64_t slot, int h, int tid) {
+  // the sequence of this stretch
+  int64_t lo = 0, hi = seqs;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (seq_range(offsets, n, mid).t0 / kStretch + mid <= slot)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const SeqRange s = seq_range(offsets, n, lo);
+  const int64_t b0 = s.t0 + (slot - (s.t0 / kStretch + lo)) * kStretch;
+  if (b0 < s.t0 || b0 >= s.t1) return;
+  const int64_t b1 = b0 + kStretch < s.t1 ? b0 + kStretch : s.t1;
+  // <E, S> at the end: the next anchor's, or the last states'
+  const int parts = a.groups * a.ks;
+  const float* end = b1 < s.t1 ? a.hold + ((slot + 1) * H + h) * parts
+                     : a.hold_last != nullptr ? a.hold_last + (lo * H + h) * parts
+                                              : nullptr;
+  float x = 0.f;
+  if (end != nullptr)
+    for (int i = 0; i < parts; ++i) x += end[i];
+  constexpr int PER = kStretch / (32 * kGW);
+  float v[PER], sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int64_t t = b0 + tid * PER + q;
+    float o = 0.f, w = 0.f, b = 0.f;
+    if (t < b1) {
+#pragma unroll 4
+      for (int r = 0; r < a.groups; ++r) {
+        const int64_t at = (r * (int64_t)H + h) * n + t;
+        o += a.dots_o[at];
+        w += a.dots_v[at];
+        b += a.dots_x[at];
+      }
+      a.db[t * H + h] = b;
+    }
+    v[q] = o - w;
+    sum += v[q];
+  }
+  // sums of the threads behind this one
+  __shared__ float warp_sum[kGW];
+  const int lane = tid % 32, warp = tid / 32;
+  float behind = sum;
+  for (int m = 1; m < 32; m *= 2) {
+    const float y = __shfl_down_sync(0xffffffffu, behind, m);
+    if (lane + m < 32) behind += y;
+  }
+  if (lane == 0) warp_sum[warp] = behind;
+  __syncthreads();
+  behind -= sum;
+  for (int w = warp + 1; w < kGW; ++w) behind += warp_sum[w];
+  x += behind;
+#pragma unroll
+  for (int q = PER - 1; q >= 0; --q) {
+    const int64_t t = b0 + tid * PER + q;
+    x += v[q];
+    if (t < b1) a.dg[t * H + h] = x;
+  }
+}
+
+// ----------------------------------------------------------------------------
+// delta_tokens_grad_kernel: dQ and dK of one chunk and head.  8 warps: 4 blocks
+// of 16 tokens x 2 halves of the columns at hand.  dO, U, dV stay in shared memory;
+// S, E, Q, K pass in strips of 32 columns, two deep.
+// ----------------------------------------------------------------------------
 template <int D>
 struct GK {
-  static constexpr int TOK = kC * D * 2;    // one of dO, Q, K, U, dV
-  static constexpr int STRIP = D * 32 * 2;  // 32 columns of S or E
-  static constexpr int OFF_S = 5 * TOK;
-  static constexpr int OFF_A = OFF_S + 2 * STRIP;
-  static constexpr int OFF_BAR = OFF_A + 2 * kC * 128;
+  static constexpr int TOK = kC * D * 2;        // one of dO, U, dV
+  static constexpr int ST = D * 32 * 2;         // 32 columns of S or E
+  static constexpr int QS = kC * 64;            // 32 columns of Q or K
+  static constexpr int STRIP = 2 * ST + 2 * QS;
+  static constexpr int NS = D / 32;
+  static constexpr int OFF_S = 3 * TOK;
+  static constexpr int OFF_M = OFF_S + 2 * STRIP;
+  static constexpr int OFF_A = OFF_M + kC * 128;
+  static constexpr int OFF_BAR = OFF_A + kTri;
   static constexpr int SMEM = OFF_BAR + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -487,43 +568,53 @@ struct TokensGradArgs {
   const __nv_bfloat16 *S0, *E, *U, *dVt;
   __nv_bfloat16 *dQ, *dK;  // heads of their own
   float *pq, *pk;          // shared heads: each head's share, [n][H * d]
+  int64_t slots;           // the blocks from this on take the gates' gradients
+  GateArgs gates;
   int* err;
 };
 
 template <int D>
-__global__ void __launch_bounds__(32 * kGW)
+__global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     delta_tokens_grad_kernel(const __grid_constant__ CUtensorMap mQ,
                              const __grid_constant__ CUtensorMap mK,
                              const __grid_constant__ CUtensorMap mG, const TokensGradArgs a) {
   using L = GK<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  __shared__ double G[kC];
-  uint8_t *pG = smem, *pQ = smem + L::TOK, *pK = smem + 2 * L::TOK, *pU = smem + 3 * L::TOK,
-          *pV = smem + 4 * L::TOK, *pS = smem + L::OFF_S, *pE = pS + L::STRIP,
-          *pA = smem + L::OFF_A, *pM = pA + kC * 128;
+  __shared__ float Gh[kC], Gl[kC];  // running sums of the log decays in two parts
+  uint8_t *pG = smem, *pU = smem + L::TOK, *pV = smem + 2 * L::TOK, *pS = smem + L::OFF_S,
+          *pM = smem + L::OFF_M, *pA = smem + L::OFF_A;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);  // tokens, strips
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 3);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t slot = blockIdx.x;
   const int h = blockIdx.y, hk = h / (a.H / a.Hk);
+  if (slot >= a.slots) {
+    gate_stretch(a.gates, a.offsets, a.n, a.seqs, a.H, slot - a.slots, h, tid);
+    return;
+  }
   const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
   if (c.len == 0) return;
   const int64_t at = slot * a.H + h;
+  const auto load_strip = [&](int s) {
+    uint8_t* to = pS + s % 2 * L::STRIP;
+    uint64_t* b = &bar[1 + s % 2];
+    mbar_arrive_expect_tx(b, L::STRIP);
+    bulk_load(to, a.S0 + at * D * D + s * (D * 32), L::ST, b);
+    bulk_load(to + L::ST, a.E + at * D * D + s * (D * 32), L::ST, b);
+    tma_load_2d(to + 2 * L::ST, &mQ, b, hk * D + s * 32, (int)c.t0);
+    tma_load_2d(to + 2 * L::ST + L::QS, &mK, b, hk * D + s * 32, (int)c.t0);
+  };
   if (tid == 0) {
-    mbar_init(&bar[0], 1);
-    mbar_init(&bar[1], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
-    mbar_arrive_expect_tx(&bar[0], 5 * L::TOK);
+    mbar_arrive_expect_tx(&bar[0], 3 * L::TOK);
     tma_load_3d(pG, &mG, &bar[0], 0, (int)c.t0, h * (D / 64));
-    tma_load_3d(pQ, &mQ, &bar[0], 0, (int)c.t0, hk * (D / 64));
-    tma_load_3d(pK, &mK, &bar[0], 0, (int)c.t0, hk * (D / 64));
     bulk_load(pU, a.U + at * kC * D, L::TOK, &bar[0]);
     bulk_load(pV, a.dVt + at * kC * D, L::TOK, &bar[0]);
-    mbar_arrive_expect_tx(&bar[1], 2 * L::STRIP);
-    bulk_load(pS, a.S0 + at * D * D, L::STRIP, &bar[1]);
-    bulk_load(pE, a.E + at * D * D, L::STRIP, &bar[1]);
+    load_strip(0);
+    load_strip(1);
   }
   if (warp == 1) {
     double x[2];
@@ -538,24 +629,18 @@ __global__ void __launch_bounds__(32 * kGW)
       const double o = __shfl_up_sync(0xffffffffu, s, m);
       if (lane >= m) s += o;
     }
-    G[2 * lane] = s - x[1];
-    G[2 * lane + 1] = s;
-  }
-  __syncthreads();
-  bool ok = mbar_wait(&bar[0], 0, abort_flag, a.err, kErrWaitFull);
-  if (c.len < kC) {  // rows behind the sequence count as zero
-    for (int e = tid; e < (kC - c.len) * (D / 8); e += 32 * kGW) {
-      const uint32_t o = sw(kC, c.len + e / (D / 8), e % (D / 8) * 8);
-      *reinterpret_cast<uint4*>(pG + o) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(pQ + o) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(pK + o) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const double g = i == 0 ? s - x[1] : s;
+      Gh[2 * lane + i] = (float)g;
+      Gl[2 * lane + i] = (float)(g - (double)(float)g);
     }
   }
   __syncthreads();
-  const uint32_t sG = smem_u32(pG), sQ = smem_u32(pQ), sK = smem_u32(pK), sU = smem_u32(pU),
-                 sV = smem_u32(pV), sS = smem_u32(pS), sE = smem_u32(pE), sA = smem_u32(pA),
+  bool ok = mbar_wait(&bar[0], 0, abort_flag, a.err, kErrWaitFull);
+  const uint32_t sG = smem_u32(pG), sU = smem_u32(pU), sV = smem_u32(pV), sA = smem_u32(pA),
                  sM = smem_u32(pM);
-  const int m0 = warp / 2 * 16, half = warp % 2;
+  const int mb = warp / 2, m0 = mb * 16, half = warp % 2;
   const int row = lane / 4, col = 2 * (lane % 4);
   const int nk_r = (lane / 16) * 8 + lane % 8, nk_c = (lane / 8 % 2) * 8;
   const int kn_r = lane % 16, kn_c = (lane / 16) * 8;
@@ -585,19 +670,20 @@ __global__ void __launch_bounds__(32 * kGW)
         mma(dl[2 * p + 1], av, b[2], b[3]);
       }
     }
-    // A, and M with its transpose: every (i, j) of the lower part is this warp's alone
+    // A (rows behind the sequence are zero: dO there may be anything), and M with its
+    // transpose: every (i, j) of the lower part is this warp's alone
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int i = m0 + row + 8 * y, j = half * 32 + q * 8 + col;
-        float x[2], m[2];
+        float x[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const float e = j + z <= i ? expf((float)(G[i] - G[j + z])) : 0.f;
-          x[z] = j + z <= i ? a.scale * e * dp[q][2 * y + z] : 0.f;
-          m[z] = -e * dl[q][2 * y + z];
-          __nv_bfloat16 v = __float2bfloat16_rn(m[z]);
+          const float e =
+              j + z <= i ? expf((Gh[i] - Gh[j + z]) + (Gl[i] - Gl[j + z])) : 0.f;
+          x[z] = j + z <= i && i < c.len ? a.scale * e * dp[q][2 * y + z] : 0.f;
+          const __nv_bfloat16 v = __float2bfloat16_rn(-e * dl[q][2 * y + z]);
           if (j + z < i) {
             *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, i, j + z)) = v;
             *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, j + z, i)) = v;
@@ -605,21 +691,28 @@ __global__ void __launch_bounds__(32 * kGW)
             *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, i, i)) = __float2bfloat16_rn(0.f);
           }
         }
-        *reinterpret_cast<uint32_t*>(pA + sw(kC, i, j)) = pack_bf16x2(x[0], x[1]);
+        if (j / 16 <= mb)
+          *reinterpret_cast<uint32_t*>(pA + tri(i, j)) = pack_bf16x2(x[0], x[1]);
       }
   }
   __syncthreads();
 
-  const float gi[2] = {expf((float)G[m0 + row]), expf((float)G[m0 + row + 8])};
-  const float re[2] = {expf((float)(G[kC - 1] - G[m0 + row])),
-                       expf((float)(G[kC - 1] - G[m0 + row + 8]))};
-  for (int s = 0; s < D / 32; ++s) {  // 32 columns of dQ, dK at a time; 16 a warp
-    ok = mbar_wait(&bar[1], (uint32_t)(s & 1), abort_flag, a.err, kErrWaitFull) && ok;
+  float gi[2], re[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int i = m0 + row + 8 * y;
+    gi[y] = expf(Gh[i] + Gl[i]);
+    re[y] = expf((Gh[kC - 1] - Gh[i]) + (Gl[kC - 1] - Gl[i]));
+  }
+  for (int s = 0; s < L::NS; ++s) {  // 32 columns of dQ, dK at a time; 16 a warp
+    ok = mbar_wait(&bar[1 + s % 2], (uint32_t)(s / 2 & 1), abort_flag, a.err, kErrWaitFull) && ok;
+    const uint32_t sS = smem_u32(pS) + s % 2 * L::STRIP, sE = sS + L::ST, sQ = sS + 2 * L::ST,
+                   sK = sQ + L::QS;
     const int cw = half * 16, cs = s * 32 + cw;  // in the strip; in the head
     float dq[2][4] = {}, dk[2][4] = {}, ve[2][4] = {};
 #pragma unroll 4
     for (int k = 0; k < D; k += 16) {
-      uint32_t ag[4], av[4], au[4], b[4];
+      uint32_t ag[4], av[4], au[4], b[4], e[4];
       ldsm4(sG + sw(kC, m0 + kn_r, k + kn_c), ag);
       ldsm4_t(sV + blk_a(k, m0), av);
       ldsm4_t(sU + blk_a(k, m0), au);
@@ -627,13 +720,13 @@ __global__ void __launch_bounds__(32 * kGW)
       const uint32_t o = (uint32_t)(((k / 8 + lane / 8 % 2) * 4 + cw / 8 + lane / 16) * 128 +
                                     lane % 8 * 16);
       ldsm4_t(sS + o, b);
+      ldsm4_t(sE + o, e);
       mma(dq[0], ag, b[0], b[1]);
       mma(dq[1], ag, b[2], b[3]);
       mma(ve[0], av, b[0], b[1]);
       mma(ve[1], av, b[2], b[3]);
-      ldsm4_t(sE + o, b);
-      mma(dk[0], au, b[0], b[1]);
-      mma(dk[1], au, b[2], b[3]);
+      mma(dk[0], au, e[0], e[1]);
+      mma(dk[1], au, e[2], e[3]);
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -642,28 +735,36 @@ __global__ void __launch_bounds__(32 * kGW)
         dq[x][y] *= a.scale * gi[y / 2];
         dk[x][y] = re[y / 2] * dk[x][y] - gi[y / 2] * ve[x][y];
       }
-    __syncthreads();  // the strip has been read
-    if (tid == 0 && s + 1 < D / 32) {
-      mbar_arrive_expect_tx(&bar[1], 2 * L::STRIP);
-      bulk_load(pS, a.S0 + at * D * D + (s + 1) * (D * 32), L::STRIP, &bar[1]);
-      bulk_load(pE, a.E + at * D * D + (s + 1) * (D * 32), L::STRIP, &bar[1]);
-    }
 #pragma unroll
-    for (int k = 0; k < kC; k += 16) {
-      uint32_t aa[4], at_[4], am[4], bk[4], bq[4];
-      ldsm4(sA + sw(kC, m0 + kn_r, k + kn_c), aa);
-      // the transpose of A: rows are its columns
-      ldsm4_t(sA + sw(kC, k + nk_r, m0 + nk_c), at_);
-      ldsm4(sM + sw(kC, m0 + kn_r, k + kn_c), am);
-      ldsm4_t(sK + sw(kC, k + kn_r, cs + kn_c), bk);
-      ldsm4_t(sQ + sw(kC, k + kn_r, cs + kn_c), bq);
-      mma(dq[0], aa, bk[0], bk[1]);
-      mma(dq[1], aa, bk[2], bk[3]);
-      mma(dk[0], at_, bq[0], bq[1]);
-      mma(dk[1], at_, bq[2], bq[3]);
-      mma(dk[0], am, bk[0], bk[1]);
-      mma(dk[1], am, bk[2], bk[3]);
+    for (int kb = 0; kb < 4; ++kb) {
+      const int k = kb * 16;
+      uint32_t x[4], bk[4], bq[4];
+      // rows of Q and K, 64 bytes each, 16-byte unit u of row r at u ^ (r / 2 % 4)
+      const int r = k + kn_r, u = cw / 8 + lane / 16;
+      const uint32_t o = (uint32_t)(r * 64 + ((u ^ (r >> 1 & 3)) << 4));
+      ldsm4_t(sK + o, bk);
+      ldsm4_t(sQ + o, bq);
+      if (c.len < kC) {  // rows behind the sequence may hold anything and count as zero
+        const uint32_t k0 = keep_pair(k + col, c.len), k1 = keep_pair(k + 8 + col, c.len);
+        bk[0] &= k0, bk[1] &= k1, bk[2] &= k0, bk[3] &= k1;
+        bq[0] &= k0, bq[1] &= k1, bq[2] &= k0, bq[3] &= k1;
+      }
+      if (kb <= mb) {
+        ldsm4(sA + tri(m0 + kn_r, k + kn_c), x);
+        mma(dq[0], x, bk[0], bk[1]);
+        mma(dq[1], x, bk[2], bk[3]);
+      }
+      if (kb >= mb) {  // the transpose of A: rows are its columns
+        ldsm4_t(sA + tri(k + nk_r, m0 + nk_c), x);
+        mma(dk[0], x, bq[0], bq[1]);
+        mma(dk[1], x, bq[2], bq[3]);
+      }
+      ldsm4(sM + sw(kC, m0 + kn_r, k + kn_c), x);
+      mma(dk[0], x, bk[0], bk[1]);
+      mma(dk[1], x, bk[2], bk[3]);
     }
+    __syncthreads();  // the strip has been read
+    if (tid == 0 && s + 2 < L::NS) load_strip(s + 2);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -682,90 +783,11 @@ __global__ void __launch_bounds__(32 * kGW)
         }
       }
   }
-  if (!ok) {  // a wait gave up: the copies must land before the block is gone
+  if (!ok && tid == 0) {  // a wait gave up: the copies must land before the block is gone
     volatile int never = 0;
     mbar_wait(&bar[0], 0, &never, a.err, kErrWaitFinal);
-    mbar_wait(&bar[1], (uint32_t)((D / 32 - 1) & 1), &never, a.err, kErrWaitFinal);
-  }
-}
-
-// ----------------------------------------------------------------------------
-// delta_gates_kernel: dlog_decay and dbeta of 512 tokens of a sequence and head
-// (from one anchor to the next): sums over the d / 16 groups of columns, and
-// the running sum from the stretch's end.
-// ----------------------------------------------------------------------------
-constexpr int kStretch = kC * kAnchor;
-constexpr int kStretchThreads = 128;
-
-struct GateArgs {
-  int64_t n;
-  const int64_t* offsets;
-  int64_t seqs;
-  int H, groups, ks;
-  const float *dots_o, *dots_v, *dots_x, *hold, *hold_last;  // hold_last: or nullptr (zeros)
-  float *dg, *db;
-};
-
-__global__ void __launch_bounds__(kStretchThreads) delta_gates_kernel(const GateArgs a) {
-  const int64_t slot = blockIdx.x;
-  const int h = blockIdx.y, tid = threadIdx.x;
-  // the sequence of this stretch
-  int64_t lo = 0, hi = a.seqs;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (seq_range(a.offsets, a.n, mid).t0 / kStretch + mid <= slot)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const SeqRange s = seq_range(a.offsets, a.n, lo);
-  const int64_t b0 = s.t0 + (slot - (s.t0 / kStretch + lo)) * kStretch;
-  if (b0 < s.t0 || b0 >= s.t1) return;
-  const int64_t b1 = b0 + kStretch < s.t1 ? b0 + kStretch : s.t1;
-  // <E, S> at the end: the next anchor's, or the last states'
-  const int parts = a.groups * a.ks;
-  const float* end = b1 < s.t1 ? a.hold + ((slot + 1) * a.H + h) * parts
-                     : a.hold_last != nullptr ? a.hold_last + (lo * a.H + h) * parts
-                                              : nullptr;
-  float x = 0.f;
-  if (end != nullptr)
-    for (int i = 0; i < parts; ++i) x += end[i];
-  constexpr int PER = kStretch / kStretchThreads;
-  float v[PER], sum = 0.f;
-#pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    const int64_t t = b0 + tid * PER + q;
-    float o = 0.f, w = 0.f, b = 0.f;
-    if (t < b1) {
-      for (int r = 0; r < a.groups; ++r) {
-        const int64_t at = (r * (int64_t)a.H + h) * a.n + t;
-        o += a.dots_o[at];
-        w += a.dots_v[at];
-        b += a.dots_x[at];
-      }
-      a.db[t * a.H + h] = b;
-    }
-    v[q] = o - w;
-    sum += v[q];
-  }
-  // sums of the threads behind this one
-  __shared__ float warp_sum[kStretchThreads / 32];
-  const int lane = tid % 32, warp = tid / 32;
-  float behind = sum;
-  for (int m = 1; m < 32; m *= 2) {
-    const float y = __shfl_down_sync(0xffffffffu, behind, m);
-    if (lane + m < 32) behind += y;
-  }
-  if (lane == 0) warp_sum[warp] = behind;
-  __syncthreads();
-  behind -= sum;
-  for (int w = warp + 1; w < kStretchThreads / 32; ++w) behind += warp_sum[w];
-  x += behind;
-#pragma unroll
-  for (int q = PER - 1; q >= 0; --q) {
-    const int64_t t = b0 + tid * PER + q;
-    x += v[q];
-    if (t < b1) a.dg[t * a.H + h] = x;
+    for (int s = L::NS - 2; s < L::NS; ++s)
+      mbar_wait(&bar[1 + s % 2], (uint32_t)(s / 2 & 1), &never, a.err, kErrWaitFinal);
   }
 }
 
@@ -841,10 +863,10 @@ cudaError_t launch_reverse(const DeltaArgs& a, const Call& x, char* w, const Pla
 
 template <int D>
 cudaError_t launch_tokens(const DeltaArgs& a, const Call& x, char* w, const Plan& p,
-                          cudaStream_t st) {
+                          const GateArgs& gates, cudaStream_t st) {
   using L = GK<D>;
   CUtensorMap mQ, mK, mG;
-  if (!head_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D, D) || !head_map(&mK, a.K, a.n, a.ldk, a.Hk * D, D) ||
+  if (!strip32_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D) || !strip32_map(&mK, a.K, a.n, a.ldk, a.Hk * D) ||
       !head_map(&mG, x.dO, a.n, (int64_t)a.H * D, a.H * D, D))
     return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem_attr(delta_tokens_grad_kernel<D>, L::SMEM);
@@ -857,9 +879,10 @@ cudaError_t launch_tokens(const DeltaArgs& a, const Call& x, char* w, const Plan
                             reinterpret_cast<const __nv_bfloat16*>(w + p.dVt),
                             static_cast<__nv_bfloat16*>(x.dQ), static_cast<__nv_bfloat16*>(x.dK),
                             own ? nullptr : reinterpret_cast<float*>(w + p.pq),
-                            own ? nullptr : reinterpret_cast<float*>(w + p.pk), device_error_ptr()};
+                            own ? nullptr : reinterpret_cast<float*>(w + p.pk), chunk_slots(a), gates,
+                            device_error_ptr()};
   TraceScope ts("delta_tokens_grad", st);
-  delta_tokens_grad_kernel<D><<<dim3((unsigned)chunk_slots(a), (unsigned)a.H), 32 * kGW, L::SMEM,
+  delta_tokens_grad_kernel<D><<<dim3((unsigned)(chunk_slots(a) + stretches(a)), (unsigned)a.H), 32 * kGW, L::SMEM,
                                 st>>>(mQ, mK, mG, k);
   return cudaGetLastError();
 }
@@ -898,22 +921,14 @@ cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, co
     e = launch_reverse<256, 4, 1, 2>(a, x, w, p, kept, st);
   }
   if (e != cudaSuccess || a.n == 0) return e;
-  e = a.d == 64    ? launch_tokens<64>(a, x, w, p, st)
-      : a.d == 128 ? launch_tokens<128>(a, x, w, p, st)
-                   : launch_tokens<256>(a, x, w, p, st);
-  if (e != cudaSuccess) return e;
-  const GateArgs k = {a.n, a.offsets, a.seqs, a.H, a.d / 16, ks,
-                      reinterpret_cast<const float*>(w + p.dots_o),
-                      reinterpret_cast<const float*>(w + p.dots_v),
-                      reinterpret_cast<const float*>(w + p.dots_x),
-                      reinterpret_cast<const float*>(w + p.hold),
-                      dS_out != nullptr ? reinterpret_cast<const float*>(w + p.hold_last) : nullptr,
-                      dg, db};
-  {
-    TraceScope ts("delta_gates", st);
-    delta_gates_kernel<<<dim3((unsigned)stretches(a), (unsigned)a.H), kStretchThreads, 0, st>>>(k);
-    e = cudaGetLastError();
-  }
+  const GateArgs gates = {
+      a.d / 16, ks, reinterpret_cast<const float*>(w + p.dots_o),
+      reinterpret_cast<const float*>(w + p.dots_v), reinterpret_cast<const float*>(w + p.dots_x),
+      reinterpret_cast<const float*>(w + p.hold),
+      dS_out != nullptr ? reinterpret_cast<const float*>(w + p.hold_last) : nullptr, dg, db};
+  e = a.d == 64    ? launch_tokens<64>(a, x, w, p, gates, st)
+      : a.d == 128 ? launch_tokens<128>(a, x, w, p, gates, st)
+                   : launch_tokens<256>(a, x, w, p, gates, st);
   if (e != cudaSuccess || a.H == a.Hk) return e;
   return delta_share(a, reinterpret_cast<const float*>(w + p.pq),
                      reinterpret_cast<const float*>(w + p.pk), dQ, dK, st);
