@@ -12,6 +12,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "ops_internal.h"
@@ -88,6 +90,63 @@ struct Raw<T, 1> {
   __device__ __forceinline__ void none() { v = T(0.f); }
   __device__ __forceinline__ void unpack(float* x) const { x[0] = (float)v; }
 };
+// Two floats that one instruction works on.
+struct Two {
+  unsigned long long v;
+  Two() = default;
+  __device__ __forceinline__ Two(float x, float y) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  }
+  __device__ __forceinline__ explicit Two(float x) : Two(x, x) {}
+  __device__ __forceinline__ float x() const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return a;
+  }
+  __device__ __forceinline__ float y() const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return b;
+  }
+  __device__ __forceinline__ float sum() const { return x() + y(); }
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// The same of one float, where values are loaded one by one.
+struct One {
+  float v;
+  One() = default;
+  __device__ __forceinline__ explicit One(float x) : v(x) {}
+  __device__ __forceinline__ float x() const { return v; }
+  __device__ __forceinline__ float y() const { return 0.f; }
+  __device__ __forceinline__ float sum() const { return v; }
+};
+__device__ __forceinline__ One add(One a, One b) { return One(a.v + b.v); }
+__device__ __forceinline__ One mul(One a, One b) { return One(a.v * b.v); }
+__device__ __forceinline__ One fma(One a, One b, One c) { return One(fmaf(a.v, b.v, c.v)); }
+// Pair c of V values, or the one value.
+template <int V>
+using Num = std::conditional_t<V == 1, One, Two>;
+template <int V>
+__device__ __forceinline__ Num<V> pair(const float* x, int c) {
+  if constexpr (V == 1)
+    return One(x[0]);
+  else
+    return Two(x[2 * c], x[2 * c + 1]);
+}
 // w, b: floats, as many as the token vector holds
 template <int V>
 __device__ __forceinline__ void get_f(const float* p, float* x) {
@@ -117,57 +176,127 @@ __device__ __forceinline__ float group_sum(float x, float* red) {
 }
 
 // Threads of a block: 8 rows a block for a warp each, else one row.
-constexpr int block_of(int G) { return G == 32 ? 256 : G; }
+constexpr int block_of(int G) { return G <= 32 ? 256 : G; }
 
-template <typename T, int V, int G, int NV>
+// Sums of N values over the G threads of a group at once; one barrier.
+constexpr int warps_of(int G) { return G < 32 ? 1 : G / 32; }
+// Rows a group takes at once: 32 values a thread; half of that where they are loaded
+// one by one (a register each), in the groups whose block has few registers a thread,
+// and where two arrays of floats are in flight.
+constexpr int rows_at_once(int g, int nv, int v, bool two_floats) {
+  const int r = (v == 1 || g > 128 || two_floats ? 16 : 32) / (nv * v);
+  return r < 1 ? 1 : r > 4 ? 4 : r;
+}
+// Blocks of the backward kernel that an SM holds (128 registers a thread); the grid is
+// one wave of them.
+constexpr int backward_resident(int G) { return 512 / block_of(G); }
+template <int G, int N>
+__device__ __forceinline__ void group_sums(float (&x)[N], float (*red)[warps_of(G)]) {
+#pragma unroll
+  for (int m = (G < 32 ? G : 32) / 2; m > 0; m /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], m);
+  if (G > 32) {
+    if (threadIdx.x % 32 == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[i][threadIdx.x / 32] = x[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) x[i] += red[i][w];
+    }
+  }
+}
+
+// A group takes R rows at a time, whose sums share a barrier; the next R rows are
+// loaded meanwhile, and the weight and bias stay in registers.  (One row a block
+// and no more: 48 us for 20,011 rows of 1,153 floats.)
+template <typename T, int V, int G, int NV, int R>
 __global__ void __launch_bounds__(block_of(G))
     norm_kernel(const T* X, int64_t ldx, int64_t rows, int dim, float eps,
                 const float* __restrict__ w, const float* __restrict__ b, T* Y, float* stats) {
-  __shared__ float red[2][G / 32];
-  const int64_t row = (int64_t)blockIdx.x * (block_of(G) / G) + threadIdx.x / G;
-  if (G == 32 && row >= rows) return;  // whole warps; a larger group is the block
+  constexpr int GR = block_of(G) / G;  // groups of a block
+  __shared__ float red[2][2][R][warps_of(G)];
   const int l = threadIdx.x % G, nv = dim / V;
-  const T* x = X + row * ldx;
-  float v[NV][V], sum = 0.f;
+  const float inv = 1.f / dim;
+  float ww[NV][V], bb[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if (l + i * G < nv) {
-      Ld<T, V>::get(x + (l + i * G) * V, v[i]);
-    } else {
 #pragma unroll
-      for (int c = 0; c < V; ++c) v[i][c] = 0.f;
-    }
-#pragma unroll
-    for (int c = 0; c < V; ++c) sum += v[i][c];
+    for (int c = 0; c < V; ++c) ww[i][c] = 1.f, bb[i][c] = 0.f;
+    if (w != nullptr && l + i * G < nv) get_f<V>(w + (l + i * G) * V, ww[i]);
+    if (b != nullptr && l + i * G < nv) get_f<V>(b + (l + i * G) * V, bb[i]);
   }
-  const float inv = 1.f / dim;
-  const float mean = group_sum<G>(sum, red[0]) * inv;
-  float sq = 0.f;
+  struct Rows {
+    Raw<T, V> x[R][NV];
+  };
+  const auto load = [&](Rows& n, int64_t row) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (l + i * G < nv)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        v[i][c] -= mean;
-        sq = fmaf(v[i][c], v[i][c], sq);
+      for (int i = 0; i < NV; ++i)
+        if (row + r < rows && l + i * G < nv)
+          n.x[r][i].get(X + (row + r) * ldx + (l + i * G) * V);
+        else
+          n.x[r][i].none();
+  };
+  const int64_t step = (int64_t)gridDim.x * GR * R;
+  int64_t row = ((int64_t)blockIdx.x * GR + threadIdx.x / G) * R;
+  Rows now, next;
+  load(now, row);
+  int turn = 0;
+  // the lanes of a warp stay together: groups whose rows have ended go along with nothing
+  const int64_t lead = G < 32 ? threadIdx.x % 32 / G * R : 0;
+  for (; row - lead < rows; row += step) {
+    // in place is in order: Y's rows are this step's, the loads the next one's
+    load(next, row + step);
+    float mean[R], sq[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float x[V];
+        now.x[r][i].unpack(x);
+#pragma unroll
+        for (int c = 0; c < V; ++c) mean[r] += x[c];  // nothing behind the row's end
       }
-  const float rstd = 1.f / sqrtf(group_sum<G>(sq, red[1]) * inv + eps);
-  T* y = Y + row * dim;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (l + i * G < nv) {
-      float g[V], o[V];
-      if (w != nullptr) get_f<V>(w + (l + i * G) * V, g);
-#pragma unroll
-      for (int c = 0; c < V; ++c) o[c] = w != nullptr ? v[i][c] * rstd * g[c] : v[i][c] * rstd;
-      if (b != nullptr) {
-        get_f<V>(b + (l + i * G) * V, g);
-#pragma unroll
-        for (int c = 0; c < V; ++c) o[c] += g[c];
-      }
-      Ld<T, V>::put(y + (l + i * G) * V, o);
     }
-  if (stats != nullptr && l == 0) stats[2 * row] = mean, stats[2 * row + 1] = rstd;
+    group_sums<G, R>(mean, red[turn][0]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] *= inv;
+      sq[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (l + i * G < nv) {
+          float x[V];
+          now.x[r][i].unpack(x);
+#pragma unroll
+          for (int c = 0; c < V; ++c) sq[r] = fmaf(x[c] - mean[r], x[c] - mean[r], sq[r]);
+        }
+    }
+    group_sums<G, R>(sq, red[turn][1]);
+    turn ^= 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float rstd = 1.f / sqrtf(sq[r] * inv + eps);
+      if (row + r >= rows) continue;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (l + i * G < nv) {
+          float x[V];
+          now.x[r][i].unpack(x);
+#pragma unroll
+          for (int c = 0; c < V; ++c) x[c] = fmaf((x[c] - mean[r]) * rstd, ww[i][c], bb[i][c]);
+          Ld<T, V>::put(Y + (row + r) * dim + (l + i * G) * V, x);
+        }
+      if (stats != nullptr && l == 0) stats[2 * (row + r)] = mean[r], stats[2 * (row + r) + 1] = rstd;
+    }
+    now = next;
+  }
 }
 
 // Rows wider than the registers of a block: a block of 512 threads reads its row
@@ -200,47 +329,34 @@ __global__ void __launch_bounds__(512)
   if (stats != nullptr && threadIdx.x == 0) stats[2 * row] = mean, stats[2 * row + 1] = rstd;
 }
 
-// Sums of N values over the G threads of a group at once; one barrier.
-template <int G, int N>
-__device__ __forceinline__ void group_sums(float (&x)[N], float (*red)[G / 32]) {
-#pragma unroll
-  for (int m = 16; m > 0; m /= 2)
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], m);
-  if (G > 32) {
-    if (threadIdx.x % 32 == 0)
-#pragma unroll
-      for (int i = 0; i < N; ++i) red[i][threadIdx.x / 32] = x[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x[i] = 0.f;
-#pragma unroll
-      for (int w = 0; w < G / 32; ++w) x[i] += red[i][w];
-    }
-  }
-}
-
 // One block's sums over its rows, columns in place: part[2][blocks][dim], dw then db.
 // A group takes R rows at a time, whose 2 R sums share a barrier; the next R rows
 // are loaded meanwhile.  Rows wait as they lie in memory and are unpacked when
 // they are used (twice): registers for rows in flight, not for their conversion.
 template <typename T, int V, int G, int NV, int R, bool COLS>
-__global__ void __launch_bounds__(block_of(G))
+__global__ void __launch_bounds__(block_of(G), backward_resident(G))
     norm_backward_kernel(const T* X, int64_t ldx, const T* dY, int64_t lddy, int64_t rows, int dim,
                          const float* __restrict__ w, const float* __restrict__ stats, T* dX,
                          float* part) {
   constexpr int GR = block_of(G) / G;  // groups of a block
-  __shared__ float red[2][2 * R][G / 32];
+  __shared__ float red[2][2 * R][warps_of(G)];
   extern __shared__ float cols[];  // [GR > 1 ? dim : 0]
   const int l = threadIdx.x % G, nv = dim / V;
   const float inv = 1.f / dim;
-  float aw[COLS ? NV : 1][V] = {}, ab[COLS ? NV : 1][V] = {}, ww[NV][V];
+  constexpr int P = (V + 1) / 2;  // pairs
+  using N = Num<V>;
+  N aw[COLS ? NV : 1][P], ab[COLS ? NV : 1][P], ww[NV][P];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
+    float v[V];
 #pragma unroll
-    for (int c = 0; c < V; ++c) ww[i][c] = 1.f;
-    if (w != nullptr && l + i * G < nv) get_f<V>(w + (l + i * G) * V, ww[i]);
+    for (int c = 0; c < V; ++c) v[c] = 1.f;
+    if (w != nullptr && l + i * G < nv) get_f<V>(w + (l + i * G) * V, v);
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+      ww[i][c] = pair<V>(v, c);
+      if (COLS) aw[i][c] = ab[i][c] = N(0.f);
+    }
   }
   struct Rows {
     Raw<T, V> x[R][NV], g[R][NV];
@@ -268,53 +384,63 @@ __global__ void __launch_bounds__(block_of(G))
   Rows now, next;
   load(now, row);
   int turn = 0;
-  for (; row < rows; row += step) {
+  // the lanes of a warp stay together: groups whose rows have ended go along with nothing
+  const int64_t lead = G < 32 ? threadIdx.x % 32 / G * R : 0;
+  for (; row - lead < rows; row += step) {
     // in place is in order: dX's rows are this step's, the loads the next one's
     load(next, row + step);
+    // Values go in pairs (one instruction for two where there are two).  With d = x - mean,
+    // per row: s1 = sum g w, s2 = sum g w d;  dx = rstd (g w) - rstd^3 s2/n d - rstd s1/n.
     float sums[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float s1 = 0.f, s2 = 0.f;
+      const N mean(-now.mean[r]), rstd(now.rstd[r]);
+      N s1(0.f), s2(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (l + i * G < nv) {
-          float x[V], g[V];
-          now.x[r][i].unpack(x);
-          now.g[r][i].unpack(g);
+          float xs[V], gs[V];
+          now.x[r][i].unpack(xs);
+          now.g[r][i].unpack(gs);
 #pragma unroll
-          for (int c = 0; c < V; ++c) {
-            x[c] = (x[c] - now.mean[r]) * now.rstd[r];
+          for (int c = 0; c < P; ++c) {
+            const N d = add(pair<V>(xs, c), mean), g = pair<V>(gs, c);
             if (COLS) {
-              aw[i][c] = fmaf(g[c], x[c], aw[i][c]);
-              ab[i][c] += g[c];
+              aw[i][c] = fma(mul(g, rstd), d, aw[i][c]);
+              ab[i][c] = add(ab[i][c], g);
             }
-            g[c] *= ww[i][c];
-            s1 += g[c];
-            s2 = fmaf(g[c], x[c], s2);
+            const N gw = mul(g, ww[i][c]);
+            s1 = add(s1, gw);
+            s2 = fma(gw, d, s2);
           }
         }
-      sums[2 * r] = s1;
-      sums[2 * r + 1] = s2;
+      sums[2 * r] = s1.sum();
+      sums[2 * r + 1] = s2.sum();
     }
     if (dX != nullptr) {  // the same for the whole grid
       group_sums<G, 2 * R>(sums, red[turn]);
       turn ^= 1;
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
+        const float rs = now.rstd[r];
+        const N mean(-now.mean[r]), rstd(rs), k1(-rs * (sums[2 * r] * inv)),
+            k2(-rs * rs * rs * (sums[2 * r + 1] * inv));
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (row + r < rows && l + i * G < nv) {
-            float x[V], g[V];
-            now.x[r][i].unpack(x);
-            now.g[r][i].unpack(g);
+            float xs[V], gs[V];
+            now.x[r][i].unpack(xs);
+            now.g[r][i].unpack(gs);
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
-              x[c] = (x[c] - now.mean[r]) * now.rstd[r];
-              g[c] = now.rstd[r] *
-                     (g[c] * ww[i][c] - sums[2 * r] * inv - x[c] * (sums[2 * r + 1] * inv));
+            for (int c = 0; c < P; ++c) {
+              const N d = add(pair<V>(xs, c), mean);
+              const N y = fma(mul(pair<V>(gs, c), ww[i][c]), rstd, fma(d, k2, k1));
+              gs[2 * c] = y.x();
+              if (V > 1) gs[(2 * c + 1) % V] = y.y();
             }
-            Ld<T, V>::put(dX + (row + r) * dim + (l + i * G) * V, g);
+            Ld<T, V>::put(dX + (row + r) * dim + (l + i * G) * V, gs);
           }
+      }
     }
     now = next;
   }
@@ -322,14 +448,15 @@ __global__ void __launch_bounds__(block_of(G))
     float* pw = part + (size_t)blockIdx.x * dim;
     float* pb = pw + (size_t)gridDim.x * dim;
     for (int which = 0; which < 2; ++which) {
-      float(&acc)[COLS ? NV : 1][V] = which == 0 ? aw : ab;
+      N(&acc)[COLS ? NV : 1][P] = which == 0 ? aw : ab;
       float* out = which == 0 ? pw : pb;
+      const auto value = [&](int i, int c) { return c % 2 == 0 ? acc[i][c / 2].x() : acc[i][c / 2].y(); };
       if (GR == 1) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (l + i * G < nv)
 #pragma unroll
-            for (int c = 0; c < V; ++c) out[(l + i * G) * V + c] = acc[i][c];
+            for (int c = 0; c < V; ++c) out[(l + i * G) * V + c] = value(i, c);
       } else {  // the block's groups in turn
         for (int r = 0; r < GR; ++r) {
           if ((int)threadIdx.x / G == r)
@@ -339,7 +466,7 @@ __global__ void __launch_bounds__(block_of(G))
 #pragma unroll
                 for (int c = 0; c < V; ++c) {
                   float& z = cols[(l + i * G) * V + c];
-                  z = r == 0 ? acc[i][c] : z + acc[i][c];
+                  z = r == 0 ? value(i, c) : z + value(i, c);
                 }
           __syncthreads();
         }
@@ -433,34 +560,21 @@ int pow2_at_least(int64_t x) {
   while (p < x) p *= 2;
   return p;
 }
-// Forward: rows in flight are what counts (a row's time is a chain of latencies),
-// so few registers: a warp for each row up to 32 values a lane (16 where they are
-// loaded one by one), then 4 warps, then 16; few rows take the larger group that
-// still has a vector for every thread.
-Shape forward_shape(const NormArgs& a, bool aligned) {
+// At most 16 values a thread (32 in the largest group, forward).
+Shape shape_of(const NormArgs& a, bool aligned, bool forward) {
   Shape s = {vector_of(a, aligned), 0, 0, 1};
   const int64_t nv = a.dim / s.V;
-  const int64_t most = (s.V == 1 ? 16 : 32) / s.V;
-  s.G = nv <= 32 * most ? 32 : nv <= 128 * most ? 128 : nv <= 512 * most ? 512 : 0;
-  if (s.G == 0) return s;
-  while (s.G < 512 && a.rows * (s.G / 32) < 148 * 8 && nv >= s.G * 4) s.G *= 4;
-  s.NV = pow2_at_least((nv + s.G - 1) / s.G);
-  return s;
-}
-// Backward: a thread holds its columns' two sums and the weight besides, so at most
-// 8 to 16 values, and R rows so that 32 values are in flight.
-constexpr int rows_at_once(int nv, int v) {
-  const int r = (v == 1 ? 16 : 32) / (nv * v);  // single values take a register each
-  return r < 1 ? 1 : r > 4 ? 4 : r;
-}
-Shape backward_shape(const NormArgs& a, bool aligned) {
-  Shape s = {vector_of(a, aligned), 0, 0, 1};
-  const int64_t nv = a.dim / s.V;
-  const int most = 16 / s.V;  // vectors a thread: 16 values (fp32: 4 vectors, bf16: 2)
-  s.G = nv <= 32 * most ? 32 : nv <= 128 * most ? 128 : nv <= 512 * most ? 512 : 0;
+  const int most = 16 / s.V, last = forward ? 2 * most : most;
+  // 8 lanes up to 64 values: a warp would leave three quarters of its lanes without
+  s.G = nv <= 8 * (most < 4 ? 1 : 2) && a.dim <= 64 ? 8
+        : nv <= 32 * most                          ? 32
+        : nv <= 128 * most                         ? 128
+        : nv <= 256 * most                         ? 256
+        : nv <= 512 * last                         ? 512
+                                                   : 0;
   if (s.G == 0) return s;
   s.NV = pow2_at_least((nv + s.G - 1) / s.G);
-  s.R = rows_at_once(s.NV, s.V);
+  s.R = rows_at_once(s.G, s.NV, s.V, !forward && !a.bf16);
   return s;
 }
 
@@ -469,11 +583,12 @@ bool vector_rows(const NormArgs& a, int64_t ldx, int64_t ldy) {
   return ldx % full == 0 && ldy % full == 0;
 }
 
-// Blocks of the backward kernel (and the rows of its partial sums).
-int backward_blocks(const NormArgs& a, const Shape& s) {
-  const int64_t rb = (s.G == 32 ? 8 : 1) * s.R;
+// Blocks of the kernels (and the rows of the backward kernel's partial sums).
+int blocks_of(const NormArgs& a, const Shape& s, bool forward) {
+  const int64_t rb = block_of(s.G) / s.G * s.R;
   const int64_t need = (a.rows + rb - 1) / rb;
-  const int64_t most = 148 * (s.G == 512 ? 2 : s.G == 128 ? 5 : 3);
+  const int64_t most =
+      148 * (forward ? (s.G == 512 ? 2 : s.G == 128 ? 8 : 4) : backward_resident(s.G));
   return (int)(need < most ? (need < 1 ? 1 : need) : most);
 }
 int wide_blocks(const NormArgs& a) { return (int)(a.rows < 64 ? (a.rows < 1 ? 1 : a.rows) : 64); }
@@ -484,11 +599,11 @@ struct Forward {
   const float *w, *b;
   void* Y;
   float* stats;
+  int blocks;
 };
 template <typename T, int V, int G, int NV>
 cudaError_t launch_forward(const NormArgs& a, const Forward& f, cudaStream_t st) {
-  constexpr int rb = block_of(G) / G;
-  norm_kernel<T, V, G, NV><<<(unsigned)((a.rows + rb - 1) / rb), block_of(G), 0, st>>>(
+  norm_kernel<T, V, G, NV, rows_at_once(G, NV, V, false)><<<f.blocks, block_of(G), 0, st>>>(
       static_cast<const T*>(f.X), f.ldx, a.rows, (int)a.dim, a.eps, f.w, f.b,
       static_cast<T*>(f.Y), f.stats);
   return cudaGetLastError();
@@ -502,10 +617,11 @@ cudaError_t forward_by_nv(int nv, const NormArgs& a, const Forward& f, cudaStrea
 }
 template <typename T, int V>
 cudaError_t forward_by_g(const Shape& s, const NormArgs& a, const Forward& f, cudaStream_t st) {
-  constexpr int MOST = (V == 1 ? 16 : 32) / V;
-  return s.G == 32    ? forward_by_nv<T, V, 32, MOST>(s.NV, a, f, st)
-         : s.G == 128 ? forward_by_nv<T, V, 128, MOST>(s.NV, a, f, st)
-                      : forward_by_nv<T, V, 512, MOST>(s.NV, a, f, st);
+  return s.G == 8     ? forward_by_nv<T, V, 8, V == 8 ? 1 : 2>(s.NV, a, f, st)
+         : s.G == 32  ? forward_by_nv<T, V, 32, 16 / V>(s.NV, a, f, st)
+         : s.G == 128 ? forward_by_nv<T, V, 128, 16 / V>(s.NV, a, f, st)
+         : s.G == 256 ? forward_by_nv<T, V, 256, 16 / V>(s.NV, a, f, st)
+                      : forward_by_nv<T, V, 512, 32 / V>(s.NV, a, f, st);
 }
 
 struct Backward {
@@ -520,7 +636,7 @@ struct Backward {
 };
 template <typename T, int V, int G, int NV>
 cudaError_t launch_backward(const NormArgs& a, const Backward& b, cudaStream_t st) {
-  constexpr int R = rows_at_once(NV, V);
+  constexpr int R = rows_at_once(G, NV, V, sizeof(T) == 4);
   const auto go = [&](auto kernel, int smem) {
     kernel<<<b.blocks, block_of(G), smem, st>>>(static_cast<const T*>(b.X), b.ldx,
                                                 static_cast<const T*>(b.dY), b.lddy, a.rows,
@@ -529,20 +645,22 @@ cudaError_t launch_backward(const NormArgs& a, const Backward& b, cudaStream_t s
     return cudaGetLastError();
   };
   if (b.part != nullptr)
-    return go(norm_backward_kernel<T, V, G, NV, R, true>, G == 32 ? (int)a.dim * 4 : 0);
+    return go(norm_backward_kernel<T, V, G, NV, R, true>, G <= 32 ? (int)a.dim * 4 : 0);
   return go(norm_backward_kernel<T, V, G, NV, R, false>, 0);
 }
-template <typename T, int V, int G, int NV = 1>
+template <typename T, int V, int G, int MOST, int NV = 1>
 cudaError_t backward_by_nv(int nv, const NormArgs& a, const Backward& b, cudaStream_t st) {
-  if constexpr (NV < 16 / V)
-    if (nv > NV) return backward_by_nv<T, V, G, 2 * NV>(nv, a, b, st);
+  if constexpr (NV < MOST)
+    if (nv > NV) return backward_by_nv<T, V, G, MOST, 2 * NV>(nv, a, b, st);
   return launch_backward<T, V, G, NV>(a, b, st);
 }
 template <typename T, int V>
 cudaError_t backward_by_g(const Shape& s, const NormArgs& a, const Backward& b, cudaStream_t st) {
-  return s.G == 32    ? backward_by_nv<T, V, 32>(s.NV, a, b, st)
-         : s.G == 128 ? backward_by_nv<T, V, 128>(s.NV, a, b, st)
-                      : backward_by_nv<T, V, 512>(s.NV, a, b, st);
+  return s.G == 8     ? backward_by_nv<T, V, 8, V == 8 ? 1 : 2>(s.NV, a, b, st)
+         : s.G == 32  ? backward_by_nv<T, V, 32, 16 / V>(s.NV, a, b, st)
+         : s.G == 128 ? backward_by_nv<T, V, 128, 16 / V>(s.NV, a, b, st)
+         : s.G == 256 ? backward_by_nv<T, V, 256, 16 / V>(s.NV, a, b, st)
+                      : backward_by_nv<T, V, 512, 16 / V>(s.NV, a, b, st);
 }
 
 }  // namespace
@@ -551,8 +669,8 @@ size_t norm_workspace_bytes(const NormArgs& a) {
   // the largest of the plans that strides may ask for
   size_t most = (size_t)wide_blocks(a);
   for (int aligned = 0; aligned < 2; ++aligned) {
-    const Shape s = backward_shape(a, aligned != 0);
-    if (s.G != 0 && (size_t)backward_blocks(a, s) > most) most = (size_t)backward_blocks(a, s);
+    const Shape s = shape_of(a, aligned != 0, false);
+    if (s.G != 0 && (size_t)blocks_of(a, s, false) > most) most = (size_t)blocks_of(a, s, false);
   }
   return most * 2 * (size_t)a.dim * 4;
 }
@@ -560,7 +678,7 @@ size_t norm_workspace_bytes(const NormArgs& a) {
 cudaError_t norm_forward(const NormArgs& a, const void* X, int64_t ldx, const float* w,
                          const float* b, void* Y, float* stats, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
-  const Shape s = forward_shape(a, vector_rows(a, ldx, a.dim));
+  const Shape s = shape_of(a, vector_rows(a, ldx, a.dim), true);
   TraceScope ts("layer_norm", st);
   if (s.G == 0) {
     if (a.bf16)
@@ -573,7 +691,7 @@ cudaError_t norm_forward(const NormArgs& a, const void* X, int64_t ldx, const fl
                                                          static_cast<float*>(Y), stats);
     return cudaGetLastError();
   }
-  const Forward f = {X, ldx, w, b, Y, stats};
+  const Forward f = {X, ldx, w, b, Y, stats, blocks_of(a, s, true)};
   if (a.bf16)
     return s.V == 8 ? forward_by_g<__nv_bfloat16, 8>(s, a, f, st)
                     : forward_by_g<__nv_bfloat16, 1>(s, a, f, st);
@@ -590,7 +708,7 @@ cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const v
     if (e == cudaSuccess && db != nullptr) e = cudaMemsetAsync(db, 0, (size_t)a.dim * 4, st);
     return e;
   }
-  const Shape s = backward_shape(a, vector_rows(a, ldx, lddy));
+  const Shape s = shape_of(a, vector_rows(a, ldx, lddy), false);
   float* part = cols ? static_cast<float*>(ws) : nullptr;
   cudaError_t e = cudaSuccess;
   int blocks;
@@ -619,7 +737,7 @@ cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const v
     }
     e = cudaGetLastError();
   } else {
-    blocks = backward_blocks(a, s);
+    blocks = blocks_of(a, s, false);
     TraceScope ts("layer_norm_backward", st);
     const Backward b = {X, ldx, dY, lddy, w, stats, dX, part, blocks};
     if (a.bf16)
