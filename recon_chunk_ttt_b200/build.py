@@ -30,6 +30,7 @@ NVCC_FLAGS = [
     "-lineinfo",
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
+    "--threads", "0",  # the files side by side
 ]
 
 
