@@ -158,21 +158,13 @@ __device__ __forceinline__ uint32_t tri(int row, int col) {
          (col & 7) * 2;
 }
 
-// 32 columns, as [64][32] with the 64-byte swizzle.
-inline bool strip32_map(CUtensorMap* m, const void* base, int64_t n, int64_t ld, int cols) {
-  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)n};
-  const uint64_t str[1] = {(uint64_t)ld * 2};
-  const uint32_t box[2] = {32, kC};
-  return make_map(m, base, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
 // Every kAnchor-th chunk the state is kept in fp32: there the gradient of the decays,
 // a running sum over tokens, starts anew.
 constexpr int kAnchor = 8;
 
 // Stores of accumulators for a later kernel, as bf16 in blocks of 8 x 8 values (8
 // rows of 16 bytes: what ldmatrix reads, and a whole line for a warp to write).
-// The state [D rows][DK columns from c0]: blocks [column / 32][row / 8][column / 8 % 4].
+// The state [D rows][DK columns from c0]: blocks [column / 16][row / 8][column / 8 % 2].
 template <int D, int DK>
 __device__ __forceinline__ void keep_state(__nv_bfloat16* to, const float (&s)[DK / 8][4], int r0,
                                            int c0, int lane) {
@@ -180,9 +172,9 @@ __device__ __forceinline__ void keep_state(__nv_bfloat16* to, const float (&s)[D
 #pragma unroll
   for (int j = 0; j < DK / 8; ++j) {
     const int c = c0 / 8 + j;
-    const int block = (c / 4 * (D / 8) + r0 / 8) * 4 + c % 4;
+    const int block = (c / 2 * (D / 8) + r0 / 8) * 2 + c % 2;
     w[block * 32 + lane] = pack_bf16x2(s[j][0], s[j][1]);
-    w[(block + 4) * 32 + lane] = pack_bf16x2(s[j][2], s[j][3]);
+    w[(block + 2) * 32 + lane] = pack_bf16x2(s[j][2], s[j][3]);
   }
 }
 // 16 rows of the transpose of a [64 tokens][D] array, token tile t: blocks [row / 8][token / 8].
@@ -270,7 +262,7 @@ inline bool strip_map(CUtensorMap* m, const void* base, int64_t n, int64_t ld, i
 // What the forward pass leaves for the gradient, by chunk slot and head.
 struct DeltaKept {
   __nv_bfloat16* S0;  // the state before the chunk
-  __nv_bfloat16* U;   // [d][64 tokens]
+  __nv_bfloat16* U;   // [d][64 tokens]: rounded, and what the rounding left
   float* U32;         // U in fp32, as registers lie
   float* anchors;     // the state before every kAnchor-th chunk of a sequence
   float* last;        // the last states, or nullptr

@@ -12,8 +12,8 @@
 // from the end, started anew from a product of the two states every 512 tokens.
 //
 // Four kernels: the inverses of all chunks; the forward chain once more, which
-// keeps each chunk's state and U (rounded to bf16: they only enter dQ and dK,
-// which are bf16) and the sums of dO . O; delta_reverse_kernel, the chain of E from
+// keeps each chunk's state and U (in bf16, U in two parts: they only enter dQ and
+// dK, which are bf16) and the sums of dO . O; delta_reverse_kernel, the chain of E from
 // the last chunk to the first; delta_tokens_grad_kernel, dQ and dK of all chunks
 // at once, and the running sums; where heads share a key head a fifth adds their
 // shares.  The chains carry fp32 in three bf16 parts
@@ -540,22 +540,27 @@ __device__ __forceinline__ void gate_stretch(const GateArgs& a, const int64_t* o
 
 // ----------------------------------------------------------------------------
 // delta_tokens_grad_kernel: dQ and dK of one chunk and head.  8 warps: 4 blocks
-// of 16 tokens x 2 halves of the columns at hand.  dO, U, dV stay in shared memory;
-// S, E, Q, K pass in strips of 32 columns, two deep.
+// of 16 tokens; of the two warps of a block one takes the products with S (dQ's, and
+// dV S, which it hands over), the other those with E (dK's).  dO, U, dV stay in
+// shared memory; S, E, Q, K pass in strips of 16 columns, two deep, and two blocks
+// share an SM (d = 256: one).  U and A enter in two parts: with one each, dK is off
+// by 3.0e-3 and dQ by 2.7e-3 of which 1.7e-3 are the results' own rounding; so 2.4e-3
+// and 2.1e-3.  Two parts of S, E, dV as well would leave 1.9e-3 for twice the traffic.
 // ----------------------------------------------------------------------------
 template <int D>
 struct GK {
-  static constexpr int TOK = kC * D * 2;        // one of dO, U, dV
-  static constexpr int ST = D * 32 * 2;         // 32 columns of S or E
-  static constexpr int QS = kC * 64;            // 32 columns of Q or K
+  static constexpr int TOK = kC * D * 2;        // one of dO, U (two parts), dV
+  static constexpr int ST = D * 16 * 2;         // 16 columns of S or E
+  static constexpr int QS = kC * 32;            // 16 columns of Q or K
   static constexpr int STRIP = 2 * ST + 2 * QS;
-  static constexpr int NS = D / 32;
-  static constexpr int OFF_S = 3 * TOK;
-  static constexpr int OFF_M = OFF_S + 2 * STRIP;
-  static constexpr int OFF_A = OFF_M + kC * 128;
-  static constexpr int OFF_BAR = OFF_A + kTri;
+  static constexpr int NS = D / 16;
+  static constexpr int OFF_S = 4 * TOK;
+  static constexpr int OFF_A = OFF_S + 2 * STRIP;       // A in two parts, M: triangles
+  static constexpr int OFF_X = OFF_A + 3 * kTri;        // dV S handed over, two deep
+  static constexpr int X = 4 * 2 * 32 * 16;
+  static constexpr int OFF_BAR = OFF_X + 2 * X;
   static constexpr int SMEM = OFF_BAR + 64 + 1024;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(SMEM <= (D == 256 ? 227 : 113) * 1024, "shared memory");
 };
 
 struct TokensGradArgs {
@@ -582,8 +587,8 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   __shared__ float Gh[kC], Gl[kC];  // running sums of the log decays in two parts
-  uint8_t *pG = smem, *pU = smem + L::TOK, *pV = smem + 2 * L::TOK, *pS = smem + L::OFF_S,
-          *pM = smem + L::OFF_M, *pA = smem + L::OFF_A;
+  uint8_t *pG = smem, *pU = smem + L::TOK, *pV = smem + 3 * L::TOK, *pS = smem + L::OFF_S,
+          *pA = smem + L::OFF_A, *pM = pA + 2 * kTri;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);  // tokens, strips
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 3);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -600,18 +605,18 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     uint8_t* to = pS + s % 2 * L::STRIP;
     uint64_t* b = &bar[1 + s % 2];
     mbar_arrive_expect_tx(b, L::STRIP);
-    bulk_load(to, a.S0 + at * D * D + s * (D * 32), L::ST, b);
-    bulk_load(to + L::ST, a.E + at * D * D + s * (D * 32), L::ST, b);
-    tma_load_2d(to + 2 * L::ST, &mQ, b, hk * D + s * 32, (int)c.t0);
-    tma_load_2d(to + 2 * L::ST + L::QS, &mK, b, hk * D + s * 32, (int)c.t0);
+    bulk_load(to, a.S0 + at * D * D + s * (D * 16), L::ST, b);
+    bulk_load(to + L::ST, a.E + at * D * D + s * (D * 16), L::ST, b);
+    tma_load_2d(to + 2 * L::ST, &mQ, b, hk * D + s * 16, (int)c.t0);
+    tma_load_2d(to + 2 * L::ST + L::QS, &mK, b, hk * D + s * 16, (int)c.t0);
   };
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
-    mbar_arrive_expect_tx(&bar[0], 3 * L::TOK);
+    mbar_arrive_expect_tx(&bar[0], 4 * L::TOK);
     tma_load_3d(pG, &mG, &bar[0], 0, (int)c.t0, h * (D / 64));
-    bulk_load(pU, a.U + at * kC * D, L::TOK, &bar[0]);
+    bulk_load(pU, a.U + 2 * at * kC * D, 2 * L::TOK, &bar[0]);
     bulk_load(pV, a.dVt + at * kC * D, L::TOK, &bar[0]);
     load_strip(0);
     load_strip(1);
@@ -653,7 +658,7 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     return (uint32_t)(((k / 8 + lane / 8 % 2) * 8 + t / 8 + lane / 16) * 128 + lane % 8 * 16);
   };
 
-  // dO U^T and dV U^T: 16 tokens i x 32 tokens j
+  // dO U^T (both parts of U) and dV U^T: 16 tokens i x 32 tokens j
   {
     float dp[4][4] = {}, dl[4][4] = {};
 #pragma unroll 4
@@ -663,36 +668,36 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
       ldsm4_t(sV + blk_a(k, m0), av);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        ldsm4_t(sU + blk_b(k, half * 32 + p * 16), b);
+        const uint32_t o = sU + blk_b(k, half * 32 + p * 16);
+        ldsm4_t(o + L::TOK, b);
+        mma(dp[2 * p], ag, b[0], b[1]);
+        mma(dp[2 * p + 1], ag, b[2], b[3]);
+        ldsm4_t(o, b);
         mma(dp[2 * p], ag, b[0], b[1]);
         mma(dp[2 * p + 1], ag, b[2], b[3]);
         mma(dl[2 * p], av, b[0], b[1]);
         mma(dl[2 * p + 1], av, b[2], b[3]);
       }
     }
-    // A (rows behind the sequence are zero: dO there may be anything), and M with its
-    // transpose: every (i, j) of the lower part is this warp's alone
+    // A (rows behind the sequence are zero: dO there may be anything) and M
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int i = m0 + row + 8 * y, j = half * 32 + q * 8 + col;
-        float x[2];
+        if (j / 16 > mb) continue;
+        float x[2], m[2], left[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const float e =
               j + z <= i ? expf((Gh[i] - Gh[j + z]) + (Gl[i] - Gl[j + z])) : 0.f;
           x[z] = j + z <= i && i < c.len ? a.scale * e * dp[q][2 * y + z] : 0.f;
-          const __nv_bfloat16 v = __float2bfloat16_rn(-e * dl[q][2 * y + z]);
-          if (j + z < i) {
-            *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, i, j + z)) = v;
-            *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, j + z, i)) = v;
-          } else if (j + z == i) {
-            *reinterpret_cast<__nv_bfloat16*>(pM + sw(kC, i, i)) = __float2bfloat16_rn(0.f);
-          }
+          left[z] = x[z] - __bfloat162float(__float2bfloat16_rn(x[z]));
+          m[z] = j + z < i ? -e * dl[q][2 * y + z] : 0.f;
         }
-        if (j / 16 <= mb)
-          *reinterpret_cast<uint32_t*>(pA + tri(i, j)) = pack_bf16x2(x[0], x[1]);
+        *reinterpret_cast<uint32_t*>(pA + tri(i, j)) = pack_bf16x2(x[0], x[1]);
+        *reinterpret_cast<uint32_t*>(pA + kTri + tri(i, j)) = pack_bf16x2(left[0], left[1]);
+        *reinterpret_cast<uint32_t*>(pM + tri(i, j)) = pack_bf16x2(m[0], m[1]);
       }
   }
   __syncthreads();
@@ -704,67 +709,103 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     gi[y] = expf(Gh[i] + Gl[i]);
     re[y] = expf((Gh[kC - 1] - Gh[i]) + (Gl[kC - 1] - Gl[i]));
   }
-  for (int s = 0; s < L::NS; ++s) {  // 32 columns of dQ, dK at a time; 16 a warp
+  const bool with_e = half == 1;
+  for (int s = 0; s < L::NS; ++s) {  // 16 columns of dQ, dK at a time
     ok = mbar_wait(&bar[1 + s % 2], (uint32_t)(s / 2 & 1), abort_flag, a.err, kErrWaitFull) && ok;
     const uint32_t sS = smem_u32(pS) + s % 2 * L::STRIP, sE = sS + L::ST, sQ = sS + 2 * L::ST,
                    sK = sQ + L::QS;
-    const int cw = half * 16, cs = s * 32 + cw;  // in the strip; in the head
-    float dq[2][4] = {}, dk[2][4] = {}, ve[2][4] = {};
-#pragma unroll 4
-    for (int k = 0; k < D; k += 16) {
-      uint32_t ag[4], av[4], au[4], b[4], e[4];
-      ldsm4(sG + sw(kC, m0 + kn_r, k + kn_c), ag);
-      ldsm4_t(sV + blk_a(k, m0), av);
-      ldsm4_t(sU + blk_a(k, m0), au);
-      // 16 rows x 16 columns of a strip [row / 8][4 column blocks]: stored [k][n]
-      const uint32_t o = (uint32_t)(((k / 8 + lane / 8 % 2) * 4 + cw / 8 + lane / 16) * 128 +
-                                    lane % 8 * 16);
-      ldsm4_t(sS + o, b);
-      ldsm4_t(sE + o, e);
-      mma(dq[0], ag, b[0], b[1]);
-      mma(dq[1], ag, b[2], b[3]);
-      mma(ve[0], av, b[0], b[1]);
-      mma(ve[1], av, b[2], b[3]);
-      mma(dk[0], au, e[0], e[1]);
-      mma(dk[1], au, e[2], e[3]);
+    float4* hand = reinterpret_cast<float4*>(smem + L::OFF_X + s % 2 * L::X) + mb * 64 + lane;
+    // acc: scale gamma dO S, or rest U E;  ve: dV S
+    float acc[2][4] = {}, ve[2][4] = {};
+    {
+      // the next 16 rows' operands are loaded meanwhile
+      const uint32_t from = (with_e ? sE : sS) +
+                            (uint32_t)((lane / 8 % 2 * 2 + lane / 16) * 128 + lane % 8 * 16);
+      uint32_t x[2][4], y[2][4], b[2][4];
+      const auto load = [&](int k, int f) {
+        if (with_e) {
+          ldsm4_t(sU + blk_a(k, m0), x[f]);
+          ldsm4_t(sU + L::TOK + blk_a(k, m0), y[f]);
+        } else {
+          ldsm4(sG + sw(kC, m0 + kn_r, k + kn_c), x[f]);
+          ldsm4_t(sV + blk_a(k, m0), y[f]);
+        }
+        // 16 rows x 16 columns of a strip [row / 8][2 column blocks]: stored [k][n]
+        ldsm4_t(from + (uint32_t)(k / 8 * 256), b[f]);
+      };
+      load(0, 0);
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        const int f = e % 2;
+        if (e + 1 < D / 16) load((e + 1) * 16, 1 - f);
+        mma(acc[0], x[f], b[f][0], b[f][1]);
+        mma(acc[1], x[f], b[f][2], b[f][3]);
+        mma(ve[0], y[f], b[f][0], b[f][1]);
+        mma(ve[1], y[f], b[f][2], b[f][3]);
+      }
     }
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 2; ++x) {
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        dq[x][y] *= a.scale * gi[y / 2];
-        dk[x][y] = re[y / 2] * dk[x][y] - gi[y / 2] * ve[x][y];
+        if (with_e)
+          acc[x][y] = re[y / 2] * (acc[x][y] + ve[x][y]);
+        else
+          acc[x][y] *= a.scale * gi[y / 2];
       }
+      if (!with_e)
+        hand[x * 32] = make_float4(-gi[0] * ve[x][0], -gi[0] * ve[x][1], -gi[1] * ve[x][2],
+                                   -gi[1] * ve[x][3]);
+    }
+    // + A K, or + A^T Q + (M + M^T) K
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       const int k = kb * 16;
+      if (!with_e && kb > mb) break;
       uint32_t x[4], bk[4], bq[4];
-      // rows of Q and K, 64 bytes each, 16-byte unit u of row r at u ^ (r / 2 % 4)
-      const int r = k + kn_r, u = cw / 8 + lane / 16;
-      const uint32_t o = (uint32_t)(r * 64 + ((u ^ (r >> 1 & 3)) << 4));
+      const uint32_t o = sw32(k + kn_r, lane / 16);
+      // rows behind the sequence may hold anything and count as zero
+      const uint32_t k0 = keep_pair(k + col, c.len), k1 = keep_pair(k + 8 + col, c.len);
       ldsm4_t(sK + o, bk);
-      ldsm4_t(sQ + o, bq);
-      if (c.len < kC) {  // rows behind the sequence may hold anything and count as zero
-        const uint32_t k0 = keep_pair(k + col, c.len), k1 = keep_pair(k + 8 + col, c.len);
-        bk[0] &= k0, bk[1] &= k1, bk[2] &= k0, bk[3] &= k1;
-        bq[0] &= k0, bq[1] &= k1, bq[2] &= k0, bq[3] &= k1;
+      bk[0] &= k0, bk[1] &= k1, bk[2] &= k0, bk[3] &= k1;
+      if (!with_e) {
+#pragma unroll
+        for (int part = 1; part >= 0; --part) {
+          ldsm4(sA + part * kTri + tri(m0 + kn_r, k + kn_c), x);
+          mma(acc[0], x, bk[0], bk[1]);
+          mma(acc[1], x, bk[2], bk[3]);
+        }
+        continue;
       }
       if (kb <= mb) {
-        ldsm4(sA + tri(m0 + kn_r, k + kn_c), x);
-        mma(dq[0], x, bk[0], bk[1]);
-        mma(dq[1], x, bk[2], bk[3]);
+        ldsm4(sM + tri(m0 + kn_r, k + kn_c), x);
+        mma(acc[0], x, bk[0], bk[1]);
+        mma(acc[1], x, bk[2], bk[3]);
       }
-      if (kb >= mb) {  // the transpose of A: rows are its columns
-        ldsm4_t(sA + tri(k + nk_r, m0 + nk_c), x);
-        mma(dk[0], x, bq[0], bq[1]);
-        mma(dk[1], x, bq[2], bq[3]);
+      if (kb >= mb) {  // transposes: their rows are the columns
+        ldsm4_t(sM + tri(k + nk_r, m0 + nk_c), x);
+        mma(acc[0], x, bk[0], bk[1]);
+        mma(acc[1], x, bk[2], bk[3]);
+        ldsm4_t(sQ + o, bq);
+        bq[0] &= k0, bq[1] &= k1, bq[2] &= k0, bq[3] &= k1;
+#pragma unroll
+        for (int part = 1; part >= 0; --part) {
+          ldsm4_t(sA + part * kTri + tri(k + nk_r, m0 + nk_c), x);
+          mma(acc[0], x, bq[0], bq[1]);
+          mma(acc[1], x, bq[2], bq[3]);
+        }
       }
-      ldsm4(sM + sw(kC, m0 + kn_r, k + kn_c), x);
-      mma(dk[0], x, bk[0], bk[1]);
-      mma(dk[1], x, bk[2], bk[3]);
     }
-    __syncthreads();  // the strip has been read
+    __syncthreads();  // the strip has been read, dV S is there
     if (tid == 0 && s + 2 < L::NS) load_strip(s + 2);
+    if (with_e)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float4 v = hand[x * 32];
+        acc[x][0] += v.x, acc[x][1] += v.y, acc[x][2] += v.z, acc[x][3] += v.w;
+      }
+    float* shares = with_e ? a.pk : a.pq;
+    __nv_bfloat16* grads = with_e ? a.dK : a.dQ;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -772,15 +813,13 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
         const int i = m0 + row + 8 * y;
         if (i >= c.len) continue;
         const int64_t t = c.t0 + i;
-        if (a.pq != nullptr) {
-          const int64_t o = t * a.H * D + h * D + cs + x * 8 + col;
-          *reinterpret_cast<float2*>(a.pq + o) = make_float2(dq[x][2 * y], dq[x][2 * y + 1]);
-          *reinterpret_cast<float2*>(a.pk + o) = make_float2(dk[x][2 * y], dk[x][2 * y + 1]);
-        } else {
-          const int64_t o = t * a.Hk * D + h * D + cs + x * 8 + col;
-          *reinterpret_cast<uint32_t*>(a.dQ + o) = pack_bf16x2(dq[x][2 * y], dq[x][2 * y + 1]);
-          *reinterpret_cast<uint32_t*>(a.dK + o) = pack_bf16x2(dk[x][2 * y], dk[x][2 * y + 1]);
-        }
+        const int cs = s * 16 + x * 8 + col;
+        if (shares != nullptr)
+          *reinterpret_cast<float2*>(shares + t * a.H * D + h * D + cs) =
+              make_float2(acc[x][2 * y], acc[x][2 * y + 1]);
+        else
+          *reinterpret_cast<uint32_t*>(grads + t * a.Hk * D + h * D + cs) =
+              pack_bf16x2(acc[x][2 * y], acc[x][2 * y + 1]);
       }
   }
   if (!ok && tid == 0) {  // a wait gave up: the copies must land before the block is gone
@@ -810,7 +849,7 @@ Plan plan_of(const DeltaArgs& a) {
   p.blocks = take(blocks_bytes(a, 3)) + kOrderBytes;
   p.S0 = take(ch * DD * 2);
   p.E = take(ch * DD * 2);
-  p.U = take(ch * kC * D * 2);
+  p.U = take(2 * ch * kC * D * 2);
   p.dVt = take(ch * kC * D * 2);
   p.U32 = take(ch * kC * D * 4);
   p.anchors = take(an * DD * 4);
@@ -866,7 +905,7 @@ cudaError_t launch_tokens(const DeltaArgs& a, const Call& x, char* w, const Plan
                           const GateArgs& gates, cudaStream_t st) {
   using L = GK<D>;
   CUtensorMap mQ, mK, mG;
-  if (!strip32_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D) || !strip32_map(&mK, a.K, a.n, a.ldk, a.Hk * D) ||
+  if (!strip_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D) || !strip_map(&mK, a.K, a.n, a.ldk, a.Hk * D) ||
       !head_map(&mG, x.dO, a.n, (int64_t)a.H * D, a.H * D, D))
     return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem_attr(delta_tokens_grad_kernel<D>, L::SMEM);

@@ -612,7 +612,11 @@ __global__ void __launch_bounds__(SK<D, KS, RG, ST, GRAD>::THREADS, ST == 1 ? 2 
       d[64] = make_uint2(mid[0], mid[1]);
       if (GRAD) {
         d[320] = make_uint2(lo[0], lo[1]);
-        keep_tile<D>(a.kept.U + at * kC * D, ut[j], r0, t, lane);
+        float left[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) left[y] = ut[j][y] - __bfloat162float(__float2bfloat16_rn(ut[j][y]));
+        keep_tile<D>(a.kept.U + 2 * at * kC * D, ut[j], r0, t, lane);
+        keep_tile<D>(a.kept.U + (2 * at + 1) * kC * D, left, r0, t, lane);
         reinterpret_cast<float4*>(a.kept.U32)[((at * (D / 16) + r0 / 16) * 8 + t) * 32 + lane] =
             make_float4(ut[j][0], ut[j][1], ut[j][2], ut[j][3]);
       }
