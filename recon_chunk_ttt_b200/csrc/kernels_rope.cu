@@ -35,7 +35,8 @@ struct RopeParams {
   int64_t n;
   int pairs;  // rotated pairs (R / 2)
   int per;    // items of a head: what a thread takes at a time
-  uint32_t per_inv, row_inv, pair_inv;  // 2^32 / x + 1 of per, heads * per, pairs: for e / x
+  // 2^32 / x + 1 of per, heads * per (0 where a block has one token), pairs: for e / x
+  uint32_t per_inv, row_inv, pair_inv;
   float sign;
 };
 
@@ -232,14 +233,14 @@ cudaError_t launch(RopeParams& p, bool pairs, cudaStream_t st) {
   p.per = pairs ? D / N : (D - p.pairs) / unit;
   const int64_t row = (int64_t)(p.heads[0] + p.heads[1]) * p.per;
   p.per_inv = (uint32_t)((1ull << 32) / p.per + 1);
-  p.row_inv = (uint32_t)((1ull << 32) / row + 1);
   p.pair_inv = (uint32_t)((1ull << 32) / p.pairs + 1);
-  // tokens of a block: four items a thread, but blocks for the whole GPU first.  (One
-  // token may have more items than 2^16, where e / row = 0 all the same and e / per stays
-  // exact: per <= 192 and e < 2^21 keep the product's error below 1 / per.)
+  // tokens of a block: four items a thread, but blocks for the whole GPU first
   int64_t tok = 4 * kThreads / row;
   if (tok > p.n / (148 * 4)) tok = p.n / (148 * 4);
   tok = tok < 1 ? 1 : tok > kTok ? kTok : tok;
+  // Exact: several tokens have e < 2^12 items.  One token may have up to 2^21: e / row is 0,
+  // and per <= 192 keeps the error of e / per below 1 / per.
+  p.row_inv = tok == 1 ? 0 : (uint32_t)((1ull << 32) / row + 1);
   const unsigned grid = (unsigned)((p.n + tok - 1) / tok);
   TraceScope ts("rope", st);
   if (pairs)

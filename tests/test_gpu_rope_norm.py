@@ -111,6 +111,18 @@ def test_rope_sizes_strides_in_place(n, layout):
     assert ((again - Kd.double()).abs() <= 1.5 * 2.0 ** -8 * Kd.double().abs().amax(1, True)).all()
 
 
+@pytest.mark.parametrize("hq,hk,layout", [(4096, 4096, PAIRS), (4096, 4, HALF)])
+def test_rope_as_many_heads_as_there_may_be(hq, hk, layout):
+    """A token whose heads are more than 2^16 vectors; every head as the first."""
+    d, rot = 128, (32, 48, 48)
+    cfg = R.make_rope_config(d, rot, layout=layout)
+    x = torch.randn(2, d, device="cuda", dtype=torch.bfloat16)
+    pos = _positions(2, 5)
+    want, _ = R.ttt_rope(cfg, x, None, pos)
+    Q, K = R.ttt_rope(cfg, x.repeat(1, hq), x.repeat(1, hk), pos)
+    assert torch.equal(Q, want.repeat(1, hq)) and torch.equal(K, want.repeat(1, hk))
+
+
 def test_rope_values_pass_and_positions_that_are_no_numbers():
     """NaN and infinity in the part that is not rotated stay where they are; a
     position of NaN reaches its own token's axis only."""
