@@ -561,6 +561,9 @@ __global__ void __launch_bounds__(SK<D, KS, RG, ST, GRAD>::THREADS, ST == 1 ? 2 
       }
       arrive(1);
       if (!wait(1, c)) break;
+      // o's parts were written before r's; read before arrive(2), behind which the next
+      // step's may come
+      add_parts(ot, x_part + L::X_PART);
       float us[2][NT][4] = {};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -629,7 +632,6 @@ __global__ void __launch_bounds__(SK<D, KS, RG, ST, GRAD>::THREADS, ST == 1 ? 2 
     }
     arrive(2);
     // o = scale gamma o + u P^T
-    add_parts(ot, x_part + L::X_PART);  // written before r's parts were
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const float2 ga = *reinterpret_cast<const float2*>(gates + tile(j) * 8 + col);
