@@ -5,7 +5,7 @@ Like the layer's binding this marshals arguments and allocates outputs that
 are not given; types, shapes, strides and devices are checked here because the
 C function sees plain pointers (TTTError with TTT_ERR_INVALID_ARG), the rest in
 the library.  Work goes to the tensors' device, on `stream` or that device's
-current stream.
+current stream; what a call allocates belongs to that stream.
 """
 from __future__ import annotations
 
@@ -127,17 +127,25 @@ def _space(what, dev, t, nbytes):
     return t, t.data_ptr(), t.numel() * t.element_size()
 
 
-def _run(what, dev, fn, args, stream):
-    """The library's call with the tensors' device current, on `stream` or that
-    device's current stream."""
+def _on(what, t, stream):
+    """`stream` (a torch stream or a handle) as the current one.  What the call then
+    allocates belongs to that stream: its memory is not another stream's again while
+    the call's work may still use it."""
+    dev = _device(what, t)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else \
+            torch.cuda.default_stream(dev)
+    _want(stream.device.index == dev, what, f"stream is on {stream.device}, not on GPU {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _run(what, dev, fn, args):
+    """The library's call with the tensors' device current, on that device's
+    current stream."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _run(what, dev, fn, args, stream)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    status = fn(*args, stream)
+            return _run(what, dev, fn, args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status != B.TTT_OK:
         raise B.TTTError(status, what)
 
@@ -167,6 +175,13 @@ def alloc_delta_workspace(cfg: ttt_delta_config, n: int, seqs: int = 1, backward
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device or "cuda")
 
 
+def _sequences(what, offsets):
+    if offsets is None:
+        return 1
+    _want(offsets.dim() == 1 and offsets.shape[0] > 0, what, "offsets must be [seqs + 1]")
+    return offsets.shape[0] - 1
+
+
 def _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs):
     """(device, tokens of the call as bytes, their number, token type)."""
     dev, tdt = _device(what, Q), _token(cfg.precision)
@@ -186,7 +201,10 @@ def ttt_delta_chunk(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S=None, off
     """The gated delta rule over packed sequences (offsets int64 [seqs + 1] on
     the device, or one sequence); returns (O, S_out).  S_out may be S."""
     what = "ttt_delta_chunk"
-    seqs = 1 if offsets is None else offsets.shape[0] - 1
+    if stream is not None:
+        with _on(what, Q, stream):
+            return ttt_delta_chunk(cfg, Q, K, V, log_decay, beta, S, offsets, S_out, O, workspace)
+    seqs = _sequences(what, offsets)
     dev, t, n, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs)
     shape = (seqs, cfg.heads, cfg.d, cfg.d)
     pS = _maybe(what, dev, "S", S, _F32, shape)
@@ -194,7 +212,7 @@ def ttt_delta_chunk(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S=None, off
     O, pO = _out(what, dev, "O", O, tdt, (n, cfg.heads * cfg.d), V)
     workspace, pW, nbytes = _space(what, dev, workspace,
                                    lambda: ttt_delta_workspace_bytes(cfg, n, seqs))
-    _run(what, dev, _lib().ttt_delta_chunk, (ctypes.byref(cfg), t, pS, pSo, pO, pW, nbytes), stream)
+    _run(what, dev, _lib().ttt_delta_chunk, (ctypes.byref(cfg), t, pS, pSo, pO, pW, nbytes))
     return O, S_out
 
 
@@ -204,6 +222,9 @@ def ttt_delta_step(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S, slots=Non
     (slots: int32 [n], -1 for padding; without them request i has state i).
     The new states go to S_out, or into S where that is not given; returns O."""
     what = "ttt_delta_step"
+    if stream is not None:
+        with _on(what, Q, stream):
+            return ttt_delta_step(cfg, Q, K, V, log_decay, beta, S, slots, S_out, O)
     dev, t, n, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, None, Q.shape[0])
     _want(isinstance(S, torch.Tensor) and S.dim() == 4, what, "S must be [pool, heads, d, d]")
     pool = S.shape[0]
@@ -212,7 +233,7 @@ def ttt_delta_step(cfg: ttt_delta_config, Q, K, V, log_decay, beta, S, slots=Non
     pSo = pS if S_out is None else _check(what, dev, "S_out", S_out, _F32, shape)
     pI = _maybe(what, dev, "slots", slots, torch.int32, (n,))
     O, pO = _out(what, dev, "O", O, tdt, (n, cfg.heads * cfg.d), V)
-    _run(what, dev, _lib().ttt_delta_step, (ctypes.byref(cfg), t, pI, pool, pS, pSo, pO), stream)
+    _run(what, dev, _lib().ttt_delta_step, (ctypes.byref(cfg), t, pI, pool, pS, pSo, pO))
     return O
 
 
@@ -222,7 +243,11 @@ def ttt_delta_backward(cfg: ttt_delta_config, Q, K, V, log_decay, beta, dO, S=No
     """Gradients of sum(dO * O) + sum(dS_out * S_out) of ttt_delta_chunk:
     (dQ, dK, dV, dlog_decay, dbeta, dS).  dS may be dS_out."""
     what = "ttt_delta_backward"
-    seqs = 1 if offsets is None else offsets.shape[0] - 1
+    if stream is not None:
+        with _on(what, Q, stream):
+            return ttt_delta_backward(cfg, Q, K, V, log_decay, beta, dO, S, offsets, dS_out, dQ, dK, dV,
+                                      dlog_decay, dbeta, dS, workspace)
+    seqs = _sequences(what, offsets)
     dev, t, n, tdt = _delta_tokens(what, cfg, Q, K, V, log_decay, beta, offsets, seqs)
     qk, hv, per = (n, cfg.qk_heads * cfg.d), (n, cfg.heads * cfg.d), (n, cfg.heads)
     shape = (seqs, cfg.heads, cfg.d, cfg.d)
@@ -238,7 +263,7 @@ def ttt_delta_backward(cfg: ttt_delta_config, Q, K, V, log_decay, beta, dO, S=No
     workspace, pW, nbytes = _space(what, dev, workspace,
                                    lambda: ttt_delta_workspace_bytes(cfg, n, seqs, True))
     _run(what, dev, _lib().ttt_delta_backward,
-         (ctypes.byref(cfg), t, pS, pG, pE, p1, p2, p3, p4, p5, p6, pW, nbytes), stream)
+         (ctypes.byref(cfg), t, pS, pG, pE, p1, p2, p3, p4, p5, p6, pW, nbytes))
     return dQ, dK, dV, dlog_decay, dbeta, dS
 
 
@@ -258,6 +283,9 @@ def ttt_rope(cfg: ttt_rope_config, Q, K, positions, Q_out=None, K_out=None, inve
     positions float [n, 3]; returns (Q_out, K_out).  Q_out may be Q and K_out
     K.  inverse=True turns back: the gradient."""
     what = "ttt_rope"
+    if stream is not None:
+        with _on(what, Q, stream):
+            return ttt_rope(cfg, Q, K, positions, Q_out, K_out, inverse)
     dev, tdt = _device(what, Q), _token(cfg.precision)
     n = Q.shape[0]
 
@@ -278,7 +306,7 @@ def ttt_rope(cfg: ttt_rope_config, Q, K, positions, Q_out=None, K_out=None, inve
     hk, pK, lk, K_out, pKo, lko = side("K", K, K_out)
     pP = _check(what, dev, "positions", positions, _F32, (n, 3))
     _run(what, dev, _lib().ttt_rope, (ctypes.byref(cfg), pQ, lq, hq, pK, lk, hk, pP, n, pQo, lqo, pKo,
-                                      lko, 1 if inverse else 0), stream)
+                                      lko, 1 if inverse else 0))
     return Q_out, K_out
 
 
@@ -297,6 +325,9 @@ def ttt_layer_norm(cfg: ttt_norm_config, X, weight=None, bias=None, Y=None, stat
     """Layer norm of the rows of X [rows, dim]; returns (Y, stats), stats
     float [rows, 2] holding each row's mean and 1/sqrt(var + eps)."""
     what = "ttt_layer_norm"
+    if stream is not None:
+        with _on(what, X, stream):
+            return ttt_layer_norm(cfg, X, weight, bias, Y, stats)
     dev, tdt = _device(what, X), _token(cfg.precision)
     dim = cfg.dim
     rows = X.shape[0]
@@ -307,8 +338,7 @@ def ttt_layer_norm(cfg: ttt_norm_config, X, weight=None, bias=None, Y=None, stat
     if stats is None:
         stats = torch.empty((rows, 2), dtype=_F32, device=X.device)
     ps = _check(what, dev, "stats", stats, _F32, (rows, 2))
-    _run(what, dev, _lib().ttt_layer_norm, (ctypes.byref(cfg), pX, _ld(X), rows, pw, pb, pY, ps),
-         stream)
+    _run(what, dev, _lib().ttt_layer_norm, (ctypes.byref(cfg), pX, _ld(X), rows, pw, pb, pY, ps))
     return Y, stats
 
 
@@ -316,6 +346,9 @@ def ttt_layer_norm_backward(cfg: ttt_norm_config, X, dY, stats, weight=None, dX=
                             dweight=None, dbias=None, workspace=None, stream=None):
     """(dX, dweight, dbias) from the forward call's X and stats."""
     what = "ttt_layer_norm_backward"
+    if stream is not None:
+        with _on(what, X, stream):
+            return ttt_layer_norm_backward(cfg, X, dY, stats, weight, dX, dweight, dbias, workspace)
     dev, tdt = _device(what, X), _token(cfg.precision)
     dim = cfg.dim
     rows = X.shape[0]
@@ -328,5 +361,5 @@ def ttt_layer_norm_backward(cfg: ttt_norm_config, X, dY, stats, weight=None, dX=
     dbias, p3 = _out(what, dev, "dbias", dbias, _F32, (dim,), dweight)
     workspace, pW, nbytes = _space(what, dev, workspace, lambda: ttt_norm_workspace_bytes(cfg, rows))
     _run(what, dev, _lib().ttt_layer_norm_backward,
-         (ctypes.byref(cfg), pX, _ld(X), pY, _ld(dY), rows, pw, ps, p1, p2, p3, pW, nbytes), stream)
+         (ctypes.byref(cfg), pX, _ld(X), pY, _ld(dY), rows, pw, ps, p1, p2, p3, pW, nbytes))
     return dX, dweight, dbias

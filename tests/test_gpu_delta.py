@@ -420,3 +420,38 @@ def test_binding_refusals():
     with pytest.raises(R.TTTError):
         R.ttt_delta_step(cfg, **x, S=S)  # 100 requests, one state
     assert np.isfinite(R.ttt_delta_chunk(cfg, **x, S=S)[0].float().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_stream_argument(handle):
+    """A call on a stream that is behind the current one: the workspace and the
+    outputs it allocates are not the current stream's to use."""
+    H, d, n = 4, 128, 700
+    x, S, dO, dSo = _inputs(43, n, H, H, d, BF)
+    cfg = R.make_delta_config(H, d)
+    want = R.ttt_delta_chunk(cfg, **x, S=S)
+    grad = R.ttt_delta_backward(cfg, **x, dO=dO, S=S, dS_out=dSo)
+    sizes = [R.ttt_delta_workspace_bytes(cfg, n, backward=b) for b in (False, True)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    s = side.cuda_stream if handle else side
+    got = R.ttt_delta_chunk(cfg, **x, S=S, stream=s)
+    ggot = R.ttt_delta_backward(cfg, **x, dO=dO, S=S, dS_out=dSo, stream=s)
+    for b in sizes:
+        for _ in range(4):
+            torch.empty(b, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    for a, b in zip(got + ggot, want + grad):
+        assert torch.equal(a, b)
+    assert torch.equal(R.ttt_delta_chunk(cfg, **x, S=S, stream=0)[0], want[0])
+
+
+def test_offsets_without_an_entry():
+    x, _, _, _ = _inputs(1, 20, 1, 1, 64, BF)
+    cfg = R.make_delta_config(1, 64)
+    for bad in (torch.empty(0, dtype=torch.int64, device="cuda"),
+                torch.tensor([[0, 20]], device="cuda")):
+        with pytest.raises(R.TTTError):
+            R.ttt_delta_chunk(cfg, **x, offsets=bad)
