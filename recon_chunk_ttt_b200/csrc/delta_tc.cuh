@@ -40,6 +40,7 @@ __device__ __forceinline__ SeqRange seq_range(const int64_t* offsets, int64_t n,
 struct ChunkRange {
   int64_t t0;
   int len;
+  int64_t sequence;  // tokens of the sequence it is of
 };
 __device__ __forceinline__ ChunkRange chunk_range(const int64_t* offsets, int64_t n, int64_t seqs,
                                                   int64_t slot) {
@@ -54,6 +55,7 @@ __device__ __forceinline__ ChunkRange chunk_range(const int64_t* offsets, int64_
   const SeqRange s = seq_range(offsets, n, lo);
   ChunkRange c;
   c.t0 = s.t0 + (slot - s.slot) * kC;
+  c.sequence = s.t1 - s.t0;
   c.len = slot < s.slot || c.t0 >= s.t1 ? 0 : s.t1 - c.t0 < kC ? (int)(s.t1 - c.t0) : kC;
   return c;
 }

@@ -60,6 +60,7 @@ struct TokArgs {
   int H, Hk;
   float scale;
   int* err;
+  int64_t longest;  // sequences of more tokens are left alone
 };
 
 // grid (d / rows of a block, H, sequences or requests), 128 threads.  A row of
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
   } else {
     sq = sequence(a.offsets, a.n, i, kKeep, a.err);
+    if (sq.t1 - sq.t0 > a.longest) return;
   }
 
   float s[kRows][4 * NC];
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(256)
 
 TokArgs pack(const DeltaArgs& a, int* err) {
   return {a.Q, a.K, a.V, a.g, a.b, a.ldq, a.ldk, a.ldv, a.n, a.offsets, nullptr, 0,
-          a.H, a.Hk, a.scale, err};
+          a.H, a.Hk, a.scale, err, INT64_MAX};
 }
 
 // One block's rows of S.
@@ -400,11 +402,13 @@ cudaError_t launch_backward(const DeltaArgs& a, const TokArgs& k, const void* dO
 
 }  // namespace
 
-cudaError_t delta_tokens(const DeltaArgs& a, const float* S_in, float* S_out, void* O,
-                         cudaStream_t st) {
+cudaError_t delta_tokens(const DeltaArgs& a, int64_t longest, const float* S_in, float* S_out,
+                         void* O, cudaStream_t st) {
   int* err = device_error_ptr();
   if (err == nullptr) return cudaErrorInvalidDevice;
-  return by_type<false, false>(a, pack(a, err), a.seqs, S_in, S_out, O, nullptr, st);
+  TokArgs k = pack(a, err);
+  k.longest = longest;
+  return by_type<false, false>(a, k, a.seqs, S_in, S_out, O, nullptr, st);
 }
 
 cudaError_t delta_step(const DeltaArgs& a, const int32_t* slots, int64_t pool, const float* S,

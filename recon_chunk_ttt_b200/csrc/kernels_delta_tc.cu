@@ -44,6 +44,7 @@ struct ChunkArgs {
   float scale;
   uint8_t* blocks;
   int64_t slots;
+  int64_t brief;   // chunks of sequences of at most so many tokens are left out
   int32_t* order;  // written where it is not nullptr
 };
 
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kChunkThreads)
     return;
   }
   const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
-  if (c.len == 0) return;
+  if (c.len == 0 || c.sequence <= a.brief) return;
 
   for (int e = tid; e < kC * D / 8; e += kChunkThreads) {
     const int row = e / (D / 8), col = e % (D / 8) * 8;
@@ -293,6 +294,7 @@ struct StateArgs {
   const float* S_in;
   float* S_out;
   __nv_bfloat16* O;
+  int64_t brief;   // sequences of at most so many tokens are left alone
   DeltaKept kept;  // for the gradient
   int* err;
 };
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(SK<D, KS, RG, ST, GRAD>::THREADS, ST == 1 ? 2 
   const int64_t seq = a.order != nullptr ? a.order[blockIdx.z] : blockIdx.z;
   const SeqRange sr = seq_range(a.offsets, a.n, seq);
   const int64_t len = sr.t1 - sr.t0;
+  if (!GRAD && len <= a.brief) return;
   const int64_t nc = (len + kC - 1) / kC;
   if (threadIdx.x == 0) {
     if (sr.bad) atomicExch(a.err, (int)kErrOffsets);
@@ -785,7 +788,7 @@ cudaError_t launch_chunks(const DeltaArgs& a, uint8_t* blocks, cudaStream_t st) 
   if (e != cudaSuccess) return e;
   const ChunkArgs k = {static_cast<const __nv_bfloat16*>(a.Q), static_cast<const __nv_bfloat16*>(a.K),
                        a.g, a.b, a.ldq, a.ldk, a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, blocks,
-                       chunk_slots(a), order_of(a, blocks)};
+                       chunk_slots(a), a.brief, order_of(a, blocks)};
   TraceScope ts("delta_chunk", st);
   delta_chunk_kernel<D, GRAD>
       <<<dim3((unsigned)(chunk_slots(a) + (k.order != nullptr)), (unsigned)a.H), kChunkThreads, smem,
@@ -809,9 +812,12 @@ cudaError_t launch_state(const DeltaArgs& a, const float* S_in, float* S_out, vo
   const cudaError_t e = ensure_smem_attr(delta_state_kernel<D, KS, RG, ST, GRAD>, L::SMEM);
   if (e != cudaSuccess) return e;
   const StateArgs k = {a.n,  a.offsets, a.H,   a.Hk, a.scale, blocks, order_of(a, blocks), S_in, S_out,
-                       static_cast<__nv_bfloat16*>(O), kept ? *kept : DeltaKept{}, err};
+                       static_cast<__nv_bfloat16*>(O), a.brief, kept ? *kept : DeltaKept{}, err};
+  // no more sequences than this have more than a.brief tokens, and they come first
+  const int64_t most = k.order == nullptr || a.brief < 0 ? a.seqs : a.n / (a.brief + 1);
+  const unsigned seqs = (unsigned)(most < a.seqs ? most : a.seqs);
   TraceScope ts(GRAD ? "delta_state_kept" : "delta_state", st);
-  delta_state_kernel<D, KS, RG, ST, GRAD><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
+  delta_state_kernel<D, KS, RG, ST, GRAD><<<dim3(D / (16 * RG), (unsigned)a.H, seqs),
                                         L::THREADS, L::SMEM, st>>>(mQ, mK, mV, mG, k);
   return cudaGetLastError();
 }

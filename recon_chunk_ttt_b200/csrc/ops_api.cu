@@ -54,6 +54,7 @@ ttt_status delta_args(const ttt_delta_config* c, const ttt_delta_tokens* t, Delt
   a->n = t->n;
   a->offsets = t->offsets;
   a->seqs = t->seqs;
+  a->brief = -1;
   if (t->n > 0) {
     if (!t->Q || !t->K || !t->V || !t->log_decay || !t->beta) return TTT_ERR_INVALID_ARG;
     const int64_t qk = (int64_t)a->Hk * a->d, v = (int64_t)a->H * a->d;
@@ -75,13 +76,19 @@ ttt_status check_sequences(const DeltaArgs& a) {
   return aligned(a.offsets, 8) ? TTT_OK : TTT_ERR_ALIGNMENT;
 }
 
-// Chunks of 64 tokens on the tensor cores start two kernels and work on whole
-// chunks; token after token takes about 0.6 us a token.  For one
-// sequence the two meet at 20 to 24 tokens (16 heads of 128: 14.4 us against 11.1 us
-// for 16 tokens, 15.8 us for 24); for 17 sequences of 4 tokens each it is 54 us against
-// 13 us.  The lengths are known on the device only: many sequences of 4 tokens
-// on average go token after token.
-bool by_token(const DeltaArgs& a) { return !a.bf16 || a.n <= 16 || a.n <= 4 * a.seqs; }
+// Which sequences go in chunks of 64 tokens on the tensor cores (two kernels, and a whole
+// chunk's work for any part of one) and which token after token (about 0.6 us a token).
+//  - Alone, the two meet at 20 to 24 tokens (16 heads of 128: 14.4 us against 11.1 us for
+//    16 tokens, 15.8 us for 24): calls of up to 16 tokens go by token.
+//  - Sequences shorter than a chunk on average are mixed, single tokens beside long ones:
+//    those of up to 16 tokens go by token, then the others in chunks (256 single tokens
+//    and four sequences of 1,000: 254 us; all in chunks 651 us).
+//  - Where the average is 4 tokens at most and the call small, all go by token: the longest
+//    sequence costs 77 us then, and 17 sequences of 4 tokens take 18 us against 29 us mixed.
+constexpr int64_t kBrief = 16, kMixed = 64, kSmall = 128;
+bool by_token(const DeltaArgs& a) {
+  return !a.bf16 || a.n <= kBrief || (a.n <= 4 * a.seqs && a.n <= kSmall);
+}
 
 size_t delta_bytes(const DeltaArgs& a, bool backward) {
   if (backward) return a.bf16 ? ttt::delta_grad_bytes(a) : ttt::delta_tokens_backward_bytes(a);
@@ -118,8 +125,13 @@ ttt_status ttt_delta_chunk(const ttt_delta_config* cfg, const ttt_delta_tokens* 
   const size_t need = delta_bytes(a, false);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
   if (a.seqs == 0) return TTT_OK;
-  return cuda_status(by_token(a) ? ttt::delta_tokens(a, S_in, S_out, O, cs(stream))
-                                 : ttt::delta_tc(a, S_in, S_out, O, workspace, cs(stream)));
+  if (by_token(a)) return cuda_status(ttt::delta_tokens(a, INT64_MAX, S_in, S_out, O, cs(stream)));
+  if (a.offsets != nullptr && a.n <= kMixed * a.seqs) {
+    a.brief = kBrief;
+    const cudaError_t e = ttt::delta_tokens(a, a.brief, S_in, S_out, O, cs(stream));
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return cuda_status(ttt::delta_tc(a, S_in, S_out, O, workspace, cs(stream)));
 }
 
 ttt_status ttt_delta_step(const ttt_delta_config* cfg, const ttt_delta_tokens* tok,

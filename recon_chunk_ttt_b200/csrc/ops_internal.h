@@ -18,11 +18,13 @@ struct DeltaArgs {
   int64_t n;
   const int64_t* offsets;  // [seqs + 1] or nullptr: one sequence of n tokens
   int64_t seqs;
+  int64_t brief;  // forward: sequences of at most so many tokens are not taken in chunks
 };
 
 // ---- CUDA cores, token by token (kernels_delta.cu) ---------------------------
-cudaError_t delta_tokens(const DeltaArgs& a, const float* S_in, float* S_out, void* O,
-                         cudaStream_t st);
+// The sequences of at most `longest` tokens.
+cudaError_t delta_tokens(const DeltaArgs& a, int64_t longest, const float* S_in, float* S_out,
+                         void* O, cudaStream_t st);
 cudaError_t delta_step(const DeltaArgs& a, const int32_t* slots, int64_t pool, const float* S,
                        float* S_out, void* O, cudaStream_t st);
 size_t delta_tokens_backward_bytes(const DeltaArgs& a);
@@ -35,6 +37,7 @@ cudaError_t delta_share(const DeltaArgs& a, const float* part_q, const float* pa
                         void* dK, cudaStream_t st);
 
 // ---- tensor cores, chunks of 64 tokens (kernels_delta_tc.cu): bf16 tokens ---------
+// The sequences of more than a.brief tokens.
 size_t delta_tc_bytes(const DeltaArgs& a);
 cudaError_t delta_tc(const DeltaArgs& a, const float* S_in, float* S_out, void* O, void* ws,
                      cudaStream_t st);

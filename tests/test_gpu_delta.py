@@ -422,6 +422,23 @@ def test_binding_refusals():
     assert np.isfinite(R.ttt_delta_chunk(cfg, **x, S=S)[0].float().cpu().numpy()).all()
 
 
+@pytest.mark.parametrize("lens,H,Hk,d", [
+    ([1] * 30 + [300] + [0] * 5 + [17, 16, 64] + [4] * 25, 4, 2, 128),  # ranked by length
+    ([1] * 300 + [100] + [0] * 220 + [40], 2, 2, 64),                   # too many to be ranked
+    ([9] * 30, 2, 1, 256),                                              # short ones alone
+])
+def test_short_and_long_together(lens, H, Hk, d):
+    """Single tokens and long sequences in one call, states in place."""
+    n = sum(lens)
+    x, S, _, _ = _inputs(n, n, H, Hk, d, BF, len(lens))
+    cfg = R.make_delta_config(H, d, qk_heads=Hk)
+    Or, Sr = _reference(x, S, lens, 0, H, Hk, d, d ** -0.5)
+    O, So = R.ttt_delta_chunk(cfg, **x, S=S, offsets=_offsets(lens, 0), S_out=S)
+    assert So is S and R.ttt_check_device_error() == 0
+    _close(O.view(-1, H, d), Or, TOL_O[BF], "O", 1)
+    _close(S, Sr, TOL_S[BF], "S", 1)
+
+
 @pytest.mark.parametrize("handle", [False, True])
 def test_stream_argument(handle):
     """A call on a stream that is behind the current one: the workspace and the
