@@ -710,6 +710,18 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     re[y] = expf((Gh[kC - 1] - Gh[i]) + (Gl[kC - 1] - Gl[i]));
   }
   const bool with_e = half == 1;
+  // this warp's rows of U in two parts, or of dO and dV: they stay in registers
+  uint32_t ax[D / 16][4], ay[D / 16][4];
+#pragma unroll
+  for (int e = 0; e < D / 16; ++e) {
+    if (with_e) {
+      ldsm4_t(sU + blk_a(e * 16, m0), ax[e]);
+      ldsm4_t(sU + L::TOK + blk_a(e * 16, m0), ay[e]);
+    } else {
+      ldsm4(sG + sw(kC, m0 + kn_r, e * 16 + kn_c), ax[e]);
+      ldsm4_t(sV + blk_a(e * 16, m0), ay[e]);
+    }
+  }
   for (int s = 0; s < L::NS; ++s) {  // 16 columns of dQ, dK at a time
     ok = mbar_wait(&bar[1 + s % 2], (uint32_t)(s / 2 & 1), abort_flag, a.err, kErrWaitFull) && ok;
     const uint32_t sS = smem_u32(pS) + s % 2 * L::STRIP, sE = sS + L::ST, sQ = sS + 2 * L::ST,
@@ -718,30 +730,19 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     // acc: scale gamma dO S, or rest U E;  ve: dV S
     float acc[2][4] = {}, ve[2][4] = {};
     {
-      // the next 16 rows' operands are loaded meanwhile
+      // 16 rows x 16 columns of a strip [row / 8][2 column blocks]: stored [k][n]
       const uint32_t from = (with_e ? sE : sS) +
                             (uint32_t)((lane / 8 % 2 * 2 + lane / 16) * 128 + lane % 8 * 16);
-      uint32_t x[2][4], y[2][4], b[2][4];
-      const auto load = [&](int k, int f) {
-        if (with_e) {
-          ldsm4_t(sU + blk_a(k, m0), x[f]);
-          ldsm4_t(sU + L::TOK + blk_a(k, m0), y[f]);
-        } else {
-          ldsm4(sG + sw(kC, m0 + kn_r, k + kn_c), x[f]);
-          ldsm4_t(sV + blk_a(k, m0), y[f]);
-        }
-        // 16 rows x 16 columns of a strip [row / 8][2 column blocks]: stored [k][n]
-        ldsm4_t(from + (uint32_t)(k / 8 * 256), b[f]);
-      };
-      load(0, 0);
+      uint32_t b[2][4];
+      ldsm4_t(from, b[0]);
 #pragma unroll
       for (int e = 0; e < D / 16; ++e) {
         const int f = e % 2;
-        if (e + 1 < D / 16) load((e + 1) * 16, 1 - f);
-        mma(acc[0], x[f], b[f][0], b[f][1]);
-        mma(acc[1], x[f], b[f][2], b[f][3]);
-        mma(ve[0], y[f], b[f][0], b[f][1]);
-        mma(ve[1], y[f], b[f][2], b[f][3]);
+        if (e + 1 < D / 16) ldsm4_t(from + (uint32_t)((e + 1) * 512), b[1 - f]);
+        mma(acc[0], ax[e], b[f][0], b[f][1]);
+        mma(acc[1], ax[e], b[f][2], b[f][3]);
+        mma(ve[0], ay[e], b[f][0], b[f][1]);
+        mma(ve[1], ay[e], b[f][2], b[f][3]);
       }
     }
 #pragma unroll
