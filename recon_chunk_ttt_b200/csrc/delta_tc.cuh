@@ -153,6 +153,10 @@ __host__ __device__ constexpr int chunk_bytes(int p_parts) { return (3 + p_parts
 __device__ __forceinline__ uint32_t sw32(int row, int unit) {
   return (uint32_t)(row * 32 + ((unit ^ ((row >> 2) & 1)) << 4));
 }
+// Where row 0 of a triangle's strip k would lie (it begins with row 16 k).
+__device__ __forceinline__ uint32_t tri_strip(int k) {
+  return (uint32_t)(32 * (64 * k - 8 * k * (k - 1)) - 512 * k);
+}
 // (row, col) of a triangle, col / 16 <= row / 16
 __device__ __forceinline__ uint32_t tri(int row, int col) {
   const int k = col >> 4;

@@ -554,12 +554,18 @@ struct GK {
   static constexpr int QS = kC * 32;            // 16 columns of Q or K
   static constexpr int STRIP = 2 * ST + 2 * QS;
   static constexpr int NS = D / 16;
-  static constexpr int OFF_S = 4 * TOK;
-  static constexpr int OFF_A = OFF_S + 2 * STRIP;       // A in two parts, M: triangles
-  static constexpr int OFF_X = OFF_A + 3 * kTri;        // dV S handed over, two deep
+  // strips in flight: two from the start, then as many more as dO, U, dV leave room for
+  // once they are in registers, filled from the back
+  static constexpr int RING = 2 + (4 * TOK / STRIP < NS - 2 ? 4 * TOK / STRIP : NS - 2);
+  static constexpr int OFF_S = 4 * TOK - (RING - 2) * STRIP;
+  static constexpr int OFF_A = 4 * TOK + 2 * STRIP;     // A in two parts, M: triangles
+  static constexpr int OFF_X = OFF_A + 3 * kTri;        // what is handed over, two deep
   static constexpr int X = 4 * 2 * 32 * 16;
   static constexpr int OFF_BAR = OFF_X + 2 * X;
-  static constexpr int SMEM = OFF_BAR + 64 + 1024;
+  static constexpr int SMEM = OFF_BAR + (1 + 2 * RING) * 8 + 8 + 1024;
+  static constexpr uint8_t* place(uint8_t* smem, int s) {  // of strip s
+    return smem + OFF_S + (s % RING + RING - 2) % RING * STRIP;
+  }
   static_assert(SMEM <= (D == 256 ? 227 : 113) * 1024, "shared memory");
 };
 
@@ -587,10 +593,11 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   __shared__ float Gh[kC], Gl[kC];  // running sums of the log decays in two parts
-  uint8_t *pG = smem, *pU = smem + L::TOK, *pV = smem + 3 * L::TOK, *pS = smem + L::OFF_S,
+  uint8_t *pG = smem, *pU = smem + L::TOK, *pV = smem + 3 * L::TOK,
           *pA = smem + L::OFF_A, *pM = pA + 2 * kTri;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);  // tokens, strips
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + 3);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);  // tokens
+  uint64_t *full = bar + 1, *empty = full + L::RING;               // strips
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + L::RING);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t slot = blockIdx.x;
   const int h = blockIdx.y, hk = h / (a.H / a.Hk);
@@ -602,8 +609,8 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
   if (c.len == 0) return;
   const int64_t at = slot * a.H + h;
   const auto load_strip = [&](int s) {
-    uint8_t* to = pS + s % 2 * L::STRIP;
-    uint64_t* b = &bar[1 + s % 2];
+    uint8_t* to = L::place(smem, s);
+    uint64_t* b = &full[s % L::RING];
     mbar_arrive_expect_tx(b, L::STRIP);
     bulk_load(to, a.S0 + at * D * D + s * (D * 16), L::ST, b);
     bulk_load(to + L::ST, a.E + at * D * D + s * (D * 16), L::ST, b);
@@ -611,7 +618,11 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     tma_load_2d(to + 2 * L::ST + L::QS, &mK, b, hk * D + s * 16, (int)c.t0);
   };
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+    mbar_init(bar, 1);
+    for (int i = 0; i < L::RING; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kGW);
+    }
     *abort_flag = 0;
     fence_mbar_init();
     mbar_arrive_expect_tx(&bar[0], 4 * L::TOK);
@@ -722,12 +733,26 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
       ldsm4_t(sV + blk_a(e * 16, m0), ay[e]);
     }
   }
+  float* shares = with_e ? a.pk : a.pq;
+  __nv_bfloat16* grads = with_e ? a.dK : a.dQ;
+  const int64_t out_ld = (int64_t)(shares != nullptr ? a.H : a.Hk) * D,
+                out = (c.t0 + m0 + row) * out_ld + h * D + col;
+  // this lane's addresses in Q's and K's strips; in the triangles, its row of these 16 tokens
+  // (strip kb begins at tri_strip(kb)) and of the tokens from 0 on in their columns
+  const uint32_t strip_row = sw32(kn_r, lane / 16);
+  const uint32_t tri_row = sw32(m0 + kn_r, lane / 16),
+                 tri_col = tri_strip(mb) + sw32(nk_r, lane / 8 % 2);
+  __syncthreads();  // dO, U, dV have been read: strips may lie over them
+  int issued = L::RING;
+  if (tid == 0)
+    for (int s = 2; s < L::RING; ++s) load_strip(s);
   for (int s = 0; s < L::NS; ++s) {  // 16 columns of dQ, dK at a time
-    ok = mbar_wait(&bar[1 + s % 2], (uint32_t)(s / 2 & 1), abort_flag, a.err, kErrWaitFull) && ok;
-    const uint32_t sS = smem_u32(pS) + s % 2 * L::STRIP, sE = sS + L::ST, sQ = sS + 2 * L::ST,
+    ok = mbar_wait(&full[s % L::RING], (uint32_t)(s / L::RING & 1), abort_flag, a.err,
+                   kErrWaitFull) && ok;
+    const uint32_t sS = smem_u32(L::place(smem, s)), sE = sS + L::ST, sQ = sS + 2 * L::ST,
                    sK = sQ + L::QS;
     float4* hand = reinterpret_cast<float4*>(smem + L::OFF_X + s % 2 * L::X) + mb * 64 + lane;
-    // acc: scale gamma dO S, or rest U E;  ve: dV S
+    // acc: scale gamma dO S, or rest U E;  ve: dV S, or rest U E of U's second part
     float acc[2][4] = {}, ve[2][4] = {};
     {
       // 16 rows x 16 columns of a strip [row / 8][2 column blocks]: stored [k][n]
@@ -752,82 +777,97 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
         if (with_e)
           acc[x][y] = re[y / 2] * (acc[x][y] + ve[x][y]);
         else
-          acc[x][y] *= a.scale * gi[y / 2];
-      }
-      if (!with_e)
-        hand[x * 32] = make_float4(-gi[0] * ve[x][0], -gi[0] * ve[x][1], -gi[1] * ve[x][2],
-                                   -gi[1] * ve[x][3]);
-    }
-    // + A K, or + A^T Q + (M + M^T) K
-#pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
-      const int k = kb * 16;
-      if (!with_e && kb > mb) break;
-      uint32_t x[4], bk[4], bq[4];
-      const uint32_t o = sw32(k + kn_r, lane / 16);
-      // rows behind the sequence may hold anything and count as zero
-      const uint32_t k0 = keep_pair(k + col, c.len), k1 = keep_pair(k + 8 + col, c.len);
-      ldsm4_t(sK + o, bk);
-      bk[0] &= k0, bk[1] &= k1, bk[2] &= k0, bk[3] &= k1;
-      if (!with_e) {
-#pragma unroll
-        for (int part = 1; part >= 0; --part) {
-          ldsm4(sA + part * kTri + tri(m0 + kn_r, k + kn_c), x);
-          mma(acc[0], x, bk[0], bk[1]);
-          mma(acc[1], x, bk[2], bk[3]);
-        }
-        continue;
-      }
-      if (kb <= mb) {
-        ldsm4(sM + tri(m0 + kn_r, k + kn_c), x);
-        mma(acc[0], x, bk[0], bk[1]);
-        mma(acc[1], x, bk[2], bk[3]);
-      }
-      if (kb >= mb) {  // transposes: their rows are the columns
-        ldsm4_t(sM + tri(k + nk_r, m0 + nk_c), x);
-        mma(acc[0], x, bk[0], bk[1]);
-        mma(acc[1], x, bk[2], bk[3]);
-        ldsm4_t(sQ + o, bq);
-        bq[0] &= k0, bq[1] &= k1, bq[2] &= k0, bq[3] &= k1;
-#pragma unroll
-        for (int part = 1; part >= 0; --part) {
-          ldsm4_t(sA + part * kTri + tri(k + nk_r, m0 + nk_c), x);
-          mma(acc[0], x, bq[0], bq[1]);
-          mma(acc[1], x, bq[2], bq[3]);
-        }
+          acc[x][y] *= a.scale * gi[y / 2], ve[x][y] *= -gi[y / 2];
       }
     }
-    __syncthreads();  // the strip has been read, dV S is there
-    if (tid == 0 && s + 2 < L::NS) load_strip(s + 2);
+    // + A K and A^T Q (for dK), or + (M + M^T) K
+    const auto triangles = [&](auto tail) {
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        uint32_t x[4], bk[4], bq[4];
+        ldsm4_t(sK + strip_row + kb * 512, bk);
+        const uint32_t k0 = decltype(tail)::value ? keep_pair(kb * 16 + col, c.len) : 0xffffffffu,
+                       k1 = decltype(tail)::value ? keep_pair(kb * 16 + 8 + col, c.len) : 0xffffffffu;
+        if (decltype(tail)::value) bk[0] &= k0, bk[1] &= k1, bk[2] &= k0, bk[3] &= k1;
+        if (!with_e) {
+          if (kb <= mb)
+#pragma unroll
+            for (int part = 1; part >= 0; --part) {
+              ldsm4(sA + part * kTri + tri_row + tri_strip(kb), x);
+              mma(acc[0], x, bk[0], bk[1]);
+              mma(acc[1], x, bk[2], bk[3]);
+            }
+          if (kb >= mb) {  // transposes: their rows are the columns
+            ldsm4_t(sQ + strip_row + kb * 512, bq);
+            if (decltype(tail)::value) bq[0] &= k0, bq[1] &= k1, bq[2] &= k0, bq[3] &= k1;
+#pragma unroll
+            for (int part = 1; part >= 0; --part) {
+              ldsm4_t(sA + part * kTri + tri_col + kb * 512, x);
+              mma(ve[0], x, bq[0], bq[1]);
+              mma(ve[1], x, bq[2], bq[3]);
+            }
+          }
+        } else {
+          if (kb <= mb) {
+            ldsm4(sM + tri_row + tri_strip(kb), x);
+            mma(acc[0], x, bk[0], bk[1]);
+            mma(acc[1], x, bk[2], bk[3]);
+          }
+          if (kb >= mb) {
+            ldsm4_t(sM + tri_col + kb * 512, x);
+            mma(acc[0], x, bk[0], bk[1]);
+            mma(acc[1], x, bk[2], bk[3]);
+          }
+        }
+      }
+    };
+    if (c.len == kC)
+      triangles(std::false_type());
+    else  // rows of Q and K behind the sequence may hold anything and count as zero
+      triangles(std::true_type());
+    if (!with_e)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        hand[x * 32] = make_float4(ve[x][0], ve[x][1], ve[x][2], ve[x][3]);
+    // the two warps of 16 tokens meet; in the buffer before, what this one hands over has
+    // been read when they meet again
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + mb) : "memory");
+    if (L::RING < L::NS) {
+      if (lane == 0) mbar_arrive(&empty[s % L::RING]);
+      // the place of the strip before is free as soon as the slowest warp is through with it
+      if (tid == 0 && ok && *abort_flag == 0 && s > 0 && s - 1 + L::RING < L::NS) {
+        if (mbar_wait(&empty[(s - 1) % L::RING], (uint32_t)((s - 1) / L::RING & 1), abort_flag,
+                      a.err, kErrWaitEmpty)) {
+          load_strip(s - 1 + L::RING);
+          issued = s + L::RING;
+        }
+      }
+      __syncwarp();
+    }
     if (with_e)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float4 v = hand[x * 32];
         acc[x][0] += v.x, acc[x][1] += v.y, acc[x][2] += v.z, acc[x][3] += v.w;
       }
-    float* shares = with_e ? a.pk : a.pq;
-    __nv_bfloat16* grads = with_e ? a.dK : a.dQ;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int y = 0; y < 2; ++y) {
+      if (m0 + row + 8 * y >= c.len) continue;
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int i = m0 + row + 8 * y;
-        if (i >= c.len) continue;
-        const int64_t t = c.t0 + i;
-        const int cs = s * 16 + x * 8 + col;
+      for (int x = 0; x < 2; ++x) {
+        const int64_t to = out + y * 8 * out_ld + s * 16 + x * 8;
         if (shares != nullptr)
-          *reinterpret_cast<float2*>(shares + t * a.H * D + h * D + cs) =
-              make_float2(acc[x][2 * y], acc[x][2 * y + 1]);
+          *reinterpret_cast<float2*>(shares + to) = make_float2(acc[x][2 * y], acc[x][2 * y + 1]);
         else
-          *reinterpret_cast<uint32_t*>(grads + t * a.Hk * D + h * D + cs) =
-              pack_bf16x2(acc[x][2 * y], acc[x][2 * y + 1]);
+          *reinterpret_cast<uint32_t*>(grads + to) = pack_bf16x2(acc[x][2 * y], acc[x][2 * y + 1]);
       }
+    }
   }
   if (!ok && tid == 0) {  // a wait gave up: the copies must land before the block is gone
     volatile int never = 0;
     mbar_wait(&bar[0], 0, &never, a.err, kErrWaitFinal);
-    for (int s = L::NS - 2; s < L::NS; ++s)
-      mbar_wait(&bar[1 + s % 2], (uint32_t)(s / 2 & 1), &never, a.err, kErrWaitFinal);
+    for (int s = issued - L::RING; s < issued; ++s)
+      mbar_wait(&full[s % L::RING], (uint32_t)(s / L::RING & 1), &never, a.err, kErrWaitFinal);
   }
 }
 
