@@ -200,19 +200,6 @@ __device__ __forceinline__ void keep_anchor(float* to, const float (&s)[N][4], i
     reinterpret_cast<float4*>(to)[(first + j) * 32 + lane] =
         make_float4(s[j][0], s[j][1], s[j][2], s[j][3]);
 }
-template <int N>
-__device__ __forceinline__ float dot_anchor(const float* from, const float (&s)[N][4], int first,
-                                            int lane) {
-  float x = 0.f;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float4 v = reinterpret_cast<const float4*>(from)[(first + j) * 32 + lane];
-    x = fmaf(s[j][0], v.x, fmaf(s[j][1], v.y, fmaf(s[j][2], v.z, fmaf(s[j][3], v.w, x))));
-  }
-#pragma unroll
-  for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
-  return x;
-}
 // Sums over 16 rows of an accumulator times the tile's bf16 values (w0: rows 0-7,
 // w1: rows 8-15), of the lane's two tokens; in every lane of the column.
 __device__ __forceinline__ float2 rows_sum(float2 x) {
@@ -277,9 +264,6 @@ struct DeltaKept {
 
 // Inverses, P and gates of every chunk into `blocks` (kernels_delta_tc.cu).
 cudaError_t delta_prepare(const DeltaArgs& a, bool gradient, uint8_t* blocks, cudaStream_t st);
-// The chain of states for the gradient.
-cudaError_t delta_states_kept(const DeltaArgs& a, const float* S_in, const void* dO,
-                              const uint8_t* blocks, const DeltaKept& kept, cudaStream_t st);
 // Which form of the chain's kernels a call takes (both directions the same).
 bool delta_few_rows(const DeltaArgs& a);
 

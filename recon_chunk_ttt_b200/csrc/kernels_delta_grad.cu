@@ -20,15 +20,13 @@
 // (the gates' gradients and dS are fp32 results), the rest is bf16 products
 // summed in fp32.
 
-#include <type_traits>
-
-#include "delta_tc.cuh"
+#include "delta_state.cuh"
 
 namespace ttt {
 namespace {
 
 // ----------------------------------------------------------------------------
-// delta_reverse_kernel: as delta_state_kernel, KS warps share 16 rows of E.
+// The chain of E: as in delta_state_chain, KS warps share 16 rows of E.
 // ----------------------------------------------------------------------------
 template <int D, int KS, int RG, int ST>
 struct RK {
@@ -56,34 +54,33 @@ struct ReverseArgs {
   float scale;
   const uint8_t* blocks;
   const int32_t* order;
-  DeltaKept kept;
   const float* dS_out;
   float* dS_in;
   __nv_bfloat16* dV;
   __nv_bfloat16* E;    // the gradient behind each chunk, blocked as S0
   __nv_bfloat16* dVt;  // dV, blocked as U
-  float *dots_v, *dots_x;        // [d / 16][H][n]: dV . V, X . w
-  float *hold, *hold_last;       // [anchors or sequences][H][d / 16][KS]: <E, S>
+  float* X32;          // X in fp32, as U32
+  float* anchors;      // E before every kAnchor-th chunk, as the states' anchors
+  float* last;         // E behind the last tokens, or nullptr
+  float* dots;         // [d / 16][H][n]: dV . V over 16 columns
   int* err;
 };
 
 template <int D, int KS, int RG, int ST>
-__global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
-    delta_reverse_kernel(const __grid_constant__ CUtensorMap mQ,
-                         const __grid_constant__ CUtensorMap mK,
-                         const __grid_constant__ CUtensorMap mV,
-                         const __grid_constant__ CUtensorMap mG, const ReverseArgs a) {
+__device__ __forceinline__ void delta_reverse_chain(const CUtensorMap& mQ, const CUtensorMap& mK,
+                                                    const CUtensorMap& mV, const CUtensorMap& mG,
+                                                    const ReverseArgs& a, uint8_t* smem_raw,
+                                                    int bx, int h, int64_t rank) {
   using L = RK<D, KS, RG, ST>;
   constexpr int DK = D / KS, NT = 8 / KS;
-  extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* empty = full + 2;
   uint64_t* met = empty + 2;  // 3 for each group: partial sums, dU, dV are written
   volatile int* abort_flag = reinterpret_cast<volatile int*>(met + 3 * RG);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int h = blockIdx.y, hk = h / (a.H / a.Hk);
-  const int64_t seq = a.order != nullptr ? a.order[blockIdx.z] : blockIdx.z;
+  const int hk = h / (a.H / a.Hk);
+  const int64_t seq = a.order != nullptr ? a.order[rank] : rank;
   const SeqRange sr = seq_range(a.offsets, a.n, seq);
   const int64_t len = sr.t1 - sr.t0;
   const int64_t nc = (len + kC - 1) / kC;
@@ -112,7 +109,7 @@ __global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
         tma_load_3d(st, &mK, &full[s], 0, t, hk * (D / 64));
         tma_load_3d(st + L::KQ, &mQ, &full[s], 0, t, hk * (D / 64));
         for (int g = 0; g < RG; ++g) {
-          const int x = h * D + ((int)blockIdx.x * RG + g) * 16;
+          const int x = h * D + (bx * RG + g) * 16;
           tma_load_2d(st + 2 * L::KQ + g * L::V, &mV, &full[s], x, t);
           tma_load_2d(st + 2 * L::KQ + (RG + g) * L::V, &mG, &full[s], x, t);
         }
@@ -126,7 +123,7 @@ __global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
   }
 
   const int grp = warp / KS, kw = warp % KS;
-  const int r0 = ((int)blockIdx.x * RG + grp) * 16, c0 = kw * DK;
+  const int r0 = (bx * RG + grp) * 16, c0 = kw * DK;
   const int row = lane / 4, col = 2 * (lane % 4);
   uint8_t* x_part = smem + L::OFF_X + grp * L::X;
   uint8_t* x_u = x_part + L::X_PART;
@@ -155,11 +152,8 @@ __global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
     }
     s[j][0] = x.x, s[j][1] = x.y, s[j][2] = y.x, s[j][3] = y.y;
   }
-  const int first = (r0 / 16 * KS + kw) * (DK / 8);  // this warp's place in an anchor
-  if (a.dS_out != nullptr) {
-    const float x = dot_anchor(a.kept.last + (seq * a.H + h) * (int64_t)D * D, s, first, lane);
-    if (lane == 0) a.hold_last[(seq * a.H + h) * (D / 16) * KS + r0 / 16 * KS + kw] = x;
-  }
+  if (a.last != nullptr)  // dS_in may lie over dS_out
+    keep_anchor(a.last + (seq * a.H + h) * (int64_t)D * D, s, (r0 / 16 * KS + kw) * (DK / 8), lane);
   const int nk_r = (lane / 16) * 8 + lane % 8, nk_c = lane / 8 % 2;
   const int kn_r = lane % 16, kn_c = (lane / 16) * 8;
 
@@ -284,12 +278,6 @@ __global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
     };
     put_parts(x_u, du);
     arrive(1);
-    // U of this warp's tiles, for X . w
-    float4 u32[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      u32[j] = reinterpret_cast<const float4*>(
-          a.kept.U32)[((at * (D / 16) + r0 / 16) * 8 + tile(j)) * 32 + lane];
     if (!wait(1, i)) break;
     // X = T^T dU
     float xt[NT][4] = {};
@@ -342,18 +330,15 @@ __global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
         const int j = 2 * p + z, t = tile(j) * 8 + col;
         const float2 be = *reinterpret_cast<const float2*>(gates + 2 * kC + t);
         const float2 ga = *reinterpret_cast<const float2*>(gates + t);
-        float2 xw = make_float2(fmaf(xt[j][0], u32[j].x, xt[j][2] * u32[j].z),
-                                fmaf(xt[j][1], u32[j].y, xt[j][3] * u32[j].w));
-        xw = rows_sum(xw);
-        put_dots(a.dots_x + dots + tile(j) * 8, make_float2(xw.x / be.x, xw.y / be.y), tile(j) * 8,
-                 valid, lane);
+        reinterpret_cast<float4*>(a.X32)[((at * (D / 16) + r0 / 16) * 8 + tile(j)) * 32 + lane] =
+            make_float4(xt[j][0], xt[j][1], xt[j][2], xt[j][3]);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const float b = y % 2 ? be.y : be.x;
           xt[j][y] *= b == kNoBeta ? 0.f : b;
           gd[j][y] = -(y % 2 ? ga.y : ga.x) * xt[j][y];
         }
-        put_dots(a.dots_v + dots + tile(j) * 8, dot_pair(xt[j], v[2 * z], v[2 * z + 1]), tile(j) * 8,
+        put_dots(a.dots + dots + tile(j) * 8, dot_pair(xt[j], v[2 * z], v[2 * z + 1]), tile(j) * 8,
                  valid, lane);
         keep_tile<D>(a.dVt + at * kC * D, xt[j], r0, tile(j), lane);
       }
@@ -440,11 +425,9 @@ __global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
       load_a(d + 64, lo[k]);
     }
     add_any(sK, hi, mid, lo, 1.f);
-    if (c % kAnchor == 0) {  // <E, S> before the chunk: where the decays' running sum starts anew
-      const int64_t slot = (sr.t0 / (kC * kAnchor) + seq + c / kAnchor) * a.H + h;
-      const float x = dot_anchor(a.kept.anchors + slot * D * D, s, first, lane);
-      if (lane == 0) a.hold[slot * (D / 16) * KS + r0 / 16 * KS + kw] = x;
-    }
+    if (c % kAnchor == 0)  // E before the chunk: where the decays' running sum starts anew
+      keep_anchor(a.anchors + ((sr.t0 / (kC * kAnchor) + seq + c / kAnchor) * a.H + h) *
+                                  (int64_t)D * D, s, (r0 / 16 * KS + kw) * (DK / 8), lane);
     fence_proxy_async_smem();  // dV's stores into the stage come before the next loads
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
@@ -462,17 +445,45 @@ __global__ void __launch_bounds__(RK<D, KS, RG, ST>::THREADS, ST == 1 ? 2 : 1)
 }
 
 // ----------------------------------------------------------------------------
-// dlog_decay and dbeta of 512 tokens of a sequence and head (from one anchor to the
-// next): sums over the d / 16 groups of columns, and the running sum from the
-// stretch's end.  A few blocks' work, done beside dQ and dK.
+// delta_chains_kernel: both chains of every sequence at once.  Neither needs the other:
+// what joins them (dbeta and the decays' gradient) is formed behind them.  So few long
+// sequences fill twice the SMs, and where there are many, the short chains of one kind fill
+// up beside the long ones of the other.
+// ----------------------------------------------------------------------------
+template <int D, int ST>
+constexpr int chains_smem() {
+  return SK<D, 4, 1, ST, true>::SMEM > RK<D, 4, 1, ST>::SMEM ? SK<D, 4, 1, ST, true>::SMEM
+                                                             : RK<D, 4, 1, ST>::SMEM;
+}
+template <int D, int ST>
+__global__ void __launch_bounds__(RK<D, 4, 1, ST>::THREADS, ST == 1 ? 2 : 1)
+    delta_chains_kernel(const __grid_constant__ CUtensorMap mQ,
+                        const __grid_constant__ CUtensorMap mK,
+                        const __grid_constant__ CUtensorMap mV,
+                        const __grid_constant__ CUtensorMap mG,
+                        const __grid_constant__ StateArgs f, const __grid_constant__ ReverseArgs r) {
+  extern __shared__ uint8_t smem_raw[];
+  const int x = blockIdx.x / 2, h = blockIdx.y;
+  if (blockIdx.x % 2 == 0)
+    delta_reverse_chain<D, 4, 1, ST>(mQ, mK, mV, mG, r, smem_raw, x, h, blockIdx.z);
+  else
+    delta_state_chain<D, 4, 1, ST, true>(mQ, mK, mV, mG, f, smem_raw, x, h, blockIdx.z);
+}
+
+// ----------------------------------------------------------------------------
+// dlog_decay of 512 tokens of a sequence and head (from one anchor to the next): <E, S>
+// at the stretch's end and the running sum from there.  A few blocks' work, done beside
+// dQ and dK.
 // ----------------------------------------------------------------------------
 constexpr int kGW = 8;  // warps of a block
 constexpr int kStretch = kC * kAnchor;
 
 struct GateArgs {
-  int groups, ks;
-  const float *dots_o, *dots_v, *dots_x, *hold, *hold_last;  // hold_last: or nullptr (zeros)
-  float *dg, *db;
+  int groups;
+  const float *dots_o, *dots_v;
+  const float *S, *E;            // anchors
+  const float *S_last, *E_last;  // behind the last tokens, or both nullptr: zeros
+  float* dg;
 };
 
 __device__ __forceinline__ void gate_stretch(const GateArgs& a, const int64_t* offsets, int64_t n,
@@ -490,44 +501,51 @@ __device__ __forceinline__ void gate_stretch(const GateArgs& a, const int64_t* o
   const int64_t b0 = s.t0 + (slot - (s.t0 / kStretch + lo)) * kStretch;
   if (b0 < s.t0 || b0 >= s.t1) return;
   const int64_t b1 = b0 + kStretch < s.t1 ? b0 + kStretch : s.t1;
-  // <E, S> at the end: the next anchor's, or the last states'
-  const int parts = a.groups * a.ks;
-  const float* end = b1 < s.t1 ? a.hold + ((slot + 1) * H + h) * parts
-                     : a.hold_last != nullptr ? a.hold_last + (lo * H + h) * parts
-                                              : nullptr;
+  // <E, S> at the end, the next anchor's or the last states': this thread's share
+  const int64_t size = (int64_t)a.groups * a.groups * 256;
+  const bool next = b1 < s.t1;
+  const float* es = next ? a.E + ((slot + 1) * H + h) * size
+                         : a.E_last != nullptr ? a.E_last + (lo * H + h) * size : nullptr;
+  const float* ss = next ? a.S + ((slot + 1) * H + h) * size : a.S_last + (lo * H + h) * size;
   float x = 0.f;
-  if (end != nullptr)
-    for (int i = 0; i < parts; ++i) x += end[i];
+  if (es != nullptr)
+#pragma unroll 4
+    for (int64_t i = tid * 4; i < size; i += 32 * kGW * 4) {
+      const float4 e = *reinterpret_cast<const float4*>(es + i);
+      const float4 y = *reinterpret_cast<const float4*>(ss + i);
+      x = fmaf(e.x, y.x, fmaf(e.y, y.y, fmaf(e.z, y.z, fmaf(e.w, y.w, x))));
+    }
   constexpr int PER = kStretch / (32 * kGW);
   float v[PER], sum = 0.f;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int64_t t = b0 + tid * PER + q;
-    float o = 0.f, w = 0.f, b = 0.f;
+    float o = 0.f, w = 0.f;
     if (t < b1) {
 #pragma unroll 4
       for (int r = 0; r < a.groups; ++r) {
         const int64_t at = (r * (int64_t)H + h) * n + t;
         o += a.dots_o[at];
         w += a.dots_v[at];
-        b += a.dots_x[at];
       }
-      a.db[t * H + h] = b;
     }
     v[q] = o - w;
     sum += v[q];
   }
   // sums of the threads behind this one
-  __shared__ float warp_sum[kGW];
+  __shared__ float warp_sum[kGW], warp_x[kGW];
   const int lane = tid % 32, warp = tid / 32;
   float behind = sum;
   for (int m = 1; m < 32; m *= 2) {
     const float y = __shfl_down_sync(0xffffffffu, behind, m);
     if (lane + m < 32) behind += y;
   }
-  if (lane == 0) warp_sum[warp] = behind;
+  for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+  if (lane == 0) warp_sum[warp] = behind, warp_x[warp] = x;
   __syncthreads();
   behind -= sum;
+  x = 0.f;
+  for (int w = 0; w < kGW; ++w) x += warp_x[w];
   for (int w = warp + 1; w < kGW; ++w) behind += warp_sum[w];
   x += behind;
 #pragma unroll
@@ -575,8 +593,10 @@ struct TokensGradArgs {
   int64_t seqs;
   int H, Hk;
   float scale;
-  const float* g;
+  const float *g, *b;
   const __nv_bfloat16 *S0, *E, *U, *dVt;
+  const float *U32, *X32;
+  float* db;
   __nv_bfloat16 *dQ, *dK;  // heads of their own
   float *pq, *pk;          // shared heads: each head's share, [n][H * d]
   int64_t slots;           // the blocks from this on take the gates' gradients
@@ -651,6 +671,27 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
       Gh[2 * lane + i] = (float)g;
       Gl[2 * lane + i] = (float)(g - (double)(float)g);
     }
+  }
+  // dbeta = X . w = X . U / beta: a warp takes 8 tokens
+  {
+    const int64_t first = (at * (D / 16) * 8 + warp) * 32 + lane;
+    float2 xw = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < D / 16; ++r) {
+      const float4 x = reinterpret_cast<const float4*>(a.X32)[first + r * 256];
+      const float4 u = reinterpret_cast<const float4*>(a.U32)[first + r * 256];
+      xw.x = fmaf(x.x, u.x, fmaf(x.z, u.z, xw.x));
+      xw.y = fmaf(x.y, u.y, fmaf(x.w, u.w, xw.y));
+    }
+    xw = rows_sum(xw);
+    if (lane < 4)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = warp * 8 + 2 * lane + i;
+        if (j >= c.len) continue;
+        const float b = a.b[(c.t0 + j) * a.H + h];
+        a.db[(c.t0 + j) * a.H + h] = (i == 0 ? xw.x : xw.y) / (fabsf(b) <= kNoBeta ? kNoBeta : b);
+      }
   }
   __syncthreads();
   bool ok = mbar_wait(&bar[0], 0, abort_flag, a.err, kErrWaitFull);
@@ -873,13 +914,12 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
 
 // ----------------------------------------------------------------------------
 struct Plan {  // byte offsets in the workspace, and the whole
-  size_t blocks, S0, E, U, dVt, U32, anchors, last, dots_o, dots_v, dots_x, hold, hold_last, pq, pk,
-      total;
+  size_t blocks, S0, E, U, dVt, U32, X32, anchors, anchors_e, last, last_e, dots_o, dots_v, pq, pk, total;
 };
 int64_t stretches(const DeltaArgs& a) { return a.n / kStretch + a.seqs; }
 Plan plan_of(const DeltaArgs& a) {
   const size_t D = a.d, DD = D * D, ch = (size_t)chunk_slots(a) * a.H,
-               an = (size_t)stretches(a) * a.H, sq = (size_t)a.seqs * a.H, ks = 4;
+               an = (size_t)stretches(a) * a.H, sq = (size_t)a.seqs * a.H;
   Plan p;
   size_t o = 0;
   const auto take = [&](size_t bytes) {
@@ -893,13 +933,13 @@ Plan plan_of(const DeltaArgs& a) {
   p.U = take(2 * ch * kC * D * 2);
   p.dVt = take(ch * kC * D * 2);
   p.U32 = take(ch * kC * D * 4);
+  p.X32 = take(ch * kC * D * 4);
   p.anchors = take(an * DD * 4);
+  p.anchors_e = take(an * DD * 4);
   p.last = take(sq * DD * 4);
+  p.last_e = take(sq * DD * 4);
   p.dots_o = take(D / 16 * a.H * (size_t)a.n * 4);
   p.dots_v = take(D / 16 * a.H * (size_t)a.n * 4);
-  p.dots_x = take(D / 16 * a.H * (size_t)a.n * 4);
-  p.hold = take(an * (D / 16) * ks * 4);
-  p.hold_last = take(sq * (D / 16) * ks * 4);
   const size_t share = a.H == a.Hk ? 0 : (size_t)a.n * a.H * D * 4;
   p.pq = take(share);
   p.pk = take(share);
@@ -914,30 +954,21 @@ struct Call {
   float *dg, *db, *dS_in;
 };
 
-template <int D, int KS, int RG, int ST>
-cudaError_t launch_reverse(const DeltaArgs& a, const Call& x, char* w, const Plan& p,
-                           const DeltaKept& kept, cudaStream_t st) {
-  using L = RK<D, KS, RG, ST>;
+template <int D, int ST>
+cudaError_t launch_chains(const DeltaArgs& a, const Call& x, const StateArgs& f,
+                          const ReverseArgs& r, cudaStream_t st) {
   CUtensorMap mQ = {}, mK = {}, mV = {}, mG = {};
   if (a.n > 0 && (!head_map(&mQ, a.Q, a.n, a.ldq, a.Hk * D, D) ||
                   !head_map(&mK, a.K, a.n, a.ldk, a.Hk * D, D) ||
                   !strip_map(&mV, a.V, a.n, a.ldv, a.H * D) ||
                   !strip_map(&mG, x.dO, a.n, (int64_t)a.H * D, a.H * D)))
     return cudaErrorInvalidValue;
-  const cudaError_t e = ensure_smem_attr(delta_reverse_kernel<D, KS, RG, ST>, L::SMEM);
+  const cudaError_t e = ensure_smem_attr(delta_chains_kernel<D, ST>, chains_smem<D, ST>());
   if (e != cudaSuccess) return e;
-  const ReverseArgs k = {a.n, a.offsets, a.H, a.Hk, a.scale,
-                         reinterpret_cast<const uint8_t*>(w + p.blocks),
-                         order_of(a, reinterpret_cast<const uint8_t*>(w + p.blocks)), kept, x.dS_out, x.dS_in,
-                         static_cast<__nv_bfloat16*>(x.dV),
-                         reinterpret_cast<__nv_bfloat16*>(w + p.E),
-                         reinterpret_cast<__nv_bfloat16*>(w + p.dVt),
-                         reinterpret_cast<float*>(w + p.dots_v),
-                         reinterpret_cast<float*>(w + p.dots_x), reinterpret_cast<float*>(w + p.hold),
-                         reinterpret_cast<float*>(w + p.hold_last), device_error_ptr()};
-  TraceScope ts("delta_reverse", st);
-  delta_reverse_kernel<D, KS, RG, ST><<<dim3(D / (16 * RG), (unsigned)a.H, (unsigned)a.seqs),
-                                    L::THREADS, L::SMEM, st>>>(mQ, mK, mV, mG, k);
+  TraceScope ts("delta_chains", st);
+  delta_chains_kernel<D, ST><<<dim3(2 * (D / 16), (unsigned)a.H, (unsigned)a.seqs),
+                               RK<D, 4, 1, ST>::THREADS, chains_smem<D, ST>(), st>>>(mQ, mK, mV, mG,
+                                                                                     f, r);
   return cudaGetLastError();
 }
 
@@ -952,11 +983,13 @@ cudaError_t launch_tokens(const DeltaArgs& a, const Call& x, char* w, const Plan
   const cudaError_t e = ensure_smem_attr(delta_tokens_grad_kernel<D>, L::SMEM);
   if (e != cudaSuccess) return e;
   const bool own = a.H == a.Hk;
-  const TokensGradArgs k = {a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, a.g,
+  const TokensGradArgs k = {a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, a.g, a.b,
                             reinterpret_cast<const __nv_bfloat16*>(w + p.S0),
                             reinterpret_cast<const __nv_bfloat16*>(w + p.E),
                             reinterpret_cast<const __nv_bfloat16*>(w + p.U),
                             reinterpret_cast<const __nv_bfloat16*>(w + p.dVt),
+                            reinterpret_cast<const float*>(w + p.U32),
+                            reinterpret_cast<const float*>(w + p.X32), x.db,
                             static_cast<__nv_bfloat16*>(x.dQ), static_cast<__nv_bfloat16*>(x.dK),
                             own ? nullptr : reinterpret_cast<float*>(w + p.pq),
                             own ? nullptr : reinterpret_cast<float*>(w + p.pk), chunk_slots(a), gates,
@@ -978,34 +1011,28 @@ cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, co
   const Plan p = plan_of(a);
   char* w = static_cast<char*>(ws);
   uint8_t* blocks = reinterpret_cast<uint8_t*>(w + p.blocks);
-  const DeltaKept kept = {reinterpret_cast<__nv_bfloat16*>(w + p.S0),
-                          reinterpret_cast<__nv_bfloat16*>(w + p.U),
-                          reinterpret_cast<float*>(w + p.U32),
-                          reinterpret_cast<float*>(w + p.anchors),
-                          dS_out != nullptr ? reinterpret_cast<float*>(w + p.last) : nullptr,
-                          reinterpret_cast<float*>(w + p.dots_o)};
+  const auto floats = [&](size_t at) { return reinterpret_cast<float*>(w + at); };
+  const auto halves = [&](size_t at) { return reinterpret_cast<__nv_bfloat16*>(w + at); };
   const Call x = {dS_out, dO, dQ, dK, dV, dg, db, dS_in};
   cudaError_t e = delta_prepare(a, true, blocks, st);
   if (e != cudaSuccess) return e;
-  e = delta_states_kept(a, S_in, dO, blocks, kept, st);
-  if (e != cudaSuccess) return e;
+  float* last = dS_out != nullptr ? floats(p.last) : nullptr;
+  float* last_e = dS_out != nullptr ? floats(p.last_e) : nullptr;
+  const DeltaKept kept = {halves(p.S0), halves(p.U), floats(p.U32), floats(p.anchors),
+                          last, floats(p.dots_o)};
+  const StateArgs f = {a.n, a.offsets, a.H, a.Hk, a.scale, blocks, order_of(a, blocks), S_in, nullptr,
+                       nullptr, -1, kept, device_error_ptr()};
+  const ReverseArgs r = {a.n, a.offsets, a.H, a.Hk, a.scale, blocks, order_of(a, blocks), dS_out,
+                         dS_in, static_cast<__nv_bfloat16*>(dV), halves(p.E), halves(p.dVt),
+                         floats(p.X32), floats(p.anchors_e), last_e,
+                         floats(p.dots_v), device_error_ptr()};
   const bool few = delta_few_rows(a);
-  constexpr int ks = 4;  // of every form of the reverse chain
-  if (a.d == 64) {
-    e = few ? launch_reverse<64, 4, 1, 2>(a, x, w, p, kept, st)
-            : launch_reverse<64, 4, 1, 1>(a, x, w, p, kept, st);
-  } else if (a.d == 128) {
-    e = few ? launch_reverse<128, 4, 1, 2>(a, x, w, p, kept, st)
-            : launch_reverse<128, 4, 1, 1>(a, x, w, p, kept, st);
-  } else {
-    e = launch_reverse<256, 4, 1, 2>(a, x, w, p, kept, st);
-  }
+  e = a.d == 64    ? few ? launch_chains<64, 2>(a, x, f, r, st) : launch_chains<64, 1>(a, x, f, r, st)
+      : a.d == 128 ? few ? launch_chains<128, 2>(a, x, f, r, st) : launch_chains<128, 1>(a, x, f, r, st)
+                   : launch_chains<256, 2>(a, x, f, r, st);
   if (e != cudaSuccess || a.n == 0) return e;
-  const GateArgs gates = {
-      a.d / 16, ks, reinterpret_cast<const float*>(w + p.dots_o),
-      reinterpret_cast<const float*>(w + p.dots_v), reinterpret_cast<const float*>(w + p.dots_x),
-      reinterpret_cast<const float*>(w + p.hold),
-      dS_out != nullptr ? reinterpret_cast<const float*>(w + p.hold_last) : nullptr, dg, db};
+  const GateArgs gates = {a.d / 16, floats(p.dots_o), floats(p.dots_v), floats(p.anchors),
+                          floats(p.anchors_e), last, last_e, dg};
   e = a.d == 64    ? launch_tokens<64>(a, x, w, p, gates, st)
       : a.d == 128 ? launch_tokens<128>(a, x, w, p, gates, st)
                    : launch_tokens<256>(a, x, w, p, gates, st);
