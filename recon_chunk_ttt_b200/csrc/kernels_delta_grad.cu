@@ -447,8 +447,10 @@ __device__ __forceinline__ void delta_reverse_chain(const CUtensorMap& mQ, const
 // ----------------------------------------------------------------------------
 // delta_chains_kernel: both chains of every sequence at once.  Neither needs the other:
 // what joins them (dbeta and the decays' gradient) is formed behind them.  So few long
-// sequences fill twice the SMs, and where there are many, the short chains of one kind fill
-// up beside the long ones of the other.
+// sequences fill twice the SMs (1,374 tokens, 4 heads of 256: 99 us, one chain after the
+// other 189 us), and where there are many, the short chains of one kind fill up beside the
+// long ones of the other.  Blocks of a kind lie together in the grid: neighbouring SMs share
+// what they fetch of the code (alternating kinds: 127 us).
 // ----------------------------------------------------------------------------
 template <int D, int ST>
 constexpr int chains_smem() {
@@ -463,11 +465,12 @@ __global__ void __launch_bounds__(RK<D, 4, 1, ST>::THREADS, ST == 1 ? 2 : 1)
                         const __grid_constant__ CUtensorMap mG,
                         const __grid_constant__ StateArgs f, const __grid_constant__ ReverseArgs r) {
   extern __shared__ uint8_t smem_raw[];
-  const int x = blockIdx.x / 2, h = blockIdx.y;
-  if (blockIdx.x % 2 == 0)
-    delta_reverse_chain<D, 4, 1, ST>(mQ, mK, mV, mG, r, smem_raw, x, h, blockIdx.z);
+  const int h = blockIdx.y;
+  if (h < f.H)
+    delta_reverse_chain<D, 4, 1, ST>(mQ, mK, mV, mG, r, smem_raw, blockIdx.x, h, blockIdx.z);
   else
-    delta_state_chain<D, 4, 1, ST, true>(mQ, mK, mV, mG, f, smem_raw, x, h, blockIdx.z);
+    delta_state_chain<D, 4, 1, ST, true>(mQ, mK, mV, mG, f, smem_raw, blockIdx.x, h - f.H,
+                                         blockIdx.z);
 }
 
 // ----------------------------------------------------------------------------
@@ -599,7 +602,7 @@ struct TokensGradArgs {
   float* db;
   __nv_bfloat16 *dQ, *dK;  // heads of their own
   float *pq, *pk;          // shared heads: each head's share, [n][H * d]
-  int64_t slots;           // the blocks from this on take the gates' gradients
+  int64_t stretches;       // the first blocks take the decays' gradients
   GateArgs gates;
   int* err;
 };
@@ -619,10 +622,10 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
   uint64_t *full = bar + 1, *empty = full + L::RING;               // strips
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + L::RING);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t slot = blockIdx.x;
+  const int64_t slot = (int64_t)blockIdx.x - a.stretches;
   const int h = blockIdx.y, hk = h / (a.H / a.Hk);
-  if (slot >= a.slots) {
-    gate_stretch(a.gates, a.offsets, a.n, a.seqs, a.H, slot - a.slots, h, tid);
+  if (slot < 0) {
+    gate_stretch(a.gates, a.offsets, a.n, a.seqs, a.H, blockIdx.x, h, tid);
     return;
   }
   const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
   {
     const int64_t first = (at * (D / 16) * 8 + warp) * 32 + lane;
     float2 xw = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int r = 0; r < D / 16; ++r) {
       const float4 x = reinterpret_cast<const float4*>(a.X32)[first + r * 256];
       const float4 u = reinterpret_cast<const float4*>(a.U32)[first + r * 256];
@@ -966,7 +969,7 @@ cudaError_t launch_chains(const DeltaArgs& a, const Call& x, const StateArgs& f,
   const cudaError_t e = ensure_smem_attr(delta_chains_kernel<D, ST>, chains_smem<D, ST>());
   if (e != cudaSuccess) return e;
   TraceScope ts("delta_chains", st);
-  delta_chains_kernel<D, ST><<<dim3(2 * (D / 16), (unsigned)a.H, (unsigned)a.seqs),
+  delta_chains_kernel<D, ST><<<dim3(D / 16, 2 * (unsigned)a.H, (unsigned)a.seqs),
                                RK<D, 4, 1, ST>::THREADS, chains_smem<D, ST>(), st>>>(mQ, mK, mV, mG,
                                                                                      f, r);
   return cudaGetLastError();
@@ -992,7 +995,7 @@ cudaError_t launch_tokens(const DeltaArgs& a, const Call& x, char* w, const Plan
                             reinterpret_cast<const float*>(w + p.X32), x.db,
                             static_cast<__nv_bfloat16*>(x.dQ), static_cast<__nv_bfloat16*>(x.dK),
                             own ? nullptr : reinterpret_cast<float*>(w + p.pq),
-                            own ? nullptr : reinterpret_cast<float*>(w + p.pk), chunk_slots(a), gates,
+                            own ? nullptr : reinterpret_cast<float*>(w + p.pk), stretches(a), gates,
                             device_error_ptr()};
   TraceScope ts("delta_tokens_grad", st);
   delta_tokens_grad_kernel<D><<<dim3((unsigned)(chunk_slots(a) + stretches(a)), (unsigned)a.H), 32 * kGW, L::SMEM,
