@@ -377,12 +377,7 @@ __device__ __forceinline__ void delta_state_chain(const CUtensorMap& mQ, const C
       d[64] = make_uint2(mid[0], mid[1]);
       if (GRAD) {
         d[320] = make_uint2(lo[0], lo[1]);
-        float left[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) left[y] = ut[j][y] - __bfloat162float(__float2bfloat16_rn(ut[j][y]));
-        keep_tile<D>(a.kept.U + 2 * at * kC * D, ut[j], r0, t, lane);
-        keep_tile<D>(a.kept.U + (2 * at + 1) * kC * D, left, r0, t, lane);
-        reinterpret_cast<float4*>(a.kept.U32)[((at * (D / 16) + r0 / 16) * 8 + t) * 32 + lane] =
+        reinterpret_cast<float4*>(a.kept.U)[((at * (D / 16) + r0 / 16) * 8 + t) * 32 + lane] =
             make_float4(ut[j][0], ut[j][1], ut[j][2], ut[j][3]);
       }
       const float2 re = *reinterpret_cast<const float2*>(gates + kC + t * 8 + col);

@@ -183,14 +183,6 @@ __device__ __forceinline__ void keep_state(__nv_bfloat16* to, const float (&s)[D
     w[(block + 2) * 32 + lane] = pack_bf16x2(s[j][2], s[j][3]);
   }
 }
-// 16 rows of the transpose of a [64 tokens][D] array, token tile t: blocks [row / 8][token / 8].
-template <int D>
-__device__ __forceinline__ void keep_tile(__nv_bfloat16* to, const float (&u)[4], int r0, int t,
-                                          int lane) {
-  uint32_t* w = reinterpret_cast<uint32_t*>(to) + (r0 / 8 * 8 + t) * 32 + lane;
-  w[0] = pack_bf16x2(u[0], u[1]);
-  w[8 * 32] = pack_bf16x2(u[2], u[3]);
-}
 // The state in fp32, as the registers lie.
 template <int N>
 __device__ __forceinline__ void keep_anchor(float* to, const float (&s)[N][4], int first,
@@ -255,8 +247,7 @@ inline bool strip_map(CUtensorMap* m, const void* base, int64_t n, int64_t ld, i
 // What the forward pass leaves for the gradient, by chunk slot and head.
 struct DeltaKept {
   __nv_bfloat16* S0;  // the state before the chunk
-  __nv_bfloat16* U;   // [d][64 tokens]: rounded, and what the rounding left
-  float* U32;         // U in fp32, as registers lie
+  float* U;           // in fp32, as registers lie: [d / 16][64 / 8][lane] of 4
   float* anchors;     // the state before every kAnchor-th chunk of a sequence
   float* last;        // the last states, or nullptr
   float* dots;        // [d / 16][H][n]: dO . O over 16 columns

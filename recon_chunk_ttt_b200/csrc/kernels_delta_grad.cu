@@ -58,8 +58,7 @@ struct ReverseArgs {
   float* dS_in;
   __nv_bfloat16* dV;
   __nv_bfloat16* E;    // the gradient behind each chunk, blocked as S0
-  __nv_bfloat16* dVt;  // dV, blocked as U
-  float* X32;          // X in fp32, as U32
+  float* X;            // in fp32, as U
   float* anchors;      // E before every kAnchor-th chunk, as the states' anchors
   float* last;         // E behind the last tokens, or nullptr
   float* dots;         // [d / 16][H][n]: dV . V over 16 columns
@@ -330,7 +329,7 @@ __device__ __forceinline__ void delta_reverse_chain(const CUtensorMap& mQ, const
         const int j = 2 * p + z, t = tile(j) * 8 + col;
         const float2 be = *reinterpret_cast<const float2*>(gates + 2 * kC + t);
         const float2 ga = *reinterpret_cast<const float2*>(gates + t);
-        reinterpret_cast<float4*>(a.X32)[((at * (D / 16) + r0 / 16) * 8 + tile(j)) * 32 + lane] =
+        reinterpret_cast<float4*>(a.X)[((at * (D / 16) + r0 / 16) * 8 + tile(j)) * 32 + lane] =
             make_float4(xt[j][0], xt[j][1], xt[j][2], xt[j][3]);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -340,7 +339,6 @@ __device__ __forceinline__ void delta_reverse_chain(const CUtensorMap& mQ, const
         }
         put_dots(a.dots + dots + tile(j) * 8, dot_pair(xt[j], v[2 * z], v[2 * z + 1]), tile(j) * 8,
                  valid, lane);
-        keep_tile<D>(a.dVt + at * kC * D, xt[j], r0, tile(j), lane);
       }
     }
     put_parts(x_v, gd);
@@ -597,8 +595,8 @@ struct TokensGradArgs {
   int H, Hk;
   float scale;
   const float *g, *b;
-  const __nv_bfloat16 *S0, *E, *U, *dVt;
-  const float *U32, *X32;
+  const __nv_bfloat16 *S0, *E;
+  const float *U, *X;
   float* db;
   __nv_bfloat16 *dQ, *dK;  // heads of their own
   float *pq, *pk;          // shared heads: each head's share, [n][H * d]
@@ -648,10 +646,8 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     }
     *abort_flag = 0;
     fence_mbar_init();
-    mbar_arrive_expect_tx(&bar[0], 4 * L::TOK);
+    mbar_arrive_expect_tx(&bar[0], L::TOK);
     tma_load_3d(pG, &mG, &bar[0], 0, (int)c.t0, h * (D / 64));
-    bulk_load(pU, a.U + 2 * at * kC * D, 2 * L::TOK, &bar[0]);
-    bulk_load(pV, a.dVt + at * kC * D, L::TOK, &bar[0]);
     load_strip(0);
     load_strip(1);
   }
@@ -675,26 +671,43 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
       Gl[2 * lane + i] = (float)(g - (double)(float)g);
     }
   }
-  // dbeta = X . w = X . U / beta: a warp takes 8 tokens
+  // From U and X: U in two parts and dV = beta X, both [d][64 tokens] in blocks of 8 x 8 (8 rows
+  // of 16 bytes: what ldmatrix reads), and dbeta = X . U / beta.  A warp takes 8 tokens.
   {
     const int64_t first = (at * (D / 16) * 8 + warp) * 32 + lane;
+    float b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = warp * 8 + lane % 4 * 2 + i;
+      b[i] = j < c.len ? a.b[(c.t0 + j) * a.H + h] : 0.f;
+      if (fabsf(b[i]) <= kNoBeta) b[i] = 0.f;  // as in the chains
+    }
     float2 xw = make_float2(0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
     for (int r = 0; r < D / 16; ++r) {
-      const float4 x = reinterpret_cast<const float4*>(a.X32)[first + r * 256];
-      const float4 u = reinterpret_cast<const float4*>(a.U32)[first + r * 256];
+      const float4 x = reinterpret_cast<const float4*>(a.X)[first + r * 256];
+      const float4 u = reinterpret_cast<const float4*>(a.U)[first + r * 256];
       xw.x = fmaf(x.x, u.x, fmaf(x.z, u.z, xw.x));
       xw.y = fmaf(x.y, u.y, fmaf(x.w, u.w, xw.y));
+      const float us[4] = {u.x, u.y, u.z, u.w}, dv[4] = {b[0] * x.x, b[1] * x.y, b[0] * x.z, b[1] * x.w};
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t word = (r * 16 + y * 8 + warp) * 32 + lane;
+        const uint32_t hi = pack_bf16x2(us[2 * y], us[2 * y + 1]);
+        reinterpret_cast<uint32_t*>(pU)[word] = hi;
+        reinterpret_cast<uint32_t*>(pU + L::TOK)[word] =
+            pack_bf16x2(us[2 * y] - __uint_as_float(hi << 16),
+                        us[2 * y + 1] - __uint_as_float(hi & 0xffff0000u));
+        reinterpret_cast<uint32_t*>(pV)[word] = pack_bf16x2(dv[2 * y], dv[2 * y + 1]);
+      }
     }
     xw = rows_sum(xw);
     if (lane < 4)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = warp * 8 + 2 * lane + i;
-        if (j >= c.len) continue;
-        const float b = a.b[(c.t0 + j) * a.H + h];
-        a.db[(c.t0 + j) * a.H + h] = (i == 0 ? xw.x : xw.y) / (fabsf(b) <= kNoBeta ? kNoBeta : b);
-      }
+      for (int i = 0; i < 2; ++i)
+        if (warp * 8 + 2 * lane + i < c.len)
+          a.db[(c.t0 + warp * 8 + 2 * lane + i) * a.H + h] =
+              (i == 0 ? xw.x : xw.y) / (b[i] == 0.f ? kNoBeta : b[i]);
   }
   __syncthreads();
   bool ok = mbar_wait(&bar[0], 0, abort_flag, a.err, kErrWaitFull);
@@ -917,7 +930,7 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
 
 // ----------------------------------------------------------------------------
 struct Plan {  // byte offsets in the workspace, and the whole
-  size_t blocks, S0, E, U, dVt, U32, X32, anchors, anchors_e, last, last_e, dots_o, dots_v, pq, pk, total;
+  size_t blocks, S0, E, U, X, anchors, anchors_e, last, last_e, dots_o, dots_v, pq, pk, total;
 };
 int64_t stretches(const DeltaArgs& a) { return a.n / kStretch + a.seqs; }
 Plan plan_of(const DeltaArgs& a) {
@@ -933,10 +946,8 @@ Plan plan_of(const DeltaArgs& a) {
   p.blocks = take(blocks_bytes(a, 3)) + kOrderBytes;
   p.S0 = take(ch * DD * 2);
   p.E = take(ch * DD * 2);
-  p.U = take(2 * ch * kC * D * 2);
-  p.dVt = take(ch * kC * D * 2);
-  p.U32 = take(ch * kC * D * 4);
-  p.X32 = take(ch * kC * D * 4);
+  p.U = take(ch * kC * D * 4);
+  p.X = take(ch * kC * D * 4);
   p.anchors = take(an * DD * 4);
   p.anchors_e = take(an * DD * 4);
   p.last = take(sq * DD * 4);
@@ -989,10 +1000,8 @@ cudaError_t launch_tokens(const DeltaArgs& a, const Call& x, char* w, const Plan
   const TokensGradArgs k = {a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, a.g, a.b,
                             reinterpret_cast<const __nv_bfloat16*>(w + p.S0),
                             reinterpret_cast<const __nv_bfloat16*>(w + p.E),
-                            reinterpret_cast<const __nv_bfloat16*>(w + p.U),
-                            reinterpret_cast<const __nv_bfloat16*>(w + p.dVt),
-                            reinterpret_cast<const float*>(w + p.U32),
-                            reinterpret_cast<const float*>(w + p.X32), x.db,
+                            reinterpret_cast<const float*>(w + p.U),
+                            reinterpret_cast<const float*>(w + p.X), x.db,
                             static_cast<__nv_bfloat16*>(x.dQ), static_cast<__nv_bfloat16*>(x.dK),
                             own ? nullptr : reinterpret_cast<float*>(w + p.pq),
                             own ? nullptr : reinterpret_cast<float*>(w + p.pk), stretches(a), gates,
@@ -1021,13 +1030,13 @@ cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, co
   if (e != cudaSuccess) return e;
   float* last = dS_out != nullptr ? floats(p.last) : nullptr;
   float* last_e = dS_out != nullptr ? floats(p.last_e) : nullptr;
-  const DeltaKept kept = {halves(p.S0), halves(p.U), floats(p.U32), floats(p.anchors),
+  const DeltaKept kept = {halves(p.S0), floats(p.U), floats(p.anchors),
                           last, floats(p.dots_o)};
   const StateArgs f = {a.n, a.offsets, a.H, a.Hk, a.scale, blocks, order_of(a, blocks), S_in, nullptr,
                        nullptr, -1, kept, device_error_ptr()};
   const ReverseArgs r = {a.n, a.offsets, a.H, a.Hk, a.scale, blocks, order_of(a, blocks), dS_out,
-                         dS_in, static_cast<__nv_bfloat16*>(dV), halves(p.E), halves(p.dVt),
-                         floats(p.X32), floats(p.anchors_e), last_e,
+                         dS_in, static_cast<__nv_bfloat16*>(dV), halves(p.E),
+                         floats(p.X), floats(p.anchors_e), last_e,
                          floats(p.dots_v), device_error_ptr()};
   const bool few = delta_few_rows(a);
   e = a.d == 64    ? few ? launch_chains<64, 2>(a, x, f, r, st) : launch_chains<64, 1>(a, x, f, r, st)
