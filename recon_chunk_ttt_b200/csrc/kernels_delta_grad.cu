@@ -683,10 +683,20 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
       if (fabsf(b[i]) <= kNoBeta) b[i] = 0.f;  // as in the chains
     }
     float2 xw = make_float2(0.f, 0.f);
-#pragma unroll 4
+    constexpr int AHEAD = D / 16 < 8 ? D / 16 : 8;
+    float4 xs[AHEAD], uu[AHEAD];
+#pragma unroll
+    for (int r = 0; r < AHEAD; ++r) {
+      xs[r] = reinterpret_cast<const float4*>(a.X)[first + r * 256];
+      uu[r] = reinterpret_cast<const float4*>(a.U)[first + r * 256];
+    }
+#pragma unroll
     for (int r = 0; r < D / 16; ++r) {
-      const float4 x = reinterpret_cast<const float4*>(a.X)[first + r * 256];
-      const float4 u = reinterpret_cast<const float4*>(a.U)[first + r * 256];
+      const float4 x = xs[r % AHEAD], u = uu[r % AHEAD];
+      if (r + AHEAD < D / 16) {
+        xs[r % AHEAD] = reinterpret_cast<const float4*>(a.X)[first + (r + AHEAD) * 256];
+        uu[r % AHEAD] = reinterpret_cast<const float4*>(a.U)[first + (r + AHEAD) * 256];
+      }
       xw.x = fmaf(x.x, u.x, fmaf(x.z, u.z, xw.x));
       xw.y = fmaf(x.y, u.y, fmaf(x.w, u.w, xw.y));
       const float us[4] = {u.x, u.y, u.z, u.w}, dv[4] = {b[0] * x.x, b[1] * x.y, b[0] * x.z, b[1] * x.w};
