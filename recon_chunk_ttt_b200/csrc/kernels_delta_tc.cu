@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kChunkThreads)
   for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
+      if (nt > 2 * warp + 1) break;  // above the diagonal
       const int i = m0 + lane / 4 + 8 * half, j = nt * 8 + 2 * (lane % 4);
       float p[2];
 #pragma unroll
@@ -170,7 +171,6 @@ __global__ void __launch_bounds__(kChunkThreads)
           Lt2[(j + x - 32) * kLS + i - 32] = l;
         }
       }
-      if (j / 16 > i / 16) continue;  // above the diagonal blocks
       uint32_t* dst = reinterpret_cast<uint32_t*>(outP + tri(i, j));
       if (GRAD) {
         uint32_t hi, mid, lo;
@@ -213,27 +213,38 @@ __global__ void __launch_bounds__(kChunkThreads)
     }
   }
   __syncthreads();
-  const int r = tid / 4, cb = tid % 4 * 8;
-  float z[8] = {};
-#pragma unroll 4
-  for (int k = 0; k < 32; ++k) {
-    const float l = L21[r * kLS + k];
+  // a thread takes two rows of 4 columns
+  const auto product = [&](const float* x, const float* y, float* to, float sign) {
+    const int i = tid / 8 * 2, j = tid % 8 * 4;
+    float z[2][4] = {};
 #pragma unroll
-    for (int q = 0; q < 8; ++q) z[q] = fmaf(l, T1[k * kLS + cb + q], z[q]);
-  }
+    for (int k = 0; k < 32; k += 4) {
+      float xv[2][4], yv[4][4];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) Z[r * kLS + cb + q] = z[q];
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<float4*>(xv[q]) = *reinterpret_cast<const float4*>(x + (i + q) * kLS + k);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(yv[q]) = *reinterpret_cast<const float4*>(y + (k + q) * kLS + j);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) z[p][w] = fmaf(xv[p][q], yv[q][w], z[p][w]);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      *reinterpret_cast<float4*>(to + (i + p) * kLS + j) =
+          make_float4(sign * z[p][0], sign * z[p][1], sign * z[p][2], sign * z[p][3]);
+  };
+  product(L21, T1, Z, 1.f);
   __syncthreads();
-#pragma unroll
-  for (int q = 0; q < 8; ++q) z[q] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < 32; ++k) {
-    const float l = -T2[r * kLS + k];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) z[q] = fmaf(l, Z[k * kLS + cb + q], z[q]);
-  }
+  product(T2, Z, L21, -1.f);  // T21
+  __syncthreads();
   // rows r and r + 32 of T, 8 columns of each half, as 16-byte units
-  const float* src[3] = {T1 + r * kLS + cb, z, T2 + r * kLS + cb};
+  const int r = tid / 4, cb = tid % 4 * 8;
+  const float* src[3] = {T1 + r * kLS + cb, L21 + r * kLS + cb, T2 + r * kLS + cb};
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
     const int i = r + (q > 0 ? 32 : 0), j = cb + (q == 2 ? 32 : 0);
