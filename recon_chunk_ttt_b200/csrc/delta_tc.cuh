@@ -164,6 +164,32 @@ __device__ __forceinline__ uint32_t tri(int row, int col) {
          (col & 7) * 2;
 }
 
+// Running sums G of a chunk's log decays, in fp64 so that differences of far sums stay exact;
+// kept as two floats each.  One warp; tokens from `len` on add nothing.
+__device__ __forceinline__ void sum_decays(const float* g, int64_t t0, int len, int H, int h,
+                                           int lane, float2* G) {
+  double x[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = 2 * lane + i;
+    const float v = j < len ? g[(t0 + j) * H + h] : 0.f;
+    x[i] = v < -1e4f ? -1e4 : (double)v;  // e^-1e4 is 0 like e^-inf, but its sums are numbers
+  }
+  double s = x[0] + x[1];
+  for (int m = 1; m < 32; m *= 2) {
+    const double o = __shfl_up_sync(0xffffffffu, s, m);
+    if (lane >= m) s += o;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double v = i == 0 ? s - x[1] : s;
+    G[2 * lane + i] = make_float2((float)v, (float)(v - (double)(float)v));
+  }
+}
+// e^(a - b)
+__device__ __forceinline__ float decay(float2 a, float2 b) { return expf((a.x - b.x) + (a.y - b.y)); }
+__device__ __forceinline__ float decay(float2 a) { return expf(a.x + a.y); }
+
 // Every kAnchor-th chunk the state is kept in fp32: there the gradient of the decays,
 // a running sum over tokens, starts anew.
 constexpr int kAnchor = 8;

@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
   using L = GK<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  __shared__ float Gh[kC], Gl[kC];  // running sums of the log decays in two parts
+  __shared__ float2 G[kC];
   uint8_t *pG = smem, *pU = smem + L::TOK, *pV = smem + 3 * L::TOK,
           *pA = smem + L::OFF_A, *pM = pA + 2 * kTri;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);  // tokens
@@ -651,26 +651,7 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     load_strip(0);
     load_strip(1);
   }
-  if (warp == 1) {
-    double x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = 2 * lane + i;
-      const float g = j < c.len ? a.g[(c.t0 + j) * a.H + h] : 0.f;
-      x[i] = g < -1e4f ? -1e4 : (double)g;
-    }
-    double s = x[0] + x[1];
-    for (int m = 1; m < 32; m *= 2) {
-      const double o = __shfl_up_sync(0xffffffffu, s, m);
-      if (lane >= m) s += o;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const double g = i == 0 ? s - x[1] : s;
-      Gh[2 * lane + i] = (float)g;
-      Gl[2 * lane + i] = (float)(g - (double)(float)g);
-    }
-  }
+  if (warp == 1) sum_decays(a.g, c.t0, c.len, a.H, h, lane, G);
   // From U and X: U in two parts and dV = beta X, both [d][64 tokens] in blocks of 8 x 8 (8 rows
   // of 16 bytes: what ldmatrix reads), and dbeta = X . U / beta.  A warp takes 8 tokens.
   {
@@ -767,8 +748,7 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
         float x[2], m[2], left[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const float e =
-              j + z <= i ? expf((Gh[i] - Gh[j + z]) + (Gl[i] - Gl[j + z])) : 0.f;
+          const float e = j + z <= i ? decay(G[i], G[j + z]) : 0.f;
           x[z] = j + z <= i && i < c.len ? a.scale * e * dp[q][2 * y + z] : 0.f;
           left[z] = x[z] - __bfloat162float(__float2bfloat16_rn(x[z]));
           m[z] = j + z < i ? -e * dl[q][2 * y + z] : 0.f;
@@ -784,8 +764,8 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     const int i = m0 + row + 8 * y;
-    gi[y] = expf(Gh[i] + Gl[i]);
-    re[y] = expf((Gh[kC - 1] - Gh[i]) + (Gl[kC - 1] - Gl[i]));
+    gi[y] = decay(G[i]);
+    re[y] = decay(G[kC - 1], G[i]);
   }
   const bool with_e = half == 1;
   // this warp's rows of U in two parts, or of dO and dV: they stay in registers

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kChunkThreads)
   // fp32 blocks over the tiles once the products are taken: L21, and the
   // transposes of L11, L22; T11, T22, L21 T11, T21
   float* fb = reinterpret_cast<float*>(smem);
-  __shared__ double G[kC];
+  __shared__ float2 G[kC];
   __shared__ float beta[kC];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t slot = blockIdx.x;
@@ -98,21 +98,8 @@ __global__ void __launch_bounds__(kChunkThreads)
     cp16(smem_u32(sQ) + sw(kC, row, col), a.Q + t * a.ldq + hk * D + col, ok);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
-  if (warp == 0) {  // running sums of the log decays, in fp64: differences of far sums stay exact
-    double x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = 2 * lane + i;
-      const float g = j < c.len ? a.g[(c.t0 + j) * a.H + h] : 0.f;
-      x[i] = g < -1e4f ? -1e4 : (double)g;  // e^-1e4 is 0 like e^-inf, but its sums are numbers
-    }
-    double s = x[0] + x[1];
-    for (int m = 1; m < 32; m *= 2) {
-      const double o = __shfl_up_sync(0xffffffffu, s, m);
-      if (lane >= m) s += o;
-    }
-    G[2 * lane] = s - x[1];
-    G[2 * lane + 1] = s;
+  if (warp == 0) {
+    sum_decays(a.g, c.t0, c.len, a.H, h, lane, G);
   } else if (warp == 1) {
     for (int j = lane; j < kC; j += 32) {
       float b = j < c.len ? a.b[(c.t0 + j) * a.H + h] : 0.f;
@@ -152,24 +139,27 @@ __global__ void __launch_bounds__(kChunkThreads)
   float *L21 = fb, *Lt1 = fb + 32 * kLS, *Lt2 = fb + 2 * 32 * kLS, *T1 = fb + 3 * 32 * kLS,
         *T2 = fb + 4 * 32 * kLS, *Z = fb + 5 * 32 * kLS;
 #pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
+  for (int nt = 0; nt < 8; ++nt) {
+    if (nt > 2 * warp + 1) break;  // above the diagonal
+    const int j = nt * 8 + 2 * (lane % 4);
+    const float2 Gj[2] = {G[j], G[j + 1]};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (nt > 2 * warp + 1) break;  // above the diagonal
-      const int i = m0 + lane / 4 + 8 * half, j = nt * 8 + 2 * (lane % 4);
-      float p[2];
+      const int i = m0 + lane / 4 + 8 * half;
+      const float2 Gi = G[i];
+      const float b = beta[i];
+      float p[2], l[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float e = j + x <= i ? expf((float)(G[i] - G[j + x])) : 0.f;
+        const float e = j + x <= i ? decay(Gi, Gj[x]) : 0.f;
         p[x] = j + x <= i ? a.scale * e * qk[nt][2 * half + x] : 0.f;
-        const float l = j + x < i ? beta[i] * e * kk[nt][2 * half + x] : 0.f;
-        if (i < 32) {
-          if (j + x < 32) Lt1[(j + x) * kLS + i] = l;
-        } else if (j + x < 32) {
-          L21[(i - 32) * kLS + j + x] = l;
-        } else {
-          Lt2[(j + x - 32) * kLS + i - 32] = l;
-        }
+        l[x] = j + x < i ? b * e * kk[nt][2 * half + x] : 0.f;
+      }
+      if (nt < 4 && warp >= 2) {
+        *reinterpret_cast<float2*>(L21 + (i - 32) * kLS + j) = make_float2(l[0], l[1]);
+      } else {
+        float* to = nt < 4 ? Lt1 + j * kLS + i : Lt2 + (j - 32) * kLS + i - 32;
+        to[0] = l[0], to[kLS] = l[1];
       }
       uint32_t* dst = reinterpret_cast<uint32_t*>(outP + tri(i, j));
       if (GRAD) {
@@ -182,6 +172,7 @@ __global__ void __launch_bounds__(kChunkThreads)
         dst[0] = pack_bf16x2(p[0], p[1]);
       }
     }
+  }
   __syncthreads();
 
   // (I + L)^-1 by halves: the two diagonal blocks by substitution (a thread
@@ -207,8 +198,8 @@ __global__ void __launch_bounds__(kChunkThreads)
   } else if (warp == 2) {  // gates
     float* gates = reinterpret_cast<float*>(out + (3 + (GRAD ? 3 : 1)) * kTri);
     for (int j = lane; j < kC; j += 32) {
-      gates[j] = expf((float)G[j]);
-      gates[kC + j] = expf((float)(G[kC - 1] - G[j]));
+      gates[j] = decay(G[j]);
+      gates[kC + j] = decay(G[kC - 1], G[j]);
       gates[2 * kC + j] = beta[j];
     }
   }
