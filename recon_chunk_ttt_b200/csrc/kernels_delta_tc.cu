@@ -70,7 +70,7 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
 }
 
 template <int D, bool GRAD>
-__global__ void __launch_bounds__(kChunkThreads)
+__global__ void __launch_bounds__(kChunkThreads, D == 256 ? 0 : 5)
     delta_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
