@@ -12,10 +12,21 @@ namespace {
 // ----------------------------------------------------------------------------
 // The chain over a sequence's chunks: one block's part.
 //
-// KS warps share 16 rows of S, D / KS columns each; a block has RG such groups.
-// The partial products S K^T, S Q^T are added through shared memory, each warp
-// takes its share of the tokens through r, u and o, and gets the others' u for
-// its columns of S: three meetings a step.
+// It works on the transposes: a group of KS warps owns 16 rows of S in registers, D / KS
+// columns each, as accumulators, whose layout is that of an A operand; rows of S never
+// meet, so blocks do not either.  A step: every warp forms its columns' share of S K^T and
+// S Q^T; the shares are added through shared memory, each warp takes its share of the
+// tokens through r = beta (v - ..), u = r T^T and o, and gets the others' u for its columns
+// of S: three meetings, by mbarrier, within a group.  (tcgen05 takes 64 or 128 rows: too
+// few blocks for the GPU, and every intermediate would go from tensor memory through
+// registers to shared memory and back, three times a step, on the path that nothing
+// overlaps.)  K, Q, V tiles come by TMA and T, P, gates by one bulk copy, ST chunks deep.
+//
+// The state is fp32 in and out, so operands that are not bf16 by nature (S, T, r, u) enter
+// as three bf16 parts, of whose products those above 2^-24 are taken: S K^T and U^T K three
+// each (K is exact), T six.  O is rounded to bf16 in the end: two parts of S and U, one of
+// P (2^-9, a bf16 operand's rounding, next to O's own); for the gradient, whose decays take
+// dO . O in fp32, all three.
 // The tensor cores cut an accumulator's last bits off with every product they
 // add to it (measured: 1 + 0.75 ulp stays 1), so small parts are summed apart
 // from large ones, and the state takes one fp32 addition a chunk.
@@ -184,8 +195,8 @@ __device__ __forceinline__ void delta_state_chain(const CUtensorMap& mQ, const C
                                          (int64_t)D * D, s, ((r0 / 16) * KS + kw) * (DK / 8), lane);
     }
 
-    // r = S K^T (three parts of S), o = S Q^T (two; for the gradient three), both [16 rows x 64 tokens], over this
-    // warp's columns of S.  The parts of r are sent off before the turn to o.
+    // r = S K^T (three parts of S), o = S Q^T (two; for the gradient three), both [16 rows x
+    // 64 tokens], over this warp's columns of S.  The shares of r are sent off before o's turn.
     uint32_t sh[DK / 16][4], sm[DK / 16][4], sl[GRAD ? DK / 16 : 1][4];
     float rt[NT][4], ot[NT][4];  // this warp's tiles of the group's sums
     {

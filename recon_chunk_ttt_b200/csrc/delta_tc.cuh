@@ -281,7 +281,5 @@ struct DeltaKept {
 
 // Inverses, P and gates of every chunk into `blocks` (kernels_delta_tc.cu).
 cudaError_t delta_prepare(const DeltaArgs& a, bool gradient, uint8_t* blocks, cudaStream_t st);
-// Which form of the chain's kernels a call takes (both directions the same).
-bool delta_few_rows(const DeltaArgs& a);
 
 }  // namespace ttt

@@ -11,14 +11,18 @@
 // changes from token to token by dO_t . O_t - dV_t . V_t alone, so it is a running sum
 // from the end, started anew from a product of the two states every 512 tokens.
 //
-// Four kernels: the inverses of all chunks; the forward chain once more, which
-// keeps each chunk's state and U (in bf16, U in two parts: they only enter dQ and
-// dK, which are bf16) and the sums of dO . O; delta_reverse_kernel, the chain of E from
-// the last chunk to the first; delta_tokens_grad_kernel, dQ and dK of all chunks
-// at once, and the running sums; where heads share a key head a fifth adds their
-// shares.  The chains carry fp32 in three bf16 parts
-// (the gates' gradients and dS are fp32 results), the rest is bf16 products
-// summed in fp32.
+// Three kernels: the inverses of all chunks; delta_chains_kernel, the forward chain once more
+// (which keeps the state before each chunk in bf16, as it only enters dQ and dK, and U and
+// dO . O in fp32) and beside it the chain of E from the last chunk to the first (which keeps
+// E likewise, and X and dV . V); delta_tokens_grad_kernel, dQ, dK and dbeta of all chunks at
+// once, and the running sums.  Where heads share a key head a fourth adds their shares.  The
+// chains carry fp32 in three bf16 parts (the gates' gradients and dS are fp32 results), the
+// rest is bf16 products summed in fp32.
+//
+// Bound as the forward pass is by the chain (one frame of 1,374 tokens, 4 heads of 256: 95 us
+// of 137), and where there are enough chains to fill the GPU by how many of them an SM holds
+// (16,411 tokens in 13 sequences, 16 heads of 128: 1.07 ms of 1.57; two a SM, the tensor
+// cores busy for 39% of the time).
 
 #include "delta_state.cuh"
 
@@ -558,13 +562,17 @@ __device__ __forceinline__ void gate_stretch(const GateArgs& a, const int64_t* o
 }
 
 // ----------------------------------------------------------------------------
-// delta_tokens_grad_kernel: dQ and dK of one chunk and head.  8 warps: 4 blocks
-// of 16 tokens; of the two warps of a block one takes the products with S (dQ's, and
-// dV S, which it hands over), the other those with E (dK's).  dO, U, dV stay in
-// shared memory; S, E, Q, K pass in strips of 16 columns, two deep, and two blocks
-// share an SM (d = 256: one).  U and A enter in two parts: with one each, dK is off
-// by 3.0e-3 and dQ by 2.7e-3 of which 1.7e-3 are the results' own rounding; so 2.4e-3
-// and 2.1e-3.  Two parts of S, E, dV as well would leave 1.9e-3 for twice the traffic.
+// delta_tokens_grad_kernel: dQ, dK and dbeta of one chunk and head.  8 warps: 4 blocks of 16
+// tokens; of the two warps of a block one takes the products with S (dQ, and for dK dV S and
+// A^T Q, which it hands over), the other those with E and M (dK).  They hold dO and dV, or U,
+// of their tokens in registers; S, E, Q, K pass in strips of 16 columns, as many ahead as
+// shared memory holds.  Two blocks share an SM (d = 256: one).
+//
+// U and A enter in two parts: with one each, dK is off by 3.0e-3 and dQ by 2.7e-3 of which
+// 1.7e-3 are the results' own rounding; so 2.4e-3 and 2.1e-3.  Two parts of S, E, dV as well
+// would leave 1.9e-3 for twice the traffic.
+// 4,320 chunks and heads of d = 128: 358 us, 1.04 GB (161 us); half of the rest is a block's
+// start, U, X and dO on their way and A and M formed, with one other block to fill it.
 // ----------------------------------------------------------------------------
 template <int D>
 struct GK {
@@ -1028,7 +1036,11 @@ cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, co
                          dS_in, static_cast<__nv_bfloat16*>(dV), halves(p.E),
                          floats(p.X), floats(p.anchors_e), last_e,
                          floats(p.dots_v), device_error_ptr()};
-  const bool few = delta_few_rows(a);
+  // Two stages of copies and all registers, or two blocks an SM: the first where every chain
+  // has an SM (1,374 tokens, 4 heads of 128: 70 us against 84), the second from there on (16
+  // heads: 111 us against 131; 16,411 tokens in 13 sequences: 1,061 against 1,284).  A block
+  // of d = 256 fills an SM.
+  const bool few = 2 * a.seqs * a.H * (a.d / 16) <= num_sms();
   e = a.d == 64    ? few ? launch_chains<64, 2>(a, x, f, r, st) : launch_chains<64, 1>(a, x, f, r, st)
       : a.d == 128 ? few ? launch_chains<128, 2>(a, x, f, r, st) : launch_chains<128, 1>(a, x, f, r, st)
                    : launch_chains<256, 2>(a, x, f, r, st);

@@ -7,20 +7,12 @@
 //   S <- gamma_64 S + U^T (rest K),      rest_j = e^(G_64 - G_j)
 // T = (I + L)^-1 and P need no state: delta_chunk_kernel forms them for all
 // chunks at once.  What is left is a chain over the chunks of a sequence, and
-// delta_state_kernel makes its step short.  It works on the transposes: a warp
-// owns 16 rows of S in registers, as accumulators, whose layout is that of an
-// A operand: S K^T, then (beta ..)^T T^T, then U^T K all read the result before
-// them from registers, with no trip through shared memory and no barrier
-// between warps.  (A tcgen05 tile would take 64 or 128 rows and carry every
-// intermediate from tensor memory through registers to shared memory and back,
-// three times a step, on the one path that cannot be overlapped.)
-// K, Q, V tiles come by TMA and T, P, gates by one bulk copy, two chunks deep.
+// delta_state_chain (delta_state.cuh) makes its step short.
 //
-// The state is fp32 in and out, so operands that are not bf16 by nature (S, T,
-// the right-hand side, U) enter as three bf16 parts, of whose products those
-// above 2^-24 are taken: S K^T and U^T K three each (K is exact), T six.  O is
-// rounded to bf16 in the end: two parts of S and U, one of P (2^-9, a bf16
-// operand's rounding, next to O's own).
+// Bound by that chain, not by memory or by the tensor cores: a step of 64 tokens takes
+// 3.0 us at d = 256 (2.7 us at 128), of which the products are 1.2 us; the rest is the
+// latency of one product's result on its way to be the next one's operand.  (137,400
+// tokens, 4 heads of 256: 2,147 steps, 6.4 ms; the bytes alone would be 0.18 ms.)
 
 #include "delta_state.cuh"
 
@@ -28,7 +20,11 @@ namespace ttt {
 namespace {
 
 // ----------------------------------------------------------------------------
-// delta_chunk_kernel: T, P and the gates of one chunk and head.
+// delta_chunk_kernel: T, P and the gates of one chunk and head.  The inverse is fp32 on
+// CUDA cores (its entries multiply up, so L's rounding would too).  Bound by its own
+// instructions and shared memory, about a third in the decays and triangles, a fifth each
+// in the substitution and the two products: 95 us for 4,320 chunks and heads of d = 128
+// (0.15 GB, 23 us); it is 4% of a long sequence's time and a fifth of a packed batch's.
 // ----------------------------------------------------------------------------
 constexpr int kChunkThreads = 128;
 constexpr int kLS = 36;  // row length of the 32 x 32 fp32 blocks: 16-byte rows, spread over banks
@@ -48,8 +44,8 @@ struct ChunkArgs {
 };
 
 // The sequences from the longest to the shortest, equal ones as they come: a chain's
-// time is its length, so the longest has to start first (16,411 tokens in 13 sequences,
-// the longest last: 457 us; first: 340 us).
+// time is its length, so the longest has to start first (16,411 tokens in 13 sequences, the
+// longest last, 16 heads of 128: 602 us as they come, 512 us from the longest).
 __device__ __forceinline__ void rank_sequences(const ChunkArgs& a, int64_t* len, int tid) {
   for (int i = tid; i < a.seqs; i += kChunkThreads) {
     const SeqRange s = seq_range(a.offsets, a.n, i);
@@ -70,6 +66,7 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
 }
 
 template <int D, bool GRAD>
+// (five blocks an SM, for d = 256 the three that its tiles allow: 95 us against 100 us for four)
 __global__ void __launch_bounds__(kChunkThreads, D == 256 ? 0 : 5)
     delta_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -321,7 +318,12 @@ cudaError_t delta_tc(const DeltaArgs& a, const float* S_in, float* S_out, void* 
   uint8_t* blocks = static_cast<uint8_t*>(ws) + kOrderBytes;
   const cudaError_t e = delta_prepare(a, false, blocks, st);
   if (e != cudaSuccess) return e;
-  const bool few = delta_few_rows(a);
+  // Groups of 16 rows of S.  Where there are no more of them than SMs, four warps share each,
+  // one on each quarter of an SM (1,374 tokens, 4 heads of 128: 60 us against 95 us); else two
+  // do, with half the exchange for each product, and four groups share an SM (16,411 tokens in
+  // 13 sequences, 16 heads of 128: 511 us against 551 us; 14,000 tokens in 20 sequences, 16
+  // heads of 64: 142 us against 220 us).
+  const bool few = a.seqs * a.H * (a.d / 16) <= num_sms();
   if (a.d == 64)
     return few ? launch_state<64, 4, 1, 2>(a, S_in, S_out, O, blocks, st)
                : launch_state<64, 2, 2, 1>(a, S_in, S_out, O, blocks, st);
@@ -330,11 +332,5 @@ cudaError_t delta_tc(const DeltaArgs& a, const float* S_in, float* S_out, void* 
                : launch_state<128, 2, 2, 1>(a, S_in, S_out, O, blocks, st);
   return launch_state<256, 4, 1, 2>(a, S_in, S_out, O, blocks, st);
 }
-
-// Groups of 16 rows of S.  Where there are no more of them than SMs, four warps
-// share each (one on each quarter of an SM: 74 us against 97 us for a 1,374-token
-// sequence of 4 heads of 256); else two do, with half the exchange for each product
-// (16,411 tokens, 13 sequences, 16 heads of 128: 457 us against 596 us).
-bool delta_few_rows(const DeltaArgs& a) { return a.seqs * a.H * (a.d / 16) <= num_sms(); }
 
 }  // namespace ttt

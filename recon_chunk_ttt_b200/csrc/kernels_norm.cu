@@ -4,7 +4,7 @@
 //
 // Bound by memory: forward reads x and writes y, backward reads x and dy and
 // writes dx, each once.  A row lies in the registers of a group of threads
-// (1, 4 or 16 warps), so the mean, then the squares about the mean, then
+// (8 lanes, 1, 4, 8 or 16 warps), so the mean, then the squares about the mean, then
 // the result are taken from one read.  In the backward kernel a thread keeps
 // its columns' sums of dy and dy xh in registers over all rows of its block;
 // the blocks' sums meet in the workspace and a second kernel adds them in
