@@ -54,7 +54,8 @@
  *        shadow : bf16 copies of Ŵ for the tensor-core apply, in the same
  *                 layout as W1, W3, W2 (W1 block, then W3, then W2);
  *                 ttt_shadow_bytes() bytes.
- *  - Device pointers must be 16-byte aligned (tensor-memory-access rule).
+ *  - Device pointers must be 16-byte aligned (tensor-memory-access rule), where
+ *    an entry point does not say less.
  *  - Supported shapes: (d, hidden) = (64, 128) or (256, 512), heads >= 1
  *    (linear mode: (64, 64) or (256, 256)).
  *  - n = 0 or eta = 0 gives Ŵ = W.  Outputs may alias the weight inputs
@@ -337,15 +338,19 @@ ttt_status ttt_stream_step_static(const ttt_config* cfg,
  *   gradients) that belong to no sequence are left as they are.  Offsets that
  *   decrease or leave 0..n are clamped and reported in the device error word
  *   (TTT_DEVICE_ERR_OFFSETS); the outputs are then undefined.
+ *   n up to 2^30; up to 65,535 sequences or requests; up to 4,096 heads.
+ *   log_decay, beta, their gradients and slots: 4-byte aligned; offsets: 8.
+ *   Rows of no sequence may hold anything; an infinity or NaN in a sequence
+ *   reaches, besides all tokens behind it, up to 63 tokens before it.
  *
  * ttt_delta_chunk: all tokens of every sequence.  S_in: float
  *   [seqs][heads][d][d] or NULL (zeros); S_out: the states after the last
  *   tokens, or NULL; it may be S_in (in place).  An empty sequence hands its
  *   state on.  O: [n][heads*d] dense, token type.
  *   BF16_TC: chunks of 64 tokens on the tensor cores, the state and every sum
- *   in fp32 (operands that are not bf16 by nature go in as a bf16 pair hi +
- *   lo, so the state keeps 16 bits and more).  FP32_CHECK: token by token in
- *   fp32 on CUDA cores.
+ *   in fp32 (operands that are not bf16 by nature go in as three bf16 parts,
+ *   24 bits); short sequences, and FP32_CHECK: token by token in fp32 on CUDA
+ *   cores.
  * ttt_delta_step: one token for each of tok->n requests (tok->seqs = n,
  *   tok->offsets = NULL) on a pool of `pool` states float
  *   [pool][heads][d][d]: request i works on S[slots[i]] (slots: device int32
@@ -362,8 +367,9 @@ ttt_status ttt_stream_step_static(const ttt_config* cfg,
  *   Nothing is kept from the forward call: it is recomputed in the workspace.
  *
  * Outputs alias no input except where said.  Workspace bytes:
- * ttt_delta_workspace_bytes(cfg, n, seqs, backward); 0 for an invalid config.
- * Results are the same from run to run.
+ * ttt_delta_workspace_bytes(cfg, n, seqs, backward); 0 where a call needs none
+ * (short ones) and for an invalid config.  Nothing in it has to start at zero
+ * or outlives the call.  Results are the same from run to run.
  */
 typedef struct {
   int32_t heads;
@@ -419,6 +425,7 @@ ttt_status ttt_delta_backward(const ttt_delta_config* cfg, const ttt_delta_token
  *    FREQ_HEAD every pair still uses its own axis' base.
  *  - positions: float [n][3] (whole numbers are exact to 2^24); fractions and
  *    negative positions are fine.  A position of infinity or NaN gives NaN.
+ *    4-byte aligned.  n up to 2^30, up to 4,096 heads of q and of k.
  *  - Q: rows of q_heads*d values ldq apart, Q_out likewise ldq_out; K, K_out
  *    too, or k_heads = 0 with K = K_out = NULL.  Rows a multiple of 16 bytes
  *    apart.  Q_out may be Q and K_out K (in place, same row distance).
@@ -453,7 +460,9 @@ ttt_status ttt_rope(const ttt_rope_config* cfg, const void* Q, int64_t ldq, int3
  *   sizes only.  dX is NULL or not, at least one output is wanted.  Rows = 0
  *   gives dweight = dbias = 0.  Workspace: ttt_norm_workspace_bytes(cfg, rows)
  *   (needed for dweight or dbias).
- *  - dim 1 .. 65536; eps >= 0, finite.  ldx, lddy >= dim, any value.
+ *  - dim 1 .. 65536; eps >= 0, finite.  ldx, lddy >= dim, any value (rows that
+ *    are multiples of 16 bytes, and so far apart, are faster).  Up to 2^30
+ *    rows.  stats: 4-byte aligned.
  */
 typedef struct {
   int64_t dim;

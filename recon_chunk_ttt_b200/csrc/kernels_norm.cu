@@ -8,7 +8,9 @@
 // the result are taken from one read.  In the backward kernel a thread keeps
 // its columns' sums of dy and dy xh in registers over all rows of its block;
 // the blocks' sums meet in the workspace and a second kernel adds them in
-// their order (no atomics).
+// their order (no atomics).  Of the measured copy rate, bf16 rows of 1,024: forward 80%,
+// backward 76% (137,400 rows, 180 us); fp32 85 to 100%.  Rows that are not whole 16-byte
+// vectors are loaded value by value: 24 to 48% in bf16, 65% in fp32 (20,011 rows of 1,153: 44 us).
 
 #include <cuda_bf16.h>
 
