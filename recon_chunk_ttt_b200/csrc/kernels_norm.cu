@@ -58,6 +58,12 @@ struct Ld<__nv_bfloat16, 8> {
   }
 };
 template <>
+struct Ld<__nv_bfloat16, 2> {
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x[0], x[1]);
+  }
+};
+template <>
 struct Ld<__nv_bfloat16, 1> {
   static __device__ __forceinline__ void get(const __nv_bfloat16* p, float* x) {
     x[0] = __bfloat162float(*p);
@@ -83,6 +89,17 @@ struct Raw {
         x[i] = __uint_as_float(w[i]);
       }
     }
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void get(const __nv_bfloat16* p) {
+    v = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ void none() { v = 0; }
+  __device__ __forceinline__ void unpack(float* x) const {
+    x[0] = __uint_as_float(v << 16), x[1] = __uint_as_float(v & 0xffff0000u);
   }
 };
 template <typename T>
@@ -154,6 +171,9 @@ template <int V>
 __device__ __forceinline__ void get_f(const float* p, float* x) {
   if (V == 1) {
     x[0] = *p;
+  } else if (V == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x, x[V - 1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += 4) Ld<float, 4>::get(p + i, x + i);
@@ -553,9 +573,12 @@ __global__ void __launch_bounds__(1024)
 struct Shape {
   int V, G, NV, R;
 };
-int vector_of(const NormArgs& a, bool aligned) {
-  const int full = a.bf16 ? 8 : 4;
-  return aligned && a.dim % full == 0 ? full : 1;
+// Values loaded at once: 16 bytes where rows are whole vectors of that and start on them, two
+// bf16 values where rows are even, else single ones.
+int full_vector(const NormArgs& a) { return a.bf16 ? 8 : 4; }
+int vector_of(const NormArgs& a, int64_t ld1, int64_t ld2) {
+  const int64_t x = a.dim | ld1 | ld2;  // the pointers are 16-byte aligned, checked at the entry
+  return x % full_vector(a) == 0 ? full_vector(a) : a.bf16 && x % 2 == 0 ? 2 : 1;
 }
 int pow2_at_least(int64_t x) {
   int p = 1;
@@ -563,8 +586,8 @@ int pow2_at_least(int64_t x) {
   return p;
 }
 // At most 16 values a thread (32 in the largest group, forward).
-Shape shape_of(const NormArgs& a, bool aligned, bool forward) {
-  Shape s = {vector_of(a, aligned), 0, 0, 1};
+Shape shape_of(const NormArgs& a, int V, bool forward) {
+  Shape s = {V, 0, 0, 1};
   const int64_t nv = a.dim / s.V;
   const int most = 16 / s.V, last = forward ? 2 * most : most;
   // 8 lanes up to 64 values: a warp would leave three quarters of its lanes without
@@ -578,11 +601,6 @@ Shape shape_of(const NormArgs& a, bool aligned, bool forward) {
   s.NV = pow2_at_least((nv + s.G - 1) / s.G);
   s.R = rows_at_once(s.G, s.NV, s.V, !forward && !a.bf16);
   return s;
-}
-
-bool vector_rows(const NormArgs& a, int64_t ldx, int64_t ldy) {
-  const int full = a.bf16 ? 8 : 4;  // the pointers are 16-byte aligned, checked at the entry
-  return ldx % full == 0 && ldy % full == 0;
 }
 
 // Blocks of the kernels (and the rows of the backward kernel's partial sums).
@@ -670,8 +688,9 @@ cudaError_t backward_by_g(const Shape& s, const NormArgs& a, const Backward& b, 
 size_t norm_workspace_bytes(const NormArgs& a) {
   // the largest of the plans that strides may ask for
   size_t most = (size_t)wide_blocks(a);
-  for (int aligned = 0; aligned < 2; ++aligned) {
-    const Shape s = shape_of(a, aligned != 0, false);
+  for (int V : {1, 2, full_vector(a)}) {
+    if (a.dim % V != 0) continue;
+    const Shape s = shape_of(a, V, false);
     if (s.G != 0 && (size_t)blocks_of(a, s, false) > most) most = (size_t)blocks_of(a, s, false);
   }
   return most * 2 * (size_t)a.dim * 4;
@@ -680,7 +699,7 @@ size_t norm_workspace_bytes(const NormArgs& a) {
 cudaError_t norm_forward(const NormArgs& a, const void* X, int64_t ldx, const float* w,
                          const float* b, void* Y, float* stats, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
-  const Shape s = shape_of(a, vector_rows(a, ldx, a.dim), true);
+  const Shape s = shape_of(a, vector_of(a, ldx, a.dim), true);
   TraceScope ts("layer_norm", st);
   if (s.G == 0) {
     if (a.bf16)
@@ -695,8 +714,9 @@ cudaError_t norm_forward(const NormArgs& a, const void* X, int64_t ldx, const fl
   }
   const Forward f = {X, ldx, w, b, Y, stats, blocks_of(a, s, true)};
   if (a.bf16)
-    return s.V == 8 ? forward_by_g<__nv_bfloat16, 8>(s, a, f, st)
-                    : forward_by_g<__nv_bfloat16, 1>(s, a, f, st);
+    return s.V == 8   ? forward_by_g<__nv_bfloat16, 8>(s, a, f, st)
+           : s.V == 2 ? forward_by_g<__nv_bfloat16, 2>(s, a, f, st)
+                      : forward_by_g<__nv_bfloat16, 1>(s, a, f, st);
   return s.V == 4 ? forward_by_g<float, 4>(s, a, f, st) : forward_by_g<float, 1>(s, a, f, st);
 }
 
@@ -710,7 +730,7 @@ cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const v
     if (e == cudaSuccess && db != nullptr) e = cudaMemsetAsync(db, 0, (size_t)a.dim * 4, st);
     return e;
   }
-  const Shape s = shape_of(a, vector_rows(a, ldx, lddy), false);
+  const Shape s = shape_of(a, vector_of(a, ldx, lddy), false);
   float* part = cols ? static_cast<float*>(ws) : nullptr;
   cudaError_t e = cudaSuccess;
   int blocks;
@@ -743,8 +763,9 @@ cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const v
     TraceScope ts("layer_norm_backward", st);
     const Backward b = {X, ldx, dY, lddy, w, stats, dX, part, blocks};
     if (a.bf16)
-      e = s.V == 8 ? backward_by_g<__nv_bfloat16, 8>(s, a, b, st)
-                   : backward_by_g<__nv_bfloat16, 1>(s, a, b, st);
+      e = s.V == 8   ? backward_by_g<__nv_bfloat16, 8>(s, a, b, st)
+          : s.V == 2 ? backward_by_g<__nv_bfloat16, 2>(s, a, b, st)
+                     : backward_by_g<__nv_bfloat16, 1>(s, a, b, st);
     else
       e = s.V == 4 ? backward_by_g<float, 4>(s, a, b, st) : backward_by_g<float, 1>(s, a, b, st);
   }

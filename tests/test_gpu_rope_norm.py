@@ -381,3 +381,23 @@ def test_all_in_a_row():
         o = R.ttt_delta_step(dc, qt, kt, vt, gate[t:t + 1], beta[t:t + 1], st)
         assert rel(o, out[t:t + 1].detach()) <= tol
     assert rel(st, S.double().cpu()) <= tol
+
+
+@pytest.mark.parametrize("dim", [6, 34, 66, 258, 1154, 4098, 8190, 16386])
+def test_norm_rows_of_pairs(dim):
+    """bf16 rows that are even but no whole 16-byte vectors; rows that are, apart
+    by an even distance."""
+    test_norm(dim, 2, BF)
+    test_norm_backward(dim, 50, BF)
+    test_norm_backward(dim, 3001, BF)
+    rows, whole = 65, dim // 8 * 8 + 8
+    x = torch.randn(rows, whole + 2, device="cuda", dtype=torch.bfloat16)[:, :whole]
+    dy = torch.randn(rows, whole + 6, device="cuda", dtype=torch.bfloat16)[:, :whole]
+    w = torch.randn(whole, device="cuda")
+    cfg = R.make_norm_config(whole)
+    Y, st = R.ttt_layer_norm(cfg, x, w)
+    Yd, _ = R.ttt_layer_norm(cfg, x.contiguous(), w)
+    assert (Y.double() - Yd.double()).norm() <= 2.0 ** -8 * Yd.double().norm()
+    got = R.ttt_layer_norm_backward(cfg, x, dy, st, w)
+    for a, c in zip(got, _norm_grads(x, dy, w, 1e-5)):
+        assert (a.double() - c).norm() <= (2.0 ** -8 if a.dtype == torch.bfloat16 else 1e-5) * c.norm()
