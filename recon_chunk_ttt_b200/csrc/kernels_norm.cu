@@ -580,10 +580,15 @@ int vector_of(const NormArgs& a, int64_t ld1, int64_t ld2) {
   const int64_t x = a.dim | ld1 | ld2;  // the pointers are 16-byte aligned, checked at the entry
   return x % full_vector(a) == 0 ? full_vector(a) : a.bf16 && x % 2 == 0 ? 2 : 1;
 }
-int pow2_at_least(int64_t x) {
-  int p = 1;
-  while (p < x) p *= 2;
-  return p;
+// Vectors a thread may hold: 1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 32.  (Powers of two alone left up to
+// half empty: 20,011 rows of 1,153 floats 45 us, so 34 us; backward 72 us and 56 us.)
+constexpr int next_nv(int nv) {
+  return nv < 6 ? nv + 1 : nv < 8 ? 8 : nv < 12 ? nv + 2 : nv < 16 ? 16 : 32;
+}
+int nv_at_least(int64_t x) {
+  int nv = 1;
+  while (nv < x) nv = next_nv(nv);
+  return nv;
 }
 // At most 16 values a thread (32 in the largest group, forward).
 Shape shape_of(const NormArgs& a, int V, bool forward) {
@@ -598,7 +603,7 @@ Shape shape_of(const NormArgs& a, int V, bool forward) {
         : nv <= 512 * last                         ? 512
                                                    : 0;
   if (s.G == 0) return s;
-  s.NV = pow2_at_least((nv + s.G - 1) / s.G);
+  s.NV = nv_at_least((nv + s.G - 1) / s.G);
   s.R = rows_at_once(s.G, s.NV, s.V, !forward && !a.bf16);
   return s;
 }
@@ -628,11 +633,10 @@ cudaError_t launch_forward(const NormArgs& a, const Forward& f, cudaStream_t st)
       static_cast<T*>(f.Y), f.stats);
   return cudaGetLastError();
 }
-// NV = 1, 2, 4, .. MOST
 template <typename T, int V, int G, int MOST, int NV = 1>
 cudaError_t forward_by_nv(int nv, const NormArgs& a, const Forward& f, cudaStream_t st) {
   if constexpr (NV < MOST)
-    if (nv > NV) return forward_by_nv<T, V, G, MOST, 2 * NV>(nv, a, f, st);
+    if (nv > NV) return forward_by_nv<T, V, G, MOST, next_nv(NV)>(nv, a, f, st);
   return launch_forward<T, V, G, NV>(a, f, st);
 }
 template <typename T, int V>
@@ -671,7 +675,7 @@ cudaError_t launch_backward(const NormArgs& a, const Backward& b, cudaStream_t s
 template <typename T, int V, int G, int MOST, int NV = 1>
 cudaError_t backward_by_nv(int nv, const NormArgs& a, const Backward& b, cudaStream_t st) {
   if constexpr (NV < MOST)
-    if (nv > NV) return backward_by_nv<T, V, G, MOST, 2 * NV>(nv, a, b, st);
+    if (nv > NV) return backward_by_nv<T, V, G, MOST, next_nv(NV)>(nv, a, b, st);
   return launch_backward<T, V, G, NV>(a, b, st);
 }
 template <typename T, int V>
