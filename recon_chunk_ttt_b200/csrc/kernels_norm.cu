@@ -8,9 +8,10 @@
 // the result are taken from one read.  In the backward kernel a thread keeps
 // its columns' sums of dy and dy xh in registers over all rows of its block;
 // the blocks' sums meet in the workspace and a second kernel adds them in
-// their order (no atomics).  Of the measured copy rate, bf16 rows of 1,024: forward 80%,
-// backward 76% (137,400 rows, 180 us); fp32 85 to 100%.  Rows that are not whole 16-byte
-// vectors are loaded value by value: 24 to 48% in bf16, 65% in fp32 (20,011 rows of 1,153: 44 us).
+// their order (no atomics).  Of the measured copy rate, bf16 rows of 1,024:
+// forward 79%, backward 76% (137,400 rows, 172 us); of 4,096 86% and 81%; fp32 75 to 100%.
+// Rows that are not whole 16-byte vectors go in pairs or one by one: 40 to 62% in bf16, 75 to
+// 90% in fp32.  Rows beyond the registers: forward 82%, backward 30%.
 
 #include <cuda_bf16.h>
 
@@ -202,11 +203,12 @@ constexpr int block_of(int G) { return G <= 32 ? 256 : G; }
 
 // Sums of N values over the G threads of a group at once; one barrier.
 constexpr int warps_of(int G) { return G < 32 ? 1 : G / 32; }
-// Rows a group takes at once: 32 values a thread; half of that where they are loaded
-// one by one (a register each), in the groups whose block has few registers a thread,
-// and where two arrays of floats are in flight.
-constexpr int rows_at_once(int g, int nv, int v, bool two_floats) {
-  const int r = (v == 1 || g > 128 || two_floats ? 16 : 32) / (nv * v);
+// Rows a group takes at once: 32 values a thread; half of that where they are loaded one by
+// one (a register each), in the groups whose block has few registers a thread, and where two
+// arrays of floats are in flight.  (34,000 rows of 4,096 in bf16, two rows of 256 threads
+// instead of one: forward 134 us and 102 us, backward 162 us and 194 us.)
+constexpr int rows_at_once(int g, int nv, int v, bool forward, bool floats) {
+  const int r = (v == 1 || g > (forward ? 256 : 128) || (!forward && floats) ? 16 : 32) / (nv * v);
   return r < 1 ? 1 : r > 4 ? 4 : r;
 }
 // Blocks of the backward kernel that an SM holds (128 registers a thread); the grid is
@@ -233,8 +235,7 @@ __device__ __forceinline__ void group_sums(float (&x)[N], float (*red)[warps_of(
 }
 
 // A group takes R rows at a time, whose sums share a barrier; the next R rows are
-// loaded meanwhile, and the weight and bias stay in registers.  (One row a block
-// and no more: 48 us for 20,011 rows of 1,153 floats.)
+// loaded meanwhile, and the weight and bias stay in registers.
 template <typename T, int V, int G, int NV, int R>
 __global__ void __launch_bounds__(block_of(G))
     norm_kernel(const T* X, int64_t ldx, int64_t rows, int dim, float eps,
@@ -604,7 +605,7 @@ Shape shape_of(const NormArgs& a, int V, bool forward) {
                                                    : 0;
   if (s.G == 0) return s;
   s.NV = nv_at_least((nv + s.G - 1) / s.G);
-  s.R = rows_at_once(s.G, s.NV, s.V, !forward && !a.bf16);
+  s.R = rows_at_once(s.G, s.NV, s.V, forward, !a.bf16);
   return s;
 }
 
@@ -628,7 +629,7 @@ struct Forward {
 };
 template <typename T, int V, int G, int NV>
 cudaError_t launch_forward(const NormArgs& a, const Forward& f, cudaStream_t st) {
-  norm_kernel<T, V, G, NV, rows_at_once(G, NV, V, false)><<<f.blocks, block_of(G), 0, st>>>(
+  norm_kernel<T, V, G, NV, rows_at_once(G, NV, V, true, sizeof(T) == 4)><<<f.blocks, block_of(G), 0, st>>>(
       static_cast<const T*>(f.X), f.ldx, a.rows, (int)a.dim, a.eps, f.w, f.b,
       static_cast<T*>(f.Y), f.stats);
   return cudaGetLastError();
@@ -660,7 +661,7 @@ struct Backward {
 };
 template <typename T, int V, int G, int NV>
 cudaError_t launch_backward(const NormArgs& a, const Backward& b, cudaStream_t st) {
-  constexpr int R = rows_at_once(G, NV, V, sizeof(T) == 4);
+  constexpr int R = rows_at_once(G, NV, V, false, sizeof(T) == 4);
   const auto go = [&](auto kernel, int smem) {
     kernel<<<b.blocks, block_of(G), smem, st>>>(static_cast<const T*>(b.X), b.ldx,
                                                 static_cast<const T*>(b.dY), b.lddy, a.rows,
