@@ -67,8 +67,9 @@ struct TokArgs {
 // S lies over LPR lanes, 4 or 8 columns each; a group of LPR lanes holds
 // kRows rows, so a step has kRows independent 16-byte loads a lane in flight
 // (8 KB a block): one-token calls are bound by the states' traffic, reading
-// and writing them once (96 requests, 32 heads of 128: 77 us, 81% of the measured copy rate).  S' k and S' q come from the same pass over S (o =
-// scale (S' q + u (k.q))), so a token has one reduction over lanes.
+// and writing them once (96 requests, 32 heads of 128: 77 us, 81% of the measured copy
+// rate).  S' k and S' q come from the same pass over S (o = scale (S' q + u (k.q))), so a
+// token has one reduction over lanes.
 // STEP: request i and every later one of the same slot, in order.
 // KEEP: the state before every kKeep-th token is written to `keep`.
 template <typename T, int D, bool STEP, bool KEEP>

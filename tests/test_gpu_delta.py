@@ -472,3 +472,32 @@ def test_offsets_without_an_entry():
                 torch.tensor([[0, 20]], device="cuda")):
         with pytest.raises(R.TTTError):
             R.ttt_delta_chunk(cfg, **x, offsets=bad)
+
+
+@pytest.mark.parametrize("lens,H,Hk,d", [([70] * 11, 8, 4, 64), ([3] * 515 + [90], 2, 1, 64),
+                                         ([1, 700, 64], 8, 8, 128)])
+def test_backward_of_many_chains(lens, H, Hk, d):
+    """More chains than SMs; more sequences than are ranked; heads of their own."""
+    test_backward(lens, H, Hk, d, BF, True)
+
+
+def test_two_calls_at_once():
+    """Forward and gradient on two streams at a time, each with its workspace."""
+    H, d, n = 4, 128, 900
+    cfg = R.make_delta_config(H, d)
+    data = [_inputs(50 + i, n, H, H, d, BF) for i in range(4)]
+    off = _offsets([400, 0, 500], 0)
+    S = [torch.stack([y[0] for _ in range(3)]) for _, y, _, _ in data]
+    want = [(R.ttt_delta_chunk(cfg, **x, S=s, offsets=off)
+             + R.ttt_delta_backward(cfg, **x, dO=dO, S=s, offsets=off))
+            for (x, _, dO, _), s in zip(data, S)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    for _ in range(3):
+        got = [(R.ttt_delta_chunk(cfg, **x, S=s, offsets=off, stream=st)
+                + R.ttt_delta_backward(cfg, **x, dO=dO, S=s, offsets=off, stream=st))
+               for (x, _, dO, _), s, st in zip(data, S, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+    R.ttt_check_device_error()
