@@ -11,7 +11,8 @@
 // their order (no atomics).  Of the measured copy rate, bf16 rows of 1,024:
 // forward 79%, backward 76% (137,400 rows, 172 us); of 4,096 86% and 81%; fp32 75 to 100%.
 // Rows that are not whole 16-byte vectors go in pairs or one by one: 40 to 62% in bf16, 75 to
-// 90% in fp32.  Rows beyond the registers: forward 82%, backward 30%.
+// 90% in fp32.  Rows beyond the registers (8,000 of 16,384, backward): 44% in
+// bf16, 54% in fp32.
 
 #include <cuda_bf16.h>
 
@@ -38,20 +39,10 @@ struct Ld<float, 4> {
 };
 template <>
 struct Ld<float, 1> {
-  static __device__ __forceinline__ void get(const float* p, float* x) { x[0] = *p; }
   static __device__ __forceinline__ void put(float* p, const float* x) { *p = x[0]; }
 };
 template <>
 struct Ld<__nv_bfloat16, 8> {
-  static __device__ __forceinline__ void get(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
   static __device__ __forceinline__ void put(__nv_bfloat16* p, const float* x) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
@@ -66,9 +57,6 @@ struct Ld<__nv_bfloat16, 2> {
 };
 template <>
 struct Ld<__nv_bfloat16, 1> {
-  static __device__ __forceinline__ void get(const __nv_bfloat16* p, float* x) {
-    x[0] = __bfloat162float(*p);
-  }
   static __device__ __forceinline__ void put(__nv_bfloat16* p, const float* x) {
     *p = __float2bfloat16_rn(x[0]);
   }
@@ -324,30 +312,48 @@ __global__ void __launch_bounds__(block_of(G))
 
 // Rows wider than the registers of a block: a block of 512 threads reads its row
 // three times (from the caches after the first).
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(512)
     norm_wide_kernel(const T* X, int64_t ldx, int dim, float eps, const float* __restrict__ w,
                      const float* __restrict__ b, T* Y, float* stats) {
   __shared__ float red[2][16];
   const int64_t row = blockIdx.x;
-  const T* x = X + row * ldx;
-  float sum = 0.f, sq = 0.f, e;
-  for (int c = threadIdx.x; c < dim; c += 512) {
-    Ld<T, 1>::get(x + c, &e);
-    sum += e;
+  const auto get = [&](int c, float* x) {
+    Raw<T, V> r;
+    r.get(X + row * ldx + c);
+    r.unpack(x);
+  };
+  float sum = 0.f, sq = 0.f, x[V], ww[V];
+#pragma unroll 4
+  for (int c = threadIdx.x * V; c < dim; c += 512 * V) {
+    get(c, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += x[i];
   }
   const float mean = group_sum<512>(sum, red[0]) / dim;
-  for (int c = threadIdx.x; c < dim; c += 512) {
-    Ld<T, 1>::get(x + c, &e);
-    sq = fmaf(e - mean, e - mean, sq);
+#pragma unroll 4
+  for (int c = threadIdx.x * V; c < dim; c += 512 * V) {
+    get(c, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sq = fmaf(x[i] - mean, x[i] - mean, sq);
   }
   const float rstd = 1.f / sqrtf(group_sum<512>(sq, red[1]) / dim + eps);
-  for (int c = threadIdx.x; c < dim; c += 512) {
-    Ld<T, 1>::get(x + c, &e);
-    e = (e - mean) * rstd;
-    if (w != nullptr) e *= w[c];
-    if (b != nullptr) e += b[c];
-    Ld<T, 1>::put(Y + row * dim + c, &e);
+#pragma unroll 2
+  for (int c = threadIdx.x * V; c < dim; c += 512 * V) {
+    get(c, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = (x[i] - mean) * rstd;
+    if (w != nullptr) {
+      get_f<V>(w + c, ww);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] *= ww[i];
+    }
+    if (b != nullptr) {
+      get_f<V>(b + c, ww);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] += ww[i];
+    }
+    Ld<T, V>::put(Y + row * dim + c, x);
   }
   if (stats != nullptr && threadIdx.x == 0) stats[2 * row] = mean, stats[2 * row + 1] = rstd;
 }
@@ -500,51 +506,70 @@ __global__ void __launch_bounds__(block_of(G), backward_resident(G))
   }
 }
 
-// dX of wide rows: three reads, as the forward kernel.
-template <typename T>
+// dX of wide rows: two reads, the second from the caches.
+template <typename T, int V>
 __global__ void __launch_bounds__(512)
     norm_backward_wide_kernel(const T* X, int64_t ldx, const T* dY, int64_t lddy, int dim,
                               const float* __restrict__ w, const float* __restrict__ stats, T* dX) {
   __shared__ float red[2][16];
   const int64_t row = blockIdx.x;
   const float mean = stats[2 * row], rstd = stats[2 * row + 1];
-  float s1 = 0.f, s2 = 0.f, x, g;
-  for (int c = threadIdx.x; c < dim; c += 512) {
-    Ld<T, 1>::get(X + row * ldx + c, &x);
-    Ld<T, 1>::get(dY + row * lddy + c, &g);
-    if (w != nullptr) g *= w[c];
-    s1 += g;
-    s2 = fmaf(g, (x - mean) * rstd, s2);
+  const auto get = [&](int c, float* xh, float* g) {  // V normalised values, and dy w
+    Raw<T, V> xr, gr;
+    xr.get(X + row * ldx + c);
+    gr.get(dY + row * lddy + c);
+    xr.unpack(xh);
+    gr.unpack(g);
+    float ww[V];
+    if (w != nullptr) get_f<V>(w + c, ww);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      xh[i] = (xh[i] - mean) * rstd;
+      if (w != nullptr) g[i] *= ww[i];
+    }
+  };
+  float s1 = 0.f, s2 = 0.f, x[V], g[V];
+#pragma unroll 2
+  for (int c = threadIdx.x * V; c < dim; c += 512 * V) {
+    get(c, x, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s1 += g[i], s2 = fmaf(g[i], x[i], s2);
   }
   s1 = group_sum<512>(s1, red[0]) / dim;
   s2 = group_sum<512>(s2, red[1]) / dim;
-  for (int c = threadIdx.x; c < dim; c += 512) {
-    Ld<T, 1>::get(X + row * ldx + c, &x);
-    Ld<T, 1>::get(dY + row * lddy + c, &g);
-    if (w != nullptr) g *= w[c];
-    g = rstd * (g - s1 - (x - mean) * rstd * s2);
-    Ld<T, 1>::put(dX + row * dim + c, &g);
+#pragma unroll 2
+  for (int c = threadIdx.x * V; c < dim; c += 512 * V) {
+    get(c, x, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = rstd * (g[i] - s1 - x[i] * s2);
+    Ld<T, V>::put(dX + row * dim + c, g);
   }
 }
 
-// Column sums of wide rows: a thread owns a column, a block a range of rows.
+// Column sums of wide rows: a thread owns V columns, a block a range of rows.
 // Runs before dX is written, which may lie over X or dY.
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(256)
     norm_cols_wide_kernel(const T* X, int64_t ldx, const T* dY, int64_t lddy, int64_t rows,
                           int64_t per, int dim, const float* __restrict__ stats, float* part) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
+  const int c = (blockIdx.x * 256 + threadIdx.x) * V;
   if (c >= dim) return;
   const int64_t r0 = (int64_t)blockIdx.y * per, r1 = r0 + per < rows ? r0 + per : rows;
-  float sw = 0.f, sb = 0.f, x, g;
+  float sw[V] = {}, sb[V] = {}, x[V], g[V];
+#pragma unroll 4
   for (int64_t row = r0; row < r1; ++row) {
-    Ld<T, 1>::get(X + row * ldx + c, &x);
-    Ld<T, 1>::get(dY + row * lddy + c, &g);
-    sw = fmaf(g, (x - stats[2 * row]) * stats[2 * row + 1], sw);
-    sb += g;
+    Raw<T, V> xr, gr;
+    xr.get(X + row * ldx + c);
+    gr.get(dY + row * lddy + c);
+    xr.unpack(x);
+    gr.unpack(g);
+    const float mean = stats[2 * row], rstd = stats[2 * row + 1];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sw[i] = fmaf(g[i], (x[i] - mean) * rstd, sw[i]), sb[i] += g[i];
   }
-  part[(size_t)blockIdx.y * dim + c] = sw;
-  part[((size_t)gridDim.y + blockIdx.y) * dim + c] = sb;
+  float* to = part + (size_t)blockIdx.y * dim + c;
+#pragma unroll
+  for (int i = 0; i < V; ++i) to[i] = sw[i], to[(size_t)gridDim.y * dim + i] = sb[i];
 }
 
 // dw, db = the blocks' sums, added in order: 32 columns a block, 32 rows of
@@ -617,7 +642,21 @@ int blocks_of(const NormArgs& a, const Shape& s, bool forward) {
       148 * (forward ? (s.G == 512 ? 2 : s.G == 128 ? 8 : 4) : backward_resident(s.G));
   return (int)(need < most ? (need < 1 ? 1 : need) : most);
 }
-int wide_blocks(const NormArgs& a) { return (int)(a.rows < 64 ? (a.rows < 1 ? 1 : a.rows) : 64); }
+int wide_blocks(const NormArgs& a) { return (int)(a.rows < 256 ? (a.rows < 1 ? 1 : a.rows) : 256); }
+
+// The wide kernels' type and vector, as go's arguments.
+template <typename F>
+void wide_by_type(const NormArgs& a, int V, const F& go) {
+  using B = __nv_bfloat16;
+  if (a.bf16 && V == 8)
+    go(B(), std::integral_constant<int, 8>());
+  else if (a.bf16)
+    go(B(), std::integral_constant<int, 1>());
+  else if (V == 4)
+    go(0.f, std::integral_constant<int, 4>());
+  else
+    go(0.f, std::integral_constant<int, 1>());
+}
 
 struct Forward {
   const void* X;
@@ -707,14 +746,12 @@ cudaError_t norm_forward(const NormArgs& a, const void* X, int64_t ldx, const fl
   const Shape s = shape_of(a, vector_of(a, ldx, a.dim), true);
   TraceScope ts("layer_norm", st);
   if (s.G == 0) {
-    if (a.bf16)
-      norm_wide_kernel<<<(unsigned)a.rows, 512, 0, st>>>(
-          static_cast<const __nv_bfloat16*>(X), ldx, (int)a.dim, a.eps, w, b,
-          static_cast<__nv_bfloat16*>(Y), stats);
-    else
-      norm_wide_kernel<<<(unsigned)a.rows, 512, 0, st>>>(static_cast<const float*>(X), ldx,
-                                                         (int)a.dim, a.eps, w, b,
-                                                         static_cast<float*>(Y), stats);
+    const auto go = [&](auto t, auto v) {
+      using T = decltype(t);
+      norm_wide_kernel<T, decltype(v)::value><<<(unsigned)a.rows, 512, 0, st>>>(
+          static_cast<const T*>(X), ldx, (int)a.dim, a.eps, w, b, static_cast<T*>(Y), stats);
+    };
+    wide_by_type(a, s.V, go);
     return cudaGetLastError();
   }
   const Forward f = {X, ldx, w, b, Y, stats, blocks_of(a, s, true)};
@@ -743,25 +780,19 @@ cudaError_t norm_backward(const NormArgs& a, const void* X, int64_t ldx, const v
     blocks = wide_blocks(a);
     const int64_t per = (a.rows + blocks - 1) / blocks;
     TraceScope ts("layer_norm_backward", st);
-    const dim3 grid((unsigned)((a.dim + 255) / 256), (unsigned)blocks);
-    if (a.bf16) {
-      using B = __nv_bfloat16;
-      const B *x = static_cast<const B*>(X), *dy = static_cast<const B*>(dY);
+    const auto go = [&](auto t, auto v) {
+      using T = decltype(t);
+      constexpr int V = decltype(v)::value;
+      const T *x = static_cast<const T*>(X), *dy = static_cast<const T*>(dY);
       if (cols)
-        norm_cols_wide_kernel<<<grid, 256, 0, st>>>(x, ldx, dy, lddy, a.rows, per, (int)a.dim,
-                                                    stats, part);
+        norm_cols_wide_kernel<T, V>
+            <<<dim3((unsigned)((a.dim + 256 * V - 1) / (256 * V)), (unsigned)blocks), 256, 0, st>>>(
+                x, ldx, dy, lddy, a.rows, per, (int)a.dim, stats, part);
       if (dX != nullptr)
-        norm_backward_wide_kernel<<<(unsigned)a.rows, 512, 0, st>>>(
-            x, ldx, dy, lddy, (int)a.dim, w, stats, static_cast<B*>(dX));
-    } else {
-      const float *x = static_cast<const float*>(X), *dy = static_cast<const float*>(dY);
-      if (cols)
-        norm_cols_wide_kernel<<<grid, 256, 0, st>>>(x, ldx, dy, lddy, a.rows, per, (int)a.dim,
-                                                    stats, part);
-      if (dX != nullptr)
-        norm_backward_wide_kernel<<<(unsigned)a.rows, 512, 0, st>>>(
-            x, ldx, dy, lddy, (int)a.dim, w, stats, static_cast<float*>(dX));
-    }
+        norm_backward_wide_kernel<T, V><<<(unsigned)a.rows, 512, 0, st>>>(
+            x, ldx, dy, lddy, (int)a.dim, w, stats, static_cast<T*>(dX));
+    };
+    wide_by_type(a, s.V, go);
     e = cudaGetLastError();
   } else {
     blocks = blocks_of(a, s, false);
