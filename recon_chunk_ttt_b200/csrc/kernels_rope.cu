@@ -36,7 +36,7 @@ struct RopeParams {
   int64_t n;
   int pairs;  // rotated pairs (R / 2)
   int per;    // items of a head: what a thread takes at a time
-  // 2^32 / x + 1 of per, heads * per (0 where a block has one token), pairs: for e / x
+  // 2^32 / x + 1 of per, heads * per (0 where a block has one token), pairs (from 2 on): for e / x
   uint32_t per_inv, row_inv, pair_inv;
   float sign;
 };
@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int b = 0; b < BATCH; ++b) load(items[b], threadIdx.x + b * kThreads);
   for (int e = threadIdx.x; e < m * half; e += kThreads) {
-    const int t = (int)__umulhi((uint32_t)e, p.pair_inv), j = e - t * half;
+    // (one pair: its reciprocal does not fit 32 bits)
+    const int t = half == 1 ? e : (int)__umulhi((uint32_t)e, p.pair_inv), j = e - t * half;
     float s, c;
     const uint64_t f = table(&p.turns[j]);
     sincospif(half_turns(p.pos[(t0 + t) * 3 + (f & 3)], f), &s, &c);
@@ -234,13 +235,13 @@ cudaError_t launch(RopeParams& p, bool pairs, cudaStream_t st) {
   p.per = pairs ? D / N : (D - p.pairs) / unit;
   const int64_t row = (int64_t)(p.heads[0] + p.heads[1]) * p.per;
   p.per_inv = (uint32_t)((1ull << 32) / p.per + 1);
-  p.pair_inv = (uint32_t)((1ull << 32) / p.pairs + 1);
+  p.pair_inv = p.pairs == 1 ? 0 : (uint32_t)((1ull << 32) / p.pairs + 1);
   // tokens of a block: four items a thread, but blocks for the whole GPU first
   int64_t tok = 4 * kThreads / row;
   if (tok > p.n / (148 * 4)) tok = p.n / (148 * 4);
   tok = tok < 1 ? 1 : tok > kTok ? kTok : tok;
   // Exact: several tokens have e < 2^12 items.  One token may have up to 2^21: e / row is 0,
-  // and per <= 192 keeps the error of e / per below 1 / per.
+  // and per <= 255 (d = 256, one pair) keeps the error of e / per below 1 / per.
   p.row_inv = tok == 1 ? 0 : (uint32_t)((1ull << 32) / row + 1);
   const unsigned grid = (unsigned)((p.n + tok - 1) / tok);
   TraceScope ts("rope", st);
