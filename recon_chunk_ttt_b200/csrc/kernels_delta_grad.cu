@@ -797,7 +797,10 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
   const uint32_t strip_row = sw32(kn_r, lane / 16);
   const uint32_t tri_row = sw32(m0 + kn_r, lane / 16),
                  tri_col = tri_strip(mb) + sw32(nk_r, lane / 8 % 2);
-  __syncthreads();  // dO, U, dV have been read: strips may lie over them
+  // dO, U, dV have been read: strips may lie over them.  U and dV were this block's own
+  // stores, which the copies have to come behind.
+  fence_proxy_async_smem();
+  __syncthreads();
   int issued = L::RING;
   if (tid == 0)
     for (int s = 2; s < L::RING; ++s) load_strip(s);
