@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(block_of(G), backward_resident(G))
     // in place is in order: dX's rows are this step's, the loads the next one's
     load(next, row + step);
     // Values go in pairs (one instruction for two where there are two).  With d = x - mean,
-    // per row: s1 = sum g w, s2 = sum g w d;  dx = rstd (g w) - rstd^3 s2/n d - rstd s1/n.
+    // per row: s1 = sum g w, s2 = sum g w d;  dx = rstd (g w - (rstd s2/n) (d rstd) - s1/n),
+    // each factor rstd beside one of the row's size: rstd^3 by itself leaves fp32's range.
     float sums[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -452,8 +453,8 @@ __global__ void __launch_bounds__(block_of(G), backward_resident(G))
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float rs = now.rstd[r];
-        const N mean(-now.mean[r]), rstd(rs), k1(-rs * (sums[2 * r] * inv)),
-            k2(-rs * rs * rs * (sums[2 * r + 1] * inv));
+        const N mean(-now.mean[r]), rstd(rs), k1(-(sums[2 * r] * inv)),
+            k2(-rs * (sums[2 * r + 1] * inv));
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (row + r < rows && l + i * G < nv) {
@@ -462,8 +463,8 @@ __global__ void __launch_bounds__(block_of(G), backward_resident(G))
             now.g[r][i].unpack(gs);
 #pragma unroll
             for (int c = 0; c < P; ++c) {
-              const N d = add(pair<V>(xs, c), mean);
-              const N y = fma(mul(pair<V>(gs, c), ww[i][c]), rstd, fma(d, k2, k1));
+              const N xh = mul(add(pair<V>(xs, c), mean), rstd);
+              const N y = mul(fma(pair<V>(gs, c), ww[i][c], fma(xh, k2, k1)), rstd);
               gs[2 * c] = y.x();
               if (V > 1) gs[(2 * c + 1) % V] = y.y();
             }
