@@ -365,6 +365,11 @@ ttt_status ttt_stream_step_static(const ttt_config* cfg,
  *   ([n][heads*d]), token type, dense; dlog_decay, dbeta: float [n][heads];
  *   dS_in: float [seqs][heads][d][d] or NULL; it may be dS_out (in place).
  *   Nothing is kept from the forward call: it is recomputed in the workspace.
+ *   dlog_decay of a token is exp(log_decay) times a product of the states on
+ *   both sides of it, and 0 where nothing of the state is left.  BF16_TC:
+ *   where log_decay >= -6 a running sum over the tokens behind it, whose fp32
+ *   terms' rounding (some 1e-6 of them) it keeps; below -6 formed by itself from
+ *   bf16 copies of the states (2e-3 of the products).
  *
  * Outputs alias no input except where said.  Workspace bytes:
  * ttt_delta_workspace_bytes(cfg, n, seqs, backward); 0 where a call needs none

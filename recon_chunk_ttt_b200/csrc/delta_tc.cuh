@@ -128,6 +128,12 @@ __device__ __forceinline__ uint32_t keep_pair(int t, int valid) {
   return t + 1 < valid ? 0xffffffffu : t < valid ? 0xffffu : 0u;
 }
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(

@@ -9,13 +9,15 @@
 // The decays' gradient needs none of these products: scaling S and its gradient
 // against each other shows that <E_t, S_t>, the gradient of token t+1's decay,
 // changes from token to token by dO_t . O_t - dV_t . V_t alone, so it is a running sum
-// from the end, started anew from a product of the two states every 512 tokens.
+// from the end, started anew from a product of the two states every 512 tokens.  Of a token
+// that fades the state below e^-6 the sum would keep few digits: its gradient is formed from
+// the terms that cross it, and the sum starts anew there too.
 //
 // Three kernels: the inverses of all chunks; delta_chains_kernel, the forward chain once more
-// (which keeps the state before each chunk in bf16, as it only enters dQ and dK, and U and
-// dO . O in fp32) and beside it the chain of E from the last chunk to the first (which keeps
+// (which keeps the state before each chunk in bf16, as it only enters dQ, dK and those terms, and
+// U and dO . O in fp32) and beside it the chain of E from the last chunk to the first (which keeps
 // E likewise, and X and dV . V); delta_tokens_grad_kernel, dQ, dK and dbeta of all chunks at
-// once, and the running sums.  Where heads share a key head a fourth adds their shares.  The
+// once, and the decays' gradients.  Where heads share a key head a fourth adds their shares.  The
 // chains carry fp32 in three bf16 parts (the gates' gradients and dS are fp32 results), the
 // rest is bf16 products summed in fp32.
 //
@@ -475,24 +477,286 @@ __global__ void __launch_bounds__(RK<D, 4, 1, ST>::THREADS, ST == 1 ? 2 : 1)
                                          blockIdx.z);
 }
 
-// ----------------------------------------------------------------------------
-// dlog_decay of 512 tokens of a sequence and head (from one anchor to the next): <E, S>
-// at the stretch's end and the running sum from there.  A few blocks' work, done beside
-// dQ and dK.
-// ----------------------------------------------------------------------------
 constexpr int kGW = 8;  // warps of a block
 constexpr int kStretch = kC * kAnchor;
 
+// ----------------------------------------------------------------------------
+// dlog_decay of the tokens of one chunk and head whose log decay is below kFade.
+// dlog_decay_t = <E_t, S'_t> is e^g_t of what the states on its two sides make together, but
+// the running sum's terms are not that small, and what their rounding leaves has e^g_t's digits
+// less: at e^-6 as many as the states in bf16 have (8 heads of 256: 3e-3, at e^-8 1.5e-2),
+// below that fewer, at last none.  So here it is the sum of all that crosses token t, each
+// term with e^g_t in it:
+//   from a token j of this chunk to a token i:  Z_ij = Gamma_ij (scale (dO_i . U_j)(q_i . k_j)
+//                                                     - (dV_i . U_j)(k_i . k_j)),  j < t <= i
+//   from the state before the chunk to i:  gamma_i (scale dO_i . S q_i - dV_i . S k_i)
+//   from j to the state behind it:         rest_j (U_j . E k_j)
+//   from the one to the other:             gamma_64 <E, S>
+// U and dV go in as two bf16 parts (2^-17), S and E as they are kept (2^-9, rounded once).
+// U, X, S and E lie as registers hold them and come straight from memory; movmatrix turns U's
+// and dV's blocks.  The whole block works on one chunk, 33 us at d = 256 (one frame of 1,374
+// tokens, 4 heads of 256: 137 us without such a token, 156 us with one in every 512, 375 us where
+// one head has no others); a call of its own keeps its registers apart from those of dQ and dK.
+// ----------------------------------------------------------------------------
+constexpr float kFade = -6.f;
+// such a token, but for those that leave nothing: their gradient is 0
+__device__ __forceinline__ bool fades(float g) { return g < kFade && expf(g) != 0.f; }
+
+// What the chains leave and the tokens, of all chunks.
+struct ChunksArgs {
+  int64_t n;
+  const int64_t* offsets;
+  int64_t seqs;
+  int H, Hk;
+  float scale;
+  const __nv_bfloat16 *Q, *K, *dO;
+  int64_t ldq, ldk;
+  const float *g, *b;
+  const __nv_bfloat16 *S0, *E;
+  const float *U, *X;
+  float* dg;
+};
+
+__device__ __forceinline__ uint32_t turned(uint32_t x) {  // an 8 x 8 block's transpose
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// Two values as two bf16 parts, packed.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+struct FadeSmem {
+  float2 G[kC];
+  float beta[kC];
+  float Z[kC][kC + 1];
+  float from_s[kGW][kC], to_e[kGW][kC], s_to_e[kGW];  // by warp
+};
+constexpr int kFadeTiles = 22 * 1024;  // behind it: K, Q, dO as [d / 64][64 tokens][64]
+static_assert(sizeof(FadeSmem) <= kFadeTiles, "shared memory of the decays' gradients");
+
+template <int D>
+__device__ __noinline__ void fade_chunk(const ChunksArgs& a, uint8_t* smem, int64_t slot, int h) {
+  FadeSmem& m = *reinterpret_cast<FadeSmem*>(smem);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, hk = h / (a.H / a.Hk);
+  const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
+  const uint32_t sK = smem_u32(smem + kFadeTiles), sQ = sK + kC * D * 2, sG = sQ + kC * D * 2;
+  for (int e = tid; e < kC * D / 8; e += 32 * kGW) {  // rows behind the sequence count as zero
+    const int t = e / (D / 8), of = e % (D / 8) * 8;
+    const bool ok = t < c.len;
+    const int64_t at = c.t0 + (ok ? t : 0);
+    cp16(sK + sw(kC, t, of), a.K + at * a.ldk + hk * D + of, ok);
+    cp16(sQ + sw(kC, t, of), a.Q + at * a.ldq + hk * D + of, ok);
+    cp16(sG + sw(kC, t, of), a.dO + (at * a.H + h) * D + of, ok);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if (warp < 2) {
+    const float x = tid < c.len ? a.b[(c.t0 + tid) * a.H + h] : 0.f;
+    m.beta[tid] = fabsf(x) <= kNoBeta ? 0.f : x;  // as in the chains
+  } else if (warp == 2) {
+    sum_decays(a.g, c.t0, c.len, a.H, h, lane, m.G);
+  }
+  for (int t = lane; t < kC; t += 32) m.from_s[warp][t] = m.to_e[warp][t] = 0.f;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  const int64_t at = slot * a.H + h;
+  const int row = lane / 4, col = 2 * (lane % 4);
+  const int nk_r = (lane / 16) * 8 + lane % 8, nk_c = (lane / 8 % 2) * 8;
+  const int kn_r = lane % 16, kn_c = (lane / 16) * 8;
+  const float4 *U = reinterpret_cast<const float4*>(a.U) + at * (D / 16) * 256 + lane,
+               *X = reinterpret_cast<const float4*>(a.X) + at * (D / 16) * 256 + lane;
+
+  // steps of 16 of d whose operands are on their way (128 registers a thread, or 256)
+  constexpr int U_AHEAD = D == 256 ? 2 : 1, S_AHEAD = D == 256 ? 4 : 1, UNROLL = D == 256 ? 16 : 2;
+  // Z of 16 tokens i and 16 tokens j <= i: ten such, one or two for a warp
+#pragma unroll 1
+  for (int unit = warp; unit < 10; unit += kGW) {
+    const int mb = unit < 1 ? 0 : unit < 3 ? 1 : unit < 6 ? 2 : 3, m0 = mb * 16,
+              j0 = (unit - mb * (mb + 1) / 2) * 16;
+    float dp[2][4] = {}, dl[2][4] = {}, qk[2][4] = {}, kk[2][4] = {};
+    float2 b[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) b[x] = *reinterpret_cast<const float2*>(m.beta + m0 + x * 8 + col);
+    float4 xs[U_AHEAD][2], us[U_AHEAD][2];
+    const auto fetch = [&](int d0) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        xs[d0 / 16 % U_AHEAD][x] = X[(d0 / 2 + m0 / 8 + x) * 32];
+        us[d0 / 16 % U_AHEAD][x] = U[(d0 / 2 + j0 / 8 + x) * 32];
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < U_AHEAD; ++i) fetch(i * 16);
+#pragma unroll UNROLL
+    for (int d0 = 0; d0 < D; d0 += 16) {
+      uint32_t ag[4], aq[4], ak[4], bk[4], vh[4], vl[4];
+      ldsm4(sG + sw(kC, m0 + kn_r, d0 + kn_c), ag);
+      ldsm4(sQ + sw(kC, m0 + kn_r, d0 + kn_c), aq);
+      ldsm4(sK + sw(kC, m0 + kn_r, d0 + kn_c), ak);
+      ldsm4(sK + sw(kC, j0 + nk_r, d0 + nk_c), bk);
+      const float4 uv[2] = {us[d0 / 16 % U_AHEAD][0], us[d0 / 16 % U_AHEAD][1]};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {  // dV = beta X of 8 tokens: rows d, columns tokens
+        const float4 v = xs[d0 / 16 % U_AHEAD][x];
+        split2(b[x].x * v.x, b[x].y * v.y, vh[x], vl[x]);
+        split2(b[x].x * v.z, b[x].y * v.w, vh[x + 2], vl[x + 2]);
+      }
+      if (d0 + U_AHEAD * 16 < D) fetch(d0 + U_AHEAD * 16);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) vh[x] = turned(vh[x]), vl[x] = turned(vl[x]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 u = uv[j];
+        uint32_t uh[2], ul[2];
+        split2(u.x, u.y, uh[0], ul[0]);
+        split2(u.z, u.w, uh[1], ul[1]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) uh[x] = turned(uh[x]), ul[x] = turned(ul[x]);
+        mma(dp[j], ag, ul[0], ul[1]);
+        mma(dp[j], ag, uh[0], uh[1]);
+        mma(dl[j], vl, uh[0], uh[1]);
+        mma(dl[j], vh, ul[0], ul[1]);
+        mma(dl[j], vh, uh[0], uh[1]);
+        mma(qk[j], aq, bk[2 * j], bk[2 * j + 1]);
+        mma(kk[j], ak, bk[2 * j], bk[2 * j + 1]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int ti = m0 + row + y / 2 * 8, tj = j0 + j * 8 + col + y % 2;
+        m.Z[ti][tj] = tj < ti && ti < c.len ? decay(m.G[ti], m.G[tj]) *
+                                                  (a.scale * dp[j][y] * qk[j][y] - dl[j][y] * kk[j][y])
+                                            : 0.f;
+      }
+  }
+
+  // S q, S k and E k of 16 rows of S and E and 32 tokens: rows of S, columns tokens
+  float both = 0.f;  // <E, S>
+#pragma unroll 1
+  for (int unit = warp; unit < D / 8; unit += kGW) {
+    const int r = unit / 2, t0 = unit % 2 * 32;
+    float sq[4][4] = {}, sk[4][4] = {}, ek[4][4] = {};
+    // blocks [column / 16][row / 8][column / 8 % 2], as operands want them: row, then column
+    const uint32_t *S = reinterpret_cast<const uint32_t*>(a.S0) + at * (D * D / 2) + r * 128 + lane,
+                   *E = reinterpret_cast<const uint32_t*>(a.E) + at * (D * D / 2) + r * 128 + lane;
+    uint32_t ss[S_AHEAD][4], es[S_AHEAD][4];
+    const auto fetch = [&](int i) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int at = i * D * 8 + x % 2 * 64 + x / 2 * 32;
+        ss[i % S_AHEAD][x] = S[at], es[i % S_AHEAD][x] = E[at];
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < S_AHEAD; ++i) fetch(i);
+#pragma unroll UNROLL
+    for (int i = 0; i < D / 16; ++i) {
+      const int d0 = i * 16;
+      uint32_t s[4], e[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[x] = ss[i % S_AHEAD][x], e[x] = es[i % S_AHEAD][x];
+      if (i + S_AHEAD < D / 16) fetch(i + S_AHEAD);
+      if (t0 == 0)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          both = fmaf(low(s[x]), low(e[x]), fmaf(high(s[x]), high(e[x]), both));
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t bq[4], bk[4];
+        ldsm4(sQ + sw(kC, t0 + p * 16 + nk_r, d0 + nk_c), bq);
+        ldsm4(sK + sw(kC, t0 + p * 16 + nk_r, d0 + nk_c), bk);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          mma(sq[2 * p + j], s, bq[2 * j], bq[2 * j + 1]);
+          mma(sk[2 * p + j], s, bk[2 * j], bk[2 * j + 1]);
+          mma(ek[2 * p + j], e, bk[2 * j], bk[2 * j + 1]);
+        }
+      }
+    }
+    float4 us[4], xs[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      us[q] = U[(r * 8 + t0 / 8 + q) * 32], xs[q] = X[(r * 8 + t0 / 8 + q) * 32];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t go[4];  // dO: (rows 0-7, 8-15) of 8 tokens, then of the next
+      ldsm4_t(sG + sw(kC, t0 + p * 16 + nk_r, r * 16 + nk_c), go);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int q = 2 * p + j, t = t0 + q * 8 + col;
+        const float4 u = us[q], x = xs[q];
+        const float2 b = *reinterpret_cast<const float2*>(m.beta + t);
+        const float dv[4] = {b.x * x.x, b.y * x.y, b.x * x.z, b.y * x.w};
+        float f[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t w = go[2 * j + y / 2];
+          f[y] = a.scale * (y % 2 ? high(w) : low(w)) * sq[q][y] - dv[y] * sk[q][y];
+        }
+        const float2 from = rows_sum(make_float2(f[0] + f[2], f[1] + f[3])),
+                     to = rows_sum(make_float2(fmaf(u.x, ek[q][0], u.z * ek[q][2]),
+                                               fmaf(u.y, ek[q][1], u.w * ek[q][3])));
+        if (lane < 4) {
+          m.from_s[warp][t] += from.x, m.from_s[warp][t + 1] += from.y;
+          m.to_e[warp][t] += to.x, m.to_e[warp][t + 1] += to.y;
+        }
+      }
+    }
+  }
+  for (int x = 16; x > 0; x /= 2) both += __shfl_xor_sync(0xffffffffu, both, x);
+  if (lane == 0) m.s_to_e[warp] = both;
+  __syncthreads();
+  // the warps' sums in order, each with its decay; Z across each token, four threads a token
+  if (tid < kC) {
+    float f = 0.f, g = 0.f;
+    for (int w = 0; w < kGW; ++w) f += m.from_s[w][tid], g += m.to_e[w][tid];
+    m.from_s[0][tid] = decay(m.G[tid]) * f;
+    m.to_e[0][tid] = decay(m.G[kC - 1], m.G[tid]) * g;
+  }
+  const int t = tid / 4;
+  float x = 0.f;
+  for (int i = t + tid % 4; i < kC; i += 4) {
+    float y = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < t; ++j) y += m.Z[i][j];
+    x += y;
+  }
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  x += __shfl_xor_sync(0xffffffffu, x, 2);
+  __syncthreads();
+  if (tid % 4 == 0 && t < c.len && fades(a.g[(c.t0 + t) * a.H + h])) {
+    float y = 0.f;
+    for (int w = 0; w < kGW; ++w) y += m.s_to_e[w];
+    x += y * decay(m.G[kC - 1]);
+    for (int i = 0; i < kC; ++i) x += i < t ? m.to_e[0][i] : m.from_s[0][i];
+    a.dg[(c.t0 + t) * a.H + h] = x;
+  }
+}
+
+// ----------------------------------------------------------------------------
+// dlog_decay of 512 tokens of a sequence and head (from one anchor to the next): <E, S>
+// at the stretch's end and the running sum from there, which starts anew with every token below
+// kFade.  A few blocks' work, done beside dQ and dK.
+// ----------------------------------------------------------------------------
 struct GateArgs {
   int groups;
   const float *dots_o, *dots_v;
   const float *S, *E;            // anchors
   const float *S_last, *E_last;  // behind the last tokens, or both nullptr: zeros
-  float* dg;
 };
 
-__device__ __forceinline__ void gate_stretch(const GateArgs& a, const int64_t* offsets, int64_t n,
-                                             int64_t seqs, int H, int64_t slot, int h, int tid) {
+template <int D>
+__device__ __forceinline__ void gate_stretch(const GateArgs& a, const ChunksArgs& c, uint8_t* smem,
+                                             int64_t slot, int h, int tid) {
+  const int64_t* offsets = c.offsets;
+  const int64_t n = c.n, seqs = c.seqs;
+  const int H = c.H;
   // the sequence of this stretch
   int64_t lo = 0, hi = seqs;
   while (hi - lo > 1) {
@@ -502,13 +766,13 @@ __device__ __forceinline__ void gate_stretch(const GateArgs& a, const int64_t* o
     else
       hi = mid;
   }
-  const SeqRange s = seq_range(offsets, n, lo);
-  const int64_t b0 = s.t0 + (slot - (s.t0 / kStretch + lo)) * kStretch;
-  if (b0 < s.t0 || b0 >= s.t1) return;
-  const int64_t b1 = b0 + kStretch < s.t1 ? b0 + kStretch : s.t1;
+  const SeqRange sr = seq_range(offsets, n, lo);
+  const int64_t b0 = sr.t0 + (slot - (sr.t0 / kStretch + lo)) * kStretch;
+  if (b0 < sr.t0 || b0 >= sr.t1) return;
+  const int64_t b1 = b0 + kStretch < sr.t1 ? b0 + kStretch : sr.t1;
   // <E, S> at the end, the next anchor's or the last states': this thread's share
   const int64_t size = (int64_t)a.groups * a.groups * 256;
-  const bool next = b1 < s.t1;
+  const bool next = b1 < sr.t1;
   const float* es = next ? a.E + ((slot + 1) * H + h) * size
                          : a.E_last != nullptr ? a.E_last + (lo * H + h) * size : nullptr;
   const float* ss = next ? a.S + ((slot + 1) * H + h) * size : a.S_last + (lo * H + h) * size;
@@ -520,44 +784,65 @@ __device__ __forceinline__ void gate_stretch(const GateArgs& a, const int64_t* o
       const float4 y = *reinterpret_cast<const float4*>(ss + i);
       x = fmaf(e.x, y.x, fmaf(e.y, y.y, fmaf(e.z, y.z, fmaf(e.w, y.w, x))));
     }
+  const auto decay_of = [&](int64_t t) { return t < b1 ? c.g[t * H + h] : 0.f; };
+  if (__syncthreads_or(fades(decay_of(b0 + tid)) || fades(decay_of(b0 + tid + 32 * kGW))))
+    for (int64_t t = b0; t < b1; t += kC) {
+      if (!__syncthreads_or(tid < kC && fades(decay_of(t + tid)))) continue;
+      fade_chunk<D>(c, smem, sr.slot + (t - sr.t0) / kC, h);
+      __syncthreads();  // its results are there, its arrays are free
+    }
+  // x of a token: its own value where it has been formed, else v + x of the next.  Over several
+  // tokens: s, and whether it ends there (`own`) or x of the token behind them is to be added.
   constexpr int PER = kStretch / (32 * kGW);
-  float v[PER], sum = 0.f;
+  float v[PER], s = 0.f;
+  bool done[PER], own = false;
 #pragma unroll
-  for (int q = 0; q < PER; ++q) {
+  for (int q = PER - 1; q >= 0; --q) {
     const int64_t t = b0 + tid * PER + q;
-    float o = 0.f, w = 0.f;
-    if (t < b1) {
+    const float g = decay_of(t);
+    done[q] = g < kFade;
+    v[q] = 0.f;
+    if (done[q]) {
+      if (fades(g)) v[q] = c.dg[t * H + h];
+    } else if (t < b1) {
+      float o = 0.f, w = 0.f;
 #pragma unroll 4
       for (int r = 0; r < a.groups; ++r) {
         const int64_t at = (r * (int64_t)H + h) * n + t;
         o += a.dots_o[at];
         w += a.dots_v[at];
       }
+      v[q] = o - w;
     }
-    v[q] = o - w;
-    sum += v[q];
+    s = done[q] ? v[q] : s + v[q];
+    own |= done[q];
   }
-  // sums of the threads behind this one
-  __shared__ float warp_sum[kGW], warp_x[kGW];
+  __shared__ float warp_s[kGW], warp_x[kGW];
+  __shared__ bool warp_own[kGW];
   const int lane = tid % 32, warp = tid / 32;
-  float behind = sum;
   for (int m = 1; m < 32; m *= 2) {
-    const float y = __shfl_down_sync(0xffffffffu, behind, m);
-    if (lane + m < 32) behind += y;
+    const float y = __shfl_down_sync(0xffffffffu, s, m);
+    const bool z = __shfl_down_sync(0xffffffffu, own, m);
+    if (lane + m < 32) {
+      s = own ? s : s + y;
+      own |= z;
+    }
   }
   for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
-  if (lane == 0) warp_sum[warp] = behind, warp_x[warp] = x;
+  if (lane == 0) warp_s[warp] = s, warp_own[warp] = own, warp_x[warp] = x;
   __syncthreads();
-  behind -= sum;
   x = 0.f;
   for (int w = 0; w < kGW; ++w) x += warp_x[w];
-  for (int w = warp + 1; w < kGW; ++w) behind += warp_sum[w];
-  x += behind;
+  for (int w = kGW - 1; w > warp; --w) x = warp_own[w] ? warp_s[w] : warp_s[w] + x;
+  // the threads behind this one in its warp
+  s = __shfl_down_sync(0xffffffffu, s, 1);
+  own = __shfl_down_sync(0xffffffffu, own, 1);
+  if (lane < 31) x = own ? s : s + x;
 #pragma unroll
   for (int q = PER - 1; q >= 0; --q) {
     const int64_t t = b0 + tid * PER + q;
-    x += v[q];
-    if (t < b1) a.dg[t * H + h] = x;
+    x = done[q] ? v[q] : v[q] + x;
+    if (t < b1) c.dg[t * H + h] = x;
   }
 }
 
@@ -594,17 +879,10 @@ struct GK {
     return smem + OFF_S + (s % RING + RING - 2) % RING * STRIP;
   }
   static_assert(SMEM <= (D == 256 ? 227 : 113) * 1024, "shared memory");
+  static_assert(kFadeTiles + 3 * kC * D * 2 + 1024 <= SMEM, "shared memory of the decays' gradients");
 };
 
-struct TokensGradArgs {
-  int64_t n;
-  const int64_t* offsets;
-  int64_t seqs;
-  int H, Hk;
-  float scale;
-  const float *g, *b;
-  const __nv_bfloat16 *S0, *E;
-  const float *U, *X;
+struct TokensGradArgs : ChunksArgs {
   float* db;
   __nv_bfloat16 *dQ, *dK;  // heads of their own
   float *pq, *pk;          // shared heads: each head's share, [n][H * d]
@@ -617,7 +895,8 @@ template <int D>
 __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
     delta_tokens_grad_kernel(const __grid_constant__ CUtensorMap mQ,
                              const __grid_constant__ CUtensorMap mK,
-                             const __grid_constant__ CUtensorMap mG, const TokensGradArgs a) {
+                             const __grid_constant__ CUtensorMap mG,
+                             const __grid_constant__ TokensGradArgs a) {
   using L = GK<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -631,7 +910,7 @@ __global__ void __launch_bounds__(32 * kGW, D == 256 ? 1 : 2)
   const int64_t slot = (int64_t)blockIdx.x - a.stretches;
   const int h = blockIdx.y, hk = h / (a.H / a.Hk);
   if (slot < 0) {
-    gate_stretch(a.gates, a.offsets, a.n, a.seqs, a.H, blockIdx.x, h, tid);
+    gate_stretch<D>(a.gates, a, smem, blockIdx.x, h, tid);
     return;
   }
   const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
@@ -998,12 +1277,16 @@ cudaError_t launch_tokens(const DeltaArgs& a, const Call& x, char* w, const Plan
   const cudaError_t e = ensure_smem_attr(delta_tokens_grad_kernel<D>, L::SMEM);
   if (e != cudaSuccess) return e;
   const bool own = a.H == a.Hk;
-  const TokensGradArgs k = {a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale, a.g, a.b,
-                            reinterpret_cast<const __nv_bfloat16*>(w + p.S0),
-                            reinterpret_cast<const __nv_bfloat16*>(w + p.E),
-                            reinterpret_cast<const float*>(w + p.U),
-                            reinterpret_cast<const float*>(w + p.X), x.db,
-                            static_cast<__nv_bfloat16*>(x.dQ), static_cast<__nv_bfloat16*>(x.dK),
+  const ChunksArgs chunks = {a.n, a.offsets, a.seqs, a.H, a.Hk, a.scale,
+                             static_cast<const __nv_bfloat16*>(a.Q),
+                             static_cast<const __nv_bfloat16*>(a.K),
+                             static_cast<const __nv_bfloat16*>(x.dO), a.ldq, a.ldk, a.g, a.b,
+                             reinterpret_cast<const __nv_bfloat16*>(w + p.S0),
+                             reinterpret_cast<const __nv_bfloat16*>(w + p.E),
+                             reinterpret_cast<const float*>(w + p.U),
+                             reinterpret_cast<const float*>(w + p.X), x.dg};
+  const TokensGradArgs k = {chunks, x.db, static_cast<__nv_bfloat16*>(x.dQ),
+                            static_cast<__nv_bfloat16*>(x.dK),
                             own ? nullptr : reinterpret_cast<float*>(w + p.pq),
                             own ? nullptr : reinterpret_cast<float*>(w + p.pk), stretches(a), gates,
                             device_error_ptr()};
@@ -1049,7 +1332,7 @@ cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, co
                    : launch_chains<256, 2>(a, x, f, r, st);
   if (e != cudaSuccess || a.n == 0) return e;
   const GateArgs gates = {a.d / 16, floats(p.dots_o), floats(p.dots_v), floats(p.anchors),
-                          floats(p.anchors_e), last, last_e, dg};
+                          floats(p.anchors_e), last, last_e};
   e = a.d == 64    ? launch_tokens<64>(a, x, w, p, gates, st)
       : a.d == 128 ? launch_tokens<128>(a, x, w, p, gates, st)
                    : launch_tokens<256>(a, x, w, p, gates, st);

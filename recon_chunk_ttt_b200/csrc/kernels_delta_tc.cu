@@ -59,12 +59,6 @@ __device__ __forceinline__ void rank_sequences(const ChunkArgs& a, int64_t* len,
   }
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
-}
-
 template <int D, bool GRAD>
 // (five blocks an SM, for d = 256 the three that its tiles allow: 95 us against 100 us for four)
 __global__ void __launch_bounds__(kChunkThreads, D == 256 ? 0 : 5)
