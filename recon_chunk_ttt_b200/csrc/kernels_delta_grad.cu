@@ -23,7 +23,7 @@
 //
 // Bound as the forward pass is by the chain (one frame of 1,374 tokens, 4 heads of 256: 95 us
 // of 137), and where there are enough chains to fill the GPU by how many of them an SM holds
-// (16,411 tokens in 13 sequences, 16 heads of 128: 1.07 ms of 1.57; two a SM, the tensor
+// (16,384 tokens in 7 sequences, 16 heads of 128: 1.07 ms of 1.57; two a SM, the tensor
 // cores busy for 39% of the time).
 
 #include "delta_state.cuh"
@@ -494,9 +494,10 @@ constexpr int kStretch = kC * kAnchor;
 //   from the one to the other:             gamma_64 <E, S>
 // U and dV go in as two bf16 parts (2^-17), S and E as they are kept (2^-9, rounded once).
 // U, X, S and E lie as registers hold them and come straight from memory; movmatrix turns U's
-// and dV's blocks.  The whole block works on one chunk, 33 us at d = 256 (one frame of 1,374
-// tokens, 4 heads of 256: 137 us without such a token, 156 us with one in every 512, 375 us where
-// one head has no others); a call of its own keeps its registers apart from those of dQ and dK.
+// and dV's blocks.  The whole block works on one chunk, some 30 us at d = 256, and forms only what
+// a token lies between (one frame of 1,374 tokens, 4 heads of 256: 137 us without such a token,
+// 149 us with one in every 512 of every head, 360 us where one head has no others); a call of its
+// own keeps its registers apart from those of dQ and dK.
 // ----------------------------------------------------------------------------
 constexpr float kFade = -6.f;
 // such a token, but for those that leave nothing: their gradient is 0
@@ -533,6 +534,7 @@ __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0
 struct FadeSmem {
   float2 G[kC];
   float beta[kC];
+  uint32_t tokens[2];  // those to do, a bit each
   float Z[kC][kC + 1];
   float from_s[kGW][kC], to_e[kGW][kC], s_to_e[kGW];  // by warp
 };
@@ -555,14 +557,19 @@ __device__ __noinline__ void fade_chunk(const ChunksArgs& a, uint8_t* smem, int6
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
   if (warp < 2) {
-    const float x = tid < c.len ? a.b[(c.t0 + tid) * a.H + h] : 0.f;
+    const bool in = tid < c.len;
+    const float x = in ? a.b[(c.t0 + tid) * a.H + h] : 0.f;
     m.beta[tid] = fabsf(x) <= kNoBeta ? 0.f : x;  // as in the chains
+    const uint32_t bits = __ballot_sync(0xffffffffu, in && fades(a.g[(c.t0 + tid) * a.H + h]));
+    if (lane == 0) m.tokens[warp] = bits;
   } else if (warp == 2) {
     sum_decays(a.g, c.t0, c.len, a.H, h, lane, m.G);
   }
   for (int t = lane; t < kC; t += 32) m.from_s[warp][t] = m.to_e[warp][t] = 0.f;
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
+  const uint64_t tokens = (uint64_t)m.tokens[1] << 32 | m.tokens[0];
+  const int first = __ffsll((int64_t)tokens) - 1, last = 63 - __clzll((int64_t)tokens);
   const int64_t at = slot * a.H + h;
   const int row = lane / 4, col = 2 * (lane % 4);
   const int nk_r = (lane / 16) * 8 + lane % 8, nk_c = (lane / 8 % 2) * 8;
@@ -572,11 +579,18 @@ __device__ __noinline__ void fade_chunk(const ChunksArgs& a, uint8_t* smem, int6
 
   // steps of 16 of d whose operands are on their way (128 registers a thread, or 256)
   constexpr int U_AHEAD = D == 256 ? 2 : 1, S_AHEAD = D == 256 ? 4 : 1, UNROLL = D == 256 ? 16 : 2;
-  // Z of 16 tokens i and 16 tokens j <= i: ten such, one or two for a warp
+  // Z of 16 tokens i and 16 tokens j <= i, ten such; those that a token lies between, shared out
+  int turn = 0;
 #pragma unroll 1
-  for (int unit = warp; unit < 10; unit += kGW) {
+  for (int unit = 0; unit < 10; ++unit) {
     const int mb = unit < 1 ? 0 : unit < 3 ? 1 : unit < 6 ? 2 : 3, m0 = mb * 16,
               j0 = (unit - mb * (mb + 1) / 2) * 16;
+    const uint64_t between = tokens >> j0 & (2ull << (m0 + 15 - j0)) - 1;  // j0 .. m0 + 15
+    if (between == 0 || turn++ % kGW != warp) {
+      if (between == 0 && warp == 0)  // it adds nothing to the sums below
+        for (int e = lane; e < 256; e += 32) m.Z[m0 + e / 16][j0 + e % 16] = 0.f;
+      continue;
+    }
     float dp[2][4] = {}, dl[2][4] = {}, qk[2][4] = {}, kk[2][4] = {};
     float2 b[2];
 #pragma unroll
@@ -641,6 +655,8 @@ __device__ __noinline__ void fade_chunk(const ChunksArgs& a, uint8_t* smem, int6
 #pragma unroll 1
   for (int unit = warp; unit < D / 8; unit += kGW) {
     const int r = unit / 2, t0 = unit % 2 * 32;
+    // what goes to tokens from the first on, and from those before the last
+    const bool with_s = t0 + 32 > first, with_e = t0 < last;
     float sq[4][4] = {}, sk[4][4] = {}, ek[4][4] = {};
     // blocks [column / 16][row / 8][column / 8 % 2], as operands want them: row, then column
     const uint32_t *S = reinterpret_cast<const uint32_t*>(a.S0) + at * (D * D / 2) + r * 128 + lane,
@@ -669,14 +685,18 @@ __device__ __noinline__ void fade_chunk(const ChunksArgs& a, uint8_t* smem, int6
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         uint32_t bq[4], bk[4];
-        ldsm4(sQ + sw(kC, t0 + p * 16 + nk_r, d0 + nk_c), bq);
         ldsm4(sK + sw(kC, t0 + p * 16 + nk_r, d0 + nk_c), bk);
+        if (with_s) {
+          ldsm4(sQ + sw(kC, t0 + p * 16 + nk_r, d0 + nk_c), bq);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mma(sq[2 * p + j], s, bq[2 * j], bq[2 * j + 1]);
-          mma(sk[2 * p + j], s, bk[2 * j], bk[2 * j + 1]);
-          mma(ek[2 * p + j], e, bk[2 * j], bk[2 * j + 1]);
+          for (int j = 0; j < 2; ++j) {
+            mma(sq[2 * p + j], s, bq[2 * j], bq[2 * j + 1]);
+            mma(sk[2 * p + j], s, bk[2 * j], bk[2 * j + 1]);
+          }
         }
+        if (with_e)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) mma(ek[2 * p + j], e, bk[2 * j], bk[2 * j + 1]);
       }
     }
     float4 us[4], xs[4];
@@ -712,30 +732,30 @@ __device__ __noinline__ void fade_chunk(const ChunksArgs& a, uint8_t* smem, int6
   for (int x = 16; x > 0; x /= 2) both += __shfl_xor_sync(0xffffffffu, both, x);
   if (lane == 0) m.s_to_e[warp] = both;
   __syncthreads();
-  // the warps' sums in order, each with its decay; Z across each token, four threads a token
+  // the warps' sums in order, each with its decay; rows of Z to sums of what is before a column
   if (tid < kC) {
     float f = 0.f, g = 0.f;
     for (int w = 0; w < kGW; ++w) f += m.from_s[w][tid], g += m.to_e[w][tid];
     m.from_s[0][tid] = decay(m.G[tid]) * f;
     m.to_e[0][tid] = decay(m.G[kC - 1], m.G[tid]) * g;
-  }
-  const int t = tid / 4;
-  float x = 0.f;
-  for (int i = t + tid % 4; i < kC; i += 4) {
-    float y = 0.f;
+  } else if (tid < 2 * kC) {
+    const int i = tid - kC;
+    float x = 0.f;
 #pragma unroll 4
-    for (int j = 0; j < t; ++j) y += m.Z[i][j];
-    x += y;
+    for (int j = 0; j <= i; ++j) {
+      const float z = m.Z[i][j];
+      m.Z[i][j] = x;
+      x += z;
+    }
   }
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  x += __shfl_xor_sync(0xffffffffu, x, 2);
   __syncthreads();
-  if (tid % 4 == 0 && t < c.len && fades(a.g[(c.t0 + t) * a.H + h])) {
-    float y = 0.f;
-    for (int w = 0; w < kGW; ++w) y += m.s_to_e[w];
-    x += y * decay(m.G[kC - 1]);
-    for (int i = 0; i < kC; ++i) x += i < t ? m.to_e[0][i] : m.from_s[0][i];
-    a.dg[(c.t0 + t) * a.H + h] = x;
+  if (tid < kC && (tokens >> tid & 1) != 0) {  // what crosses each token
+    float x = 0.f;
+    for (int w = 0; w < kGW; ++w) x += m.s_to_e[w];
+    x *= decay(m.G[kC - 1]);
+#pragma unroll 4
+    for (int i = 0; i < kC; ++i) x += i < tid ? m.to_e[0][i] : m.from_s[0][i] + m.Z[i][tid];
+    a.dg[(c.t0 + tid) * a.H + h] = x;
   }
 }
 
@@ -1324,7 +1344,7 @@ cudaError_t delta_grad(const DeltaArgs& a, const float* S_in, const void* dO, co
                          floats(p.dots_v), device_error_ptr()};
   // Two stages of copies and all registers, or two blocks an SM: the first where every chain
   // has an SM (1,374 tokens, 4 heads of 128: 70 us against 84), the second from there on (16
-  // heads: 111 us against 131; 16,411 tokens in 13 sequences: 1,061 against 1,284).  A block
+  // heads: 111 us against 131; 16,384 tokens in 7 sequences: 1,061 against 1,284).  A block
   // of d = 256 fills an SM.
   const bool few = 2 * a.seqs * a.H * (a.d / 16) <= num_sms();
   e = a.d == 64    ? few ? launch_chains<64, 2>(a, x, f, r, st) : launch_chains<64, 1>(a, x, f, r, st)
