@@ -546,6 +546,7 @@ __device__ __noinline__ void fade_chunk(const ChunksArgs& a, uint8_t* smem, int6
   FadeSmem& m = *reinterpret_cast<FadeSmem*>(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, hk = h / (a.H / a.Hk);
   const ChunkRange c = chunk_range(a.offsets, a.n, a.seqs, slot);
+  if (c.len == 0) return;  // offsets that are no offsets
   const uint32_t sK = smem_u32(smem + kFadeTiles), sQ = sK + kC * D * 2, sG = sQ + kC * D * 2;
   for (int e = tid; e < kC * D / 8; e += 32 * kGW) {  // rows behind the sequence count as zero
     const int t = e / (D / 8), of = e % (D / 8) * 8;

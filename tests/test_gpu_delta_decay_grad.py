@@ -176,3 +176,21 @@ def test_rows_around_stay(first):
         again, size = _products(part, zero, dO[used][a:b], zero, H, 2, d)
         assert (again - ref[a:b]).norm() <= 1e-12 * ref[a:b].norm()
         _fades(dg[used][a:b], ref[a:b], size, a)
+
+
+def test_bad_offsets_with_tokens_that_forget():
+    """Offsets that decrease or leave 0..n: reported, nothing outside the arrays, and the next call unharmed."""
+    H, d, n = 2, 64, 200
+    x, S, dO, dSo = _inputs(3, n, H, H, d, BF, 3)
+    x["log_decay"][::5] = -12.0
+    cfg = R.make_delta_config(H, d)
+    good = torch.tensor([0, 10, 90, 200], device="cuda")
+    want = R.ttt_delta_backward(cfg, **x, dO=dO, S=S, offsets=good, dS_out=dSo)
+    for offs in ([0, 160, 40, 200], [-70, 10, 20, 130], [0, 10, 70, 264], [200, 130, 70, 0]):
+        R.ttt_delta_backward(cfg, **x, dO=dO, S=S, offsets=torch.tensor(offs, device="cuda"), dS_out=dSo)
+        with pytest.raises(R.TTTError):
+            R.ttt_check_device_error()
+    again = R.ttt_delta_backward(cfg, **x, dO=dO, S=S, offsets=good, dS_out=dSo)
+    R.ttt_check_device_error()
+    for a, b in zip(again, want):
+        assert torch.equal(a, b)
