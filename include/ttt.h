@@ -348,9 +348,12 @@ ttt_status ttt_stream_step_static(const ttt_config* cfg,
  *   tokens, or NULL; it may be S_in (in place).  An empty sequence hands its
  *   state on.  O: [n][heads*d] dense, token type.
  *   BF16_TC: chunks of 64 tokens on the tensor cores, the state and every sum
- *   in fp32 (operands that are not bf16 by nature go in as three bf16 parts,
- *   24 bits); short sequences, and FP32_CHECK: token by token in fp32 on CUDA
- *   cores.
+ *   in fp32.  For the states, operands that are not bf16 by nature go in as
+ *   three bf16 parts, 24 bits.  For O, which is bf16 in the end, the state and
+ *   the tokens' corrections u go in as two parts and the tokens' weights of
+ *   each other as one: O is off by up to 2.4e-3 of itself (root mean square;
+ *   its own rounding is 1.6e-3).  Short sequences, and FP32_CHECK (a check
+ *   mode): token by token in fp32 on CUDA cores.
  * ttt_delta_step: one token for each of tok->n requests (tok->seqs = n,
  *   tok->offsets = NULL) on a pool of `pool` states float
  *   [pool][heads][d][d]: request i works on S[slots[i]] (slots: device int32
@@ -369,7 +372,11 @@ ttt_status ttt_stream_step_static(const ttt_config* cfg,
  *   both sides of it, and 0 where nothing of the state is left.  BF16_TC:
  *   where log_decay >= -6 a running sum over the tokens behind it, whose fp32
  *   terms' rounding (some 1e-6 of them) it keeps; below -6 formed by itself from
- *   bf16 copies of the states (2e-3 of the products).
+ *   bf16 copies of the states (2e-3 of the products).  dbeta, dS_in and what
+ *   dV is rounded from come as the states do, in 24 bits.  dQ and dK come from
+ *   bf16 copies of the states before and their gradients behind each chunk, of dV
+ *   and of one of the two weights of the tokens, two parts of the other and of u:
+ *   off by 1.7e-3 to 2.4e-3 of themselves (1.6e-3 their own rounding).
  *
  * Outputs alias no input except where said.  Workspace bytes:
  * ttt_delta_workspace_bytes(cfg, n, seqs, backward); 0 where a call needs none
@@ -424,8 +431,8 @@ ttt_status ttt_delta_backward(const ttt_delta_config* cfg, const ttt_delta_token
  *   TTT_ROPE_FREQ_HEAD: e = j / (R/2), over the whole head
  *   (x, y) -> (x cos - y sin, y cos + x sin); inverse != 0 turns back, which
  * is also the gradient: it maps dQ_out, dK_out to dQ, dK.
- * Angles are formed and reduced exactly to 2^-32 of a turn, the rotation is
- * fp32, rounded once.
+ * Angles are reduced to whole turns in fixed point, off by 2^-32 + |position|
+ * 2^-62 of a turn at most; the rotation is fp32, rounded once.
  *  - d = 64, 128 or 256; rot[] even, >= 0, sum 2..d; base[] finite, >= 1.  With
  *    FREQ_HEAD every pair still uses its own axis' base.
  *  - positions: float [n][3] (whole numbers are exact to 2^24); fractions and

@@ -9,7 +9,8 @@
 // its columns' sums of dy and dy xh in registers over all rows of its block;
 // the blocks' sums meet in the workspace and a second kernel adds them in
 // their order (no atomics).  Of the measured copy rate, bf16 rows of 1,024:
-// forward 79%, backward 76% (137,400 rows, 172 us); of 4,096 86% and 81%; fp32 75 to 100%.
+// forward 79%, backward 73% (137,400 rows, 180 us with both kernels); of 4,096 86% and 81%;
+// fp32 75 to 100%.
 // Rows that are not whole 16-byte vectors go in pairs or one by one: 40 to 62% in bf16, 75 to
 // 90% in fp32.  Rows beyond the registers (8,000 of 16,384, backward): 44% in
 // bf16, 54% in fp32.

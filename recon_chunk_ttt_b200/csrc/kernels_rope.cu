@@ -6,9 +6,9 @@
 // tokens once, in shared memory, and all heads of q and k use them; a thread's
 // first loads are on their way meanwhile.  Angles are taken in turns (position
 // * frequency / 2 pi) in fixed point: a position is a 24-bit integer times a
-// power of two, a frequency 64 bits of a turn; of their product the whole turns
-// fall off and the next 32 bits stay, however far the position (error below
-// 2^-32 turns = 1.5e-9).  The angle goes through sincospi in fp32.  (137,400 tokens of
+// power of two, a frequency 62 bits of a turn; of their product the whole turns
+// fall off and the next 32 bits stay (off by 2^-32 + |position| 2^-62 turns at
+// most: 1.5e-9 turns up to positions of 2^28).  The angle goes through sincospi in fp32.  (137,400 tokens of
 // 10 heads of 128 in bf16, 0.70 GB: 144 us, 76% of the measured copy rate.)
 
 #include <cuda_bf16.h>
